@@ -23,8 +23,25 @@ ERR_WORKSPACE = -4
 ERR_HIP = -5
 ERR_UNSUPPORTED = -6
 
+
+
+class Heads(ctypes.Structure):
+    """adaln_heads_t"""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    """adaln_rotation_t"""
+    _fields_ = [("pos", ctypes.c_void_p), ("pos_batch_stride", ctypes.c_int64),
+                ("freqs", ctypes.c_void_p), ("axes", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
 # Every function the header declares, with its ctypes signature.
 _VP, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_HP, _RP, _F = ctypes.POINTER(Heads), ctypes.POINTER(Rotation), ctypes.c_float
 SIGNATURES = {
     "adaln_fwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT,
                          _VP]),
@@ -51,6 +68,18 @@ SIGNATURES = {
     "adaln_bwd_segments": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                   _SZ, _VP, _VP, _I64, _I64, _I64, _INT,
                                   _VP]),
+    "adaln_rope_fwd": (_INT, [_HP, _HP, _RP, _HP, _HP, _I64, _I64, _I64, _I64,
+                              _I64, _INT, _VP]),
+    "adaln_rope_bwd": (_INT, [_HP, _HP, _RP, _HP, _HP, _I64, _I64, _I64, _I64,
+                              _I64, _INT, _VP]),
+    "adaln_qk_norm_rope_fwd": (_INT, [_HP, _HP, _VP, _VP, _F, _RP, _HP, _HP,
+                                      _I64, _I64, _I64, _I64, _I64, _INT,
+                                      _VP]),
+    "adaln_qk_norm_rope_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64,
+                                                     _I64, _INT]),
+    "adaln_qk_norm_rope_bwd": (_INT, [_HP, _HP, _HP, _HP, _VP, _VP, _F, _RP,
+                                      _HP, _HP, _VP, _VP, _VP, _SZ, _I64,
+                                      _I64, _I64, _I64, _I64, _INT, _VP]),
     "adaln_bshape": (_I64, [_I64, _I64, _I64, ctypes.c_int32]),
     "adaln_bshape_real": (_I64, [_I64, _I64, ctypes.c_double,
                                  ctypes.c_double]),

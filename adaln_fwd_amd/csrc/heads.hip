@@ -1,0 +1,730 @@
+// Rotary positions with several axes, alone and behind the RMS norm of each
+// query and key head, forward and backward, with their C entry points.
+//
+//     angle[n, j] = sum_a pos[n, a] * freqs[a, j]          j < R / 2
+//     (u, v)     -> (u cos - v sin, u sin + v cos)         for pair j
+//     y = rot(x * r * w),  r = 1 / sqrt(mean_d x^2 + eps)
+//     t = rot^-1(dy), g = t * w, xh = x * r
+//     dx = r * (g - xh * mean_d(g * xh)),  dw = sum_{n, h} t * xh
+//
+// Every pass reads each head once and writes it once, so HBM bounds all of
+// them; the arithmetic that could get in the way is the sines, one pair per
+// (token, j), which all heads of a token share.  A workgroup therefore takes
+// a block of tokens with all their heads, computes the block's sines once
+// into LDS (64 pairs per token at d = 128, against 64 per head), and streams
+// the heads past them.  L lanes share a head, each with two 16-byte vectors:
+// in the half layout the two ends of its own pairs, so no value crosses
+// lanes but the sums of the norm.
+#include <algorithm>
+#include <math.h>
+
+#include "adaln.h"
+#include "common.hpp"
+#include "launch.hpp"
+
+#define ADALN_API extern "C" __attribute__((visibility("default")))
+
+#define ADALN_TRY(expr)          \
+  do {                           \
+    const int rc_ = (expr);      \
+    if (rc_ != ADALN_OK) return rc_; \
+  } while (0)
+
+namespace adaln {
+namespace {
+
+constexpr int kMaxFreqs = 384;  // entries of the [axes, pairs] table
+constexpr int kMaxAxes = 4;
+constexpr int kMaxHead = 512;   // features per head
+constexpr int kMaxTokens = 16;  // tokens per block
+
+// Frequencies in turns per unit position, as 64-bit fractions of a turn:
+// pos * turns, wrapping modulo 2^64, is the phase modulo one turn with no
+// loss for any position.  (Held as a kernel argument: 3 KiB.)
+struct Rotation {
+  uint64_t turns[kMaxFreqs];
+  int32_t axes;
+  int32_t pairs;
+};
+
+// One tensor's heads: strides in 16-byte vectors.
+struct Heads {
+  const char *data;
+  int64_t batch;
+  int64_t token;
+  int32_t head;
+};
+
+struct Job {
+  Heads in[2];            // x (rope: the tensor to rotate), of q and of k
+  Heads dy[2];            // backward of the norm only
+  Heads out[2];
+  const void *w[2];       // norm weights
+  float *part[2];         // backward: partial rows of dw, [grid, d]
+  const int32_t *pos;
+  int64_t pos_batch;      // elements
+  int32_t H[2];
+  uint32_t magic[2];      // ceil(2^32 / H)
+  int32_t N;
+  int32_t d;
+  int32_t nvec;           // vectors per head
+  int32_t rot_vecs;       // half layout: vectors of the first half's pairs
+  int32_t tb;             // tokens per block
+  int32_t blocks_n;       // blocks per sample
+  int64_t blocks;
+  float eps;
+  float inv_d;
+  float dir;              // +1: by the angle, -1: by the negative angle
+  Rotation rot;
+};
+
+// cos and sin of a phase given as a 64-bit fraction of a turn.  The top 32
+// bits (rounded) are taken to the nearest quarter turn; what remains, at most
+// pi/4, goes through the Taylor polynomials of degree 9 and 10 (truncation
+// below 2e-9 and 2e-10), so both are within an ulp or so of float32 at any
+// position.
+__device__ __forceinline__ void cos_sin(uint64_t phase, float &c, float &s) {
+  const uint32_t p = (uint32_t)((phase + (uint64_t(1) << 31)) >> 32);
+  const uint32_t quarter = (p + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(p - (quarter << 30)) *
+                  (6.283185307179586f / 4294967296.0f);
+  const float x2 = x * x;
+  float a = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);
+  a = fmaf(x2, a, 8.3333333e-3f);
+  a = fmaf(x2, a, -1.6666667e-1f);
+  const float sn = fmaf(x * x2, a, x);
+  float b = fmaf(x2, -2.7557319e-7f, 2.4801587e-5f);
+  b = fmaf(x2, b, -1.3888889e-3f);
+  b = fmaf(x2, b, 4.1666667e-2f);
+  b = fmaf(x2, b, -0.5f);
+  const float cs = fmaf(x2, b, 1.0f);
+  const float u = (quarter & 1) ? sn : cs;
+  const float v = (quarter & 1) ? cs : sn;
+  c = ((quarter + 1) & 2) ? -u : u;
+  s = (quarter & 2) ? -v : v;
+}
+
+// Sum over the L lanes that share a head (L a power of two, the lanes
+// aligned to it), in a fixed order; every lane gets it.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L >= 2) v = dpp_add<0xB1>(v);
+  if constexpr (L >= 4) v = dpp_add<0x4E>(v);
+  if constexpr (L >= 8) v = dpp_add<0x141>(v);
+  if constexpr (L >= 16) v = dpp_add<0x140>(v);
+  if constexpr (L >= 32) v += __shfl_xor(v, 16);
+  if constexpr (L >= 64) v += __shfl_xor(v, 32);
+  return v;
+}
+
+// The two vectors of a head that a lane holds.  Interleaved: vectors slot and
+// slot + ceil(nvec / 2).  Half: the rot_vecs slots of rotated pairs hold
+// vectors slot and slot + rot_vecs, the rest of the head follows.
+template <bool HALF>
+__device__ __forceinline__ void slot_vectors(const Job &job, int slot, int &a,
+                                             int &b) {
+  if constexpr (HALF) {
+    const int rv = job.rot_vecs;
+    if (slot < rv) {
+      a = slot;
+      b = slot + rv;
+    } else {
+      a = rv + slot;
+      b = a + (job.nvec - 2 * rv + 1) / 2;
+    }
+  } else {
+    a = slot;
+    b = slot + (job.nvec + 1) / 2;
+  }
+}
+
+// Rotates the lane's 2 * E values; cs: its E (cos, sin) entries.
+template <int E, bool HALF>
+__device__ __forceinline__ void rotate(float (&xa)[E], float (&xb)[E],
+                                       const float2 (&cs)[E]) {
+  if constexpr (HALF) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float u = xa[i], v = xb[i];
+      xa[i] = u * cs[i].x - v * cs[i].y;
+      xb[i] = u * cs[i].y + v * cs[i].x;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      float u = xa[2 * i], v = xa[2 * i + 1];
+      xa[2 * i] = u * cs[i].x - v * cs[i].y;
+      xa[2 * i + 1] = u * cs[i].y + v * cs[i].x;
+      u = xb[2 * i], v = xb[2 * i + 1];
+      xb[2 * i] = u * cs[E / 2 + i].x - v * cs[E / 2 + i].y;
+      xb[2 * i + 1] = u * cs[E / 2 + i].y + v * cs[E / 2 + i].x;
+    }
+  }
+}
+
+enum { kRope = 0, kNormFwd = 1, kNormBwd = 2 };
+
+template <typename T, int L, bool HALF, int OP>
+__global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
+  constexpr int E = Elems<T>::value;
+  constexpr int kRows = kBlock / L;   // heads a workgroup takes at a time
+  constexpr int kPitch = L * E;       // table entries per token
+  extern __shared__ float2 table[];   // [tb][kPitch]
+  const int tid = threadIdx.x;
+  const int slot = tid % L;
+  const int group = tid / L;
+  int va, vb;
+  slot_vectors<HALF>(job, slot, va, vb);
+  const bool ok_a = va < job.nvec && slot < (job.nvec + 1) / 2;
+  const bool ok_b = ok_a && vb < job.nvec;
+  if (!ok_a) va = 0;
+  if (!ok_b) vb = va;
+  // entries of the lane's pairs in the table's row of a token
+  const int ta = HALF ? slot * E : (ok_a ? va : 0) * (E / 2);
+  const int tbl = HALF ? slot * E + E / 2 : (ok_b ? vb : 0) * (E / 2);
+
+  float acc[OP == kNormBwd ? 2 : 1][OP == kNormBwd ? 2 * E : 1];
+  if constexpr (OP == kNormBwd) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2 * E; ++i) acc[t][i] = 0.f;
+  }
+
+  for (int64_t blk = blockIdx.x; blk < job.blocks; blk += gridDim.x) {
+    const int b = (int)(blk / job.blocks_n);
+    const int n0 = (int)(blk - (int64_t)b * job.blocks_n) * job.tb;
+    const int tb = min(job.tb, job.N - n0);
+    // the sines of the block's tokens; pairs past the rotated ones turn by 0
+    const int32_t *pos = job.pos + b * job.pos_batch + (int64_t)n0 * job.rot.axes;
+    for (int i = tid; i < tb * kPitch; i += kBlock) {
+      const int tok = i / kPitch;
+      const int j = i % kPitch;
+      float2 cs = {1.f, 0.f};
+      if (j < job.rot.pairs) {
+        uint64_t phase = 0;
+        for (int a = 0; a < job.rot.axes; ++a)
+          phase += (uint64_t)(int64_t)pos[tok * job.rot.axes + a] *
+                   job.rot.turns[a * job.rot.pairs + j];
+        cos_sin(phase, cs.x, cs.y);
+        cs.y *= job.dir;
+      }
+      table[i] = cs;
+    }
+    __syncthreads();
+
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int H = job.H[t];
+      const int rows = tb * H;
+      if (rows == 0) continue;
+      const char *in = job.in[t].data +
+                       (b * job.in[t].batch + n0 * job.in[t].token) * 16;
+      const char *dy = OP != kNormBwd
+                           ? nullptr
+                           : job.dy[t].data + (b * job.dy[t].batch +
+                                               n0 * job.dy[t].token) * 16;
+      char *out = const_cast<char *>(job.out[t].data) +
+                  (b * job.out[t].batch + n0 * job.out[t].token) * 16;
+      float w[OP == kRope ? 1 : 2 * E];
+      if constexpr (OP != kRope) {
+        const Vec wa = load_vec((const char *)job.w[t] + va * 16);
+        const Vec wb = load_vec((const char *)job.w[t] + vb * 16);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          w[i] = elem<T>(wa, i);
+          w[E + i] = elem<T>(wb, i);
+        }
+      }
+      for (int row0 = 0; row0 < rows; row0 += kRows) {
+        const bool live = row0 + group < rows;
+        const int row = live ? row0 + group : 0;
+        const int tok = H == 1 ? row : (int)__umulhi((uint32_t)row, job.magic[t]);
+        const int head = row - tok * H;
+        const char *src = in + ((int64_t)tok * job.in[t].token +
+                                (int64_t)head * job.in[t].head) * 16;
+        Vec xa = load_stream(src + va * 16);
+        Vec xb = load_stream(src + vb * 16);
+        Vec ya = {}, yb = {};
+        if constexpr (OP == kNormBwd) {
+          const char *sdy = dy + ((int64_t)tok * job.dy[t].token +
+                                  (int64_t)head * job.dy[t].head) * 16;
+          ya = load_stream(sdy + va * 16);
+          yb = load_stream(sdy + vb * 16);
+        }
+        float2 cs[E];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          cs[i] = table[tok * kPitch + ta + i];
+          cs[E / 2 + i] = table[tok * kPitch + tbl + i];
+        }
+        if (!ok_a) xa = vzero(), ya = vzero();
+        if (!ok_b) xb = vzero(), yb = vzero();
+        float fa[E], fb[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          fa[i] = elem<T>(xa, i);
+          fb[i] = elem<T>(xb, i);
+        }
+        if constexpr (OP != kRope) {
+          float ss = 0.f;
+#pragma unroll
+          for (int i = 0; i < E; ++i) ss = fmaf(fa[i], fa[i], ss);
+#pragma unroll
+          for (int i = 0; i < E; ++i) ss = fmaf(fb[i], fb[i], ss);
+          if constexpr (OP == kNormFwd) {
+            ss = lanes_sum<L>(ss);
+            const float r = rsqrtf(fmaf(ss, job.inv_d, job.eps));
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              fa[i] = fa[i] * r * w[i];
+              fb[i] = fb[i] * r * w[E + i];
+            }
+            rotate<E, HALF>(fa, fb, cs);
+          } else {
+            float ga[E], gb[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              ga[i] = elem<T>(ya, i);
+              gb[i] = elem<T>(yb, i);
+            }
+            rotate<E, HALF>(ga, gb, cs);
+            float sg = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              sg = fmaf(ga[i] * w[i], fa[i], sg);
+              sg = fmaf(gb[i] * w[E + i], fb[i], sg);
+            }
+            ss = lanes_sum<L>(ss);
+            sg = lanes_sum<L>(sg);
+            const float r = rsqrtf(fmaf(ss, job.inv_d, job.eps));
+            const float m = sg * r * r * job.inv_d;  // r * mean(g * xh)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              if (live) {
+                acc[t][i] = fmaf(ga[i], fa[i] * r, acc[t][i]);
+                acc[t][E + i] = fmaf(gb[i], fb[i] * r, acc[t][E + i]);
+              }
+              fa[i] = r * (ga[i] * w[i] - fa[i] * m);
+              fb[i] = r * (gb[i] * w[E + i] - fb[i] * m);
+            }
+          }
+        } else {
+          rotate<E, HALF>(fa, fb, cs);
+        }
+        char *dst = out + ((int64_t)tok * job.out[t].token +
+                           (int64_t)head * job.out[t].head) * 16;
+        if (live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
+        if (live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
+      }
+    }
+    __syncthreads();
+  }
+
+  // One partial row of dw per workgroup: the lane groups of a wavefront are
+  // added by a butterfly, the four wavefronts in order through LDS.
+  if constexpr (OP == kNormBwd) {
+    __shared__ float stage[4][2][2 * L * E];
+    const int wave = wave_id();
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2 * E; ++i) {
+        float v = acc[t][i];
+#pragma unroll
+        for (int o = L; o < kWave; o *= 2) v += __shfl_xor(v, o);
+        const bool ok = i < E ? ok_a : ok_b;
+        if (ok && lane_id() < L)
+          stage[wave][t][(i < E ? va : vb) * E + i % E] = v;
+      }
+    __syncthreads();
+    for (int i = tid; i < 2 * job.d; i += kBlock) {
+      const int t = i >= job.d;
+      const int c = i - t * job.d;
+      if (job.H[t] > 0)
+        job.part[t][(int64_t)blockIdx.x * job.d + c] =
+            ((stage[0][t][c] + stage[1][t][c]) + stage[2][t][c]) +
+            stage[3][t][c];
+    }
+  }
+}
+
+// ------------------------------------------------------------------- checks
+
+int elems_per_vec(int dtype) { return dtype == ADALN_BF16 ? 8 : 4; }
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+int check_sizes(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
+                int dtype) {
+  if (dtype != ADALN_F32 && dtype != ADALN_BF16)
+    return fail(ADALN_ERR_DTYPE, "unknown dtype code %d", dtype);
+  if (B < 0 || N < 0 || Hq < 0 || Hk < 0)
+    return fail(ADALN_ERR_INVALID, "negative size: B=%lld N=%lld Hq=%lld Hk=%lld",
+                (long long)B, (long long)N, (long long)Hq, (long long)Hk);
+  if (d <= 0)
+    return fail(ADALN_ERR_INVALID, "d must be positive, got %lld", (long long)d);
+  const int E = elems_per_vec(dtype);
+  if (d % E != 0)
+    return fail(ADALN_ERR_ALIGN, "d=%lld is not a multiple of %d", (long long)d, E);
+  if (d > kMaxHead)
+    return fail(ADALN_ERR_UNSUPPORTED, "d=%lld exceeds the widest head (%d)",
+                (long long)d, kMaxHead);
+  if (Hq > 4096 || Hk > 4096)
+    return fail(ADALN_ERR_INVALID, "more than 4096 heads");
+  if (B > kMaxRows || N > kMaxRows || (N > 0 && B > kMaxRows / N))
+    return fail(ADALN_ERR_INVALID, "B*N exceeds 2^31-1 tokens");
+  return ADALN_OK;
+}
+
+int check_rotation(const adaln_rotation_t *rot, int64_t d, int dtype,
+                   bool rows) {
+  if (rot == nullptr) return fail(ADALN_ERR_INVALID, "rot is NULL");
+  if (rot->axes < 1 || rot->axes > kMaxAxes)
+    return fail(ADALN_ERR_INVALID, "axes must be 1 to %d, got %d", kMaxAxes,
+                rot->axes);
+  if (rot->pairs < 1 || 2 * (int64_t)rot->pairs > d)
+    return fail(ADALN_ERR_INVALID, "pairs must be 1 to d/2, got %d", rot->pairs);
+  if ((int64_t)rot->axes * rot->pairs > kMaxFreqs)
+    return fail(ADALN_ERR_UNSUPPORTED, "axes*pairs exceeds %d", kMaxFreqs);
+  if (rot->layout != ADALN_ROPE_INTERLEAVED && rot->layout != ADALN_ROPE_HALF)
+    return fail(ADALN_ERR_INVALID, "unknown layout %d", rot->layout);
+  if (rot->layout == ADALN_ROPE_HALF && rot->pairs % elems_per_vec(dtype) != 0)
+    return fail(ADALN_ERR_ALIGN,
+                "half layout: pairs=%d is not a multiple of %d", rot->pairs,
+                elems_per_vec(dtype));
+  if (rot->pos_batch_stride < 0 || rot->pos_batch_stride % rot->axes != 0)
+    return fail(ADALN_ERR_INVALID, "bad pos_batch_stride %lld",
+                (long long)rot->pos_batch_stride);
+  if (rot->freqs == nullptr) return fail(ADALN_ERR_INVALID, "freqs is NULL");
+  for (int i = 0; i < rot->axes * rot->pairs; ++i)
+    if (!(fabs(rot->freqs[i]) <= 1e6))
+      return fail(ADALN_ERR_INVALID, "freqs[%d] is not within 1e6", i);
+  if (rows && rot->pos == nullptr)
+    return fail(ADALN_ERR_INVALID, "pos is NULL");
+  if (rows && reinterpret_cast<uintptr_t>(rot->pos) % 4 != 0)
+    return fail(ADALN_ERR_ALIGN, "pos is not 4-byte aligned");
+  return ADALN_OK;
+}
+
+// One tensor: pointer, alignment, strides; an output's rows must not overlap.
+int check_heads(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
+                int64_t d, int dtype, bool output, const char *name) {
+  if (B * N == 0 || H == 0) return ADALN_OK;
+  if (t == nullptr || t->data == nullptr)
+    return fail(ADALN_ERR_INVALID, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(t->data) % 16 != 0)
+    return fail(ADALN_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  const int E = elems_per_vec(dtype);
+  struct Dim {
+    int64_t stride, size;
+  } dim[3] = {{t->head_stride, H}, {t->token_stride, N}, {t->batch_stride, B}};
+  for (Dim &s : dim) {
+    if (s.size == 1) s.stride = 0;
+    if (s.stride < 0 || s.stride > (int64_t(1) << 40))
+      return fail(ADALN_ERR_INVALID, "%s has a stride of %lld", name,
+                  (long long)s.stride);
+    if (s.stride % E != 0)
+      return fail(ADALN_ERR_ALIGN,
+                  "%s has a stride that is not a multiple of %d", name, E);
+  }
+  if (dim[0].stride / E >= (int64_t(1) << 31))
+    return fail(ADALN_ERR_UNSUPPORTED, "%s: heads too far apart", name);
+  if (output) {
+    std::sort(dim, dim + 3,
+              [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    int64_t extent = d;
+    for (const Dim &s : dim) {
+      if (s.size == 1) continue;
+      if (s.stride < extent)
+        return fail(ADALN_ERR_INVALID, "%s: heads overlap", name);
+      extent += s.stride * (s.size - 1);
+    }
+  }
+  return ADALN_OK;
+}
+
+// ---------------------------------------------------------------- launching
+
+Heads heads_of(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
+               int dtype) {
+  Heads h = {};
+  if (t == nullptr || H == 0) return h;
+  const int E = elems_per_vec(dtype);
+  h.data = static_cast<const char *>(t->data);
+  h.batch = B > 1 ? t->batch_stride / E : 0;
+  h.token = N > 1 ? t->token_stride / E : 0;
+  h.head = H > 1 ? (int32_t)(t->head_stride / E) : 0;
+  return h;
+}
+
+// Tokens per block.
+int block_tokens(int64_t B, int64_t N) {
+  int tb = kMaxTokens;
+  while (tb > 1 && B * ((N + tb - 1) / tb) < 4 * kCUs) tb /= 2;
+  return tb;
+}
+
+struct HeadsPlan {
+  int tb;
+  int64_t blocks_n;
+  int64_t blocks;
+  int64_t grid;
+};
+
+// The backward of the norm runs a persistent grid of 4 workgroups per CU, so
+// that each adds up dw over many blocks before it writes its partial row.
+HeadsPlan heads_plan(int64_t B, int64_t N, bool bwd) {
+  HeadsPlan p;
+  p.tb = block_tokens(B, N);
+  p.blocks_n = (N + p.tb - 1) / p.tb;
+  p.blocks = B * p.blocks_n;
+  p.grid = std::min<int64_t>(p.blocks, bwd ? 4 * kCUs : kMaxGrid);
+  return p;
+}
+
+int lanes_per_head(int nvec) {
+  int L = 1;
+  while (2 * L < nvec) L *= 2;
+  return L;
+}
+
+template <typename T, int OP, int L>
+hipError_t go(const Job &job, bool half, int64_t grid, hipStream_t stream) {
+  const size_t lds = (size_t)job.tb * L * Elems<T>::value * sizeof(float2);
+  return half ? launch_kernel_lds(heads_kernel<T, L, true, OP>, grid, kBlock,
+                                  lds, stream, job)
+              : launch_kernel_lds(heads_kernel<T, L, false, OP>, grid, kBlock,
+                                  lds, stream, job);
+}
+
+template <typename T, int OP>
+hipError_t launch_heads(const Job &job, bool half, int64_t grid,
+                        hipStream_t stream) {
+  switch (lanes_per_head(job.nvec)) {
+    case 1: return go<T, OP, 1>(job, half, grid, stream);
+    case 2: return go<T, OP, 2>(job, half, grid, stream);
+    case 4: return go<T, OP, 4>(job, half, grid, stream);
+    case 8: return go<T, OP, 8>(job, half, grid, stream);
+    case 16: return go<T, OP, 16>(job, half, grid, stream);
+    case 32: return go<T, OP, 32>(job, half, grid, stream);
+    default:
+      if constexpr (Elems<T>::value == 4)
+        return go<T, OP, 64>(job, half, grid, stream);
+      return hipErrorInvalidValue;
+  }
+}
+
+void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
+              bool inverse, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
+              int dtype) {
+  const int E = elems_per_vec(dtype);
+  const int64_t H[2] = {Hq, Hk};
+  for (int t = 0; t < 2; ++t) {
+    job.H[t] = (int32_t)H[t];
+    // exact quotients for rows < 16 * 4096 = 2^16: the error of the quotient,
+    // row * H / 2^32, stays below 1 / H
+    job.magic[t] =
+        H[t] > 1 ? (uint32_t)(((uint64_t(1) << 32) + H[t] - 1) / H[t]) : 0;
+  }
+  job.pos = rot->pos;
+  job.pos_batch = rot->pos_batch_stride;
+  job.N = (int32_t)N;
+  job.d = (int32_t)d;
+  job.nvec = (int32_t)(d / E);
+  job.rot_vecs = rot->layout == ADALN_ROPE_HALF ? rot->pairs / E : 0;
+  job.tb = p.tb;
+  job.blocks_n = (int32_t)p.blocks_n;
+  job.blocks = p.blocks;
+  job.dir = inverse ? -1.f : 1.f;
+  job.rot.axes = rot->axes;
+  job.rot.pairs = rot->pairs;
+  for (int i = 0; i < rot->axes * rot->pairs; ++i) {
+    // radians -> turns; the fraction of a turn in 64 bits (long double keeps
+    // the 64 bits of the product)
+    const long double t = (long double)rot->freqs[i] *
+                          0.159154943091895335768883763372514362L;
+    long double f = t - floorl(t);
+    f = f * 18446744073709551616.0L + 0.5L;
+    job.rot.turns[i] = f >= 18446744073709551616.0L ? 0 : (uint64_t)f;
+  }
+}
+
+int hip_fail(hipError_t e, const char *what) {
+  return fail(ADALN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+template <int OP>
+int enqueue(const Job &job, int layout, int64_t grid, int dtype,
+            hipStream_t stream, const char *what) {
+  const bool half = layout == ADALN_ROPE_HALF;
+  const hipError_t e = dtype == ADALN_BF16
+                           ? launch_heads<bf16, OP>(job, half, grid, stream)
+                           : launch_heads<float, OP>(job, half, grid, stream);
+  return e == hipSuccess ? ADALN_OK : hip_fail(e, what);
+}
+
+int check_weight(const void *w, bool needed, const char *name) {
+  if (!needed) return ADALN_OK;
+  if (w == nullptr) return fail(ADALN_ERR_INVALID, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(w) % 16 != 0)
+    return fail(ADALN_ERR_ALIGN, "%s is not 16-byte aligned", name);
+  return ADALN_OK;
+}
+
+int rope(const adaln_heads_t *q, const adaln_heads_t *k,
+         const adaln_rotation_t *rot, const adaln_heads_t *q_out,
+         const adaln_heads_t *k_out, bool inverse, int64_t B, int64_t N,
+         int64_t Hq, int64_t Hk, int64_t d, int dtype, void *stream,
+         const char *what) {
+  ADALN_TRY(check_sizes(B, N, Hq, Hk, d, dtype));
+  const bool rows = B * N > 0 && Hq + Hk > 0;
+  ADALN_TRY(check_rotation(rot, d, dtype, rows));
+  ADALN_TRY(check_heads(q, B, N, Hq, d, dtype, false, "q"));
+  ADALN_TRY(check_heads(k, B, N, Hk, d, dtype, false, "k"));
+  ADALN_TRY(check_heads(q_out, B, N, Hq, d, dtype, true, "q_out"));
+  ADALN_TRY(check_heads(k_out, B, N, Hk, d, dtype, true, "k_out"));
+  if (!rows) return ok();
+  const HeadsPlan p = heads_plan(B, N, false);
+  Job job = {};
+  fill_job(job, p, rot, inverse, N, Hq, Hk, d, dtype);
+  job.in[0] = heads_of(q, B, N, Hq, dtype);
+  job.in[1] = heads_of(k, B, N, Hk, dtype);
+  job.out[0] = heads_of(q_out, B, N, Hq, dtype);
+  job.out[1] = heads_of(k_out, B, N, Hk, dtype);
+  ADALN_TRY(enqueue<kRope>(job, rot->layout, p.grid, dtype,
+                           (hipStream_t)stream, what));
+  return ok();
+}
+
+}  // namespace
+}  // namespace adaln
+
+using namespace adaln;
+
+ADALN_API int adaln_rope_fwd(const adaln_heads_t *q, const adaln_heads_t *k,
+                             const adaln_rotation_t *rot,
+                             const adaln_heads_t *q_out,
+                             const adaln_heads_t *k_out, int64_t B, int64_t N,
+                             int64_t Hq, int64_t Hk, int64_t d, int dtype,
+                             void *stream) {
+  return rope(q, k, rot, q_out, k_out, false, B, N, Hq, Hk, d, dtype, stream,
+              "adaln_rope_fwd launch");
+}
+
+ADALN_API int adaln_rope_bwd(const adaln_heads_t *dq_out,
+                             const adaln_heads_t *dk_out,
+                             const adaln_rotation_t *rot,
+                             const adaln_heads_t *dq, const adaln_heads_t *dk,
+                             int64_t B, int64_t N, int64_t Hq, int64_t Hk,
+                             int64_t d, int dtype, void *stream) {
+  return rope(dq_out, dk_out, rot, dq, dk, true, B, N, Hq, Hk, d, dtype,
+              stream, "adaln_rope_bwd launch");
+}
+
+ADALN_API int adaln_qk_norm_rope_fwd(
+    const adaln_heads_t *q, const adaln_heads_t *k, const void *wq,
+    const void *wk, float eps, const adaln_rotation_t *rot,
+    const adaln_heads_t *q_out, const adaln_heads_t *k_out, int64_t B,
+    int64_t N, int64_t Hq, int64_t Hk, int64_t d, int dtype, void *stream) {
+  ADALN_TRY(check_sizes(B, N, Hq, Hk, d, dtype));
+  const bool rows = B * N > 0 && Hq + Hk > 0;
+  if (!(eps >= 0.f) || isinf(eps))
+    return fail(ADALN_ERR_INVALID, "eps must be finite and not negative");
+  ADALN_TRY(check_rotation(rot, d, dtype, rows));
+  ADALN_TRY(check_heads(q, B, N, Hq, d, dtype, false, "q"));
+  ADALN_TRY(check_heads(k, B, N, Hk, d, dtype, false, "k"));
+  ADALN_TRY(check_heads(q_out, B, N, Hq, d, dtype, true, "q_out"));
+  ADALN_TRY(check_heads(k_out, B, N, Hk, d, dtype, true, "k_out"));
+  ADALN_TRY(check_weight(wq, rows && Hq > 0, "wq"));
+  ADALN_TRY(check_weight(wk, rows && Hk > 0, "wk"));
+  if (!rows) return ok();
+  const HeadsPlan p = heads_plan(B, N, false);
+  Job job = {};
+  fill_job(job, p, rot, false, N, Hq, Hk, d, dtype);
+  job.in[0] = heads_of(q, B, N, Hq, dtype);
+  job.in[1] = heads_of(k, B, N, Hk, dtype);
+  job.out[0] = heads_of(q_out, B, N, Hq, dtype);
+  job.out[1] = heads_of(k_out, B, N, Hk, dtype);
+  job.w[0] = wq;
+  job.w[1] = wk;
+  job.eps = eps;
+  job.inv_d = 1.f / (float)d;
+  ADALN_TRY(enqueue<kNormFwd>(job, rot->layout, p.grid, dtype,
+                              (hipStream_t)stream,
+                              "adaln_qk_norm_rope_fwd launch"));
+  return ok();
+}
+
+ADALN_API size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N,
+                                                        int64_t Hq, int64_t Hk,
+                                                        int64_t d, int dtype) {
+  if (check_sizes(B, N, Hq, Hk, d, dtype) != ADALN_OK) return 0;
+  if (B * N == 0) return 0;
+  return (size_t)heads_plan(B, N, true).grid * 2 * (size_t)d * sizeof(float);
+}
+
+ADALN_API int adaln_qk_norm_rope_bwd(
+    const adaln_heads_t *dq_out, const adaln_heads_t *dk_out,
+    const adaln_heads_t *q, const adaln_heads_t *k, const void *wq,
+    const void *wk, float eps, const adaln_rotation_t *rot,
+    const adaln_heads_t *dq, const adaln_heads_t *dk, float *dwq, float *dwk,
+    void *workspace, size_t workspace_bytes, int64_t B, int64_t N, int64_t Hq,
+    int64_t Hk, int64_t d, int dtype, void *stream) {
+  ADALN_TRY(check_sizes(B, N, Hq, Hk, d, dtype));
+  const bool rows = B * N > 0 && Hq + Hk > 0;
+  if (!(eps >= 0.f) || isinf(eps))
+    return fail(ADALN_ERR_INVALID, "eps must be finite and not negative");
+  ADALN_TRY(check_rotation(rot, d, dtype, rows));
+  ADALN_TRY(check_heads(dq_out, B, N, Hq, d, dtype, false, "dq_out"));
+  ADALN_TRY(check_heads(dk_out, B, N, Hk, d, dtype, false, "dk_out"));
+  ADALN_TRY(check_heads(q, B, N, Hq, d, dtype, false, "q"));
+  ADALN_TRY(check_heads(k, B, N, Hk, d, dtype, false, "k"));
+  ADALN_TRY(check_heads(dq, B, N, Hq, d, dtype, true, "dq"));
+  ADALN_TRY(check_heads(dk, B, N, Hk, d, dtype, true, "dk"));
+  ADALN_TRY(check_weight(wq, rows && Hq > 0, "wq"));
+  ADALN_TRY(check_weight(wk, rows && Hk > 0, "wk"));
+  ADALN_TRY(check_weight(dwq, Hq > 0, "dwq"));
+  ADALN_TRY(check_weight(dwk, Hk > 0, "dwk"));
+  if (Hq + Hk == 0) return ok();
+  const HeadsPlan p = heads_plan(B, N, true);
+  const int64_t grid = rows ? p.grid : 0;
+  const size_t need = (size_t)grid * 2 * (size_t)d * sizeof(float);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(ADALN_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s",
+                  need, workspace_bytes,
+                  workspace == nullptr ? " (NULL)" : "");
+    ADALN_TRY(check_weight(workspace, true, "workspace"));
+  }
+  float *part[2] = {static_cast<float *>(workspace),
+                    static_cast<float *>(workspace) + grid * d};
+  if (rows) {
+    Job job = {};
+    fill_job(job, p, rot, true, N, Hq, Hk, d, dtype);
+    job.in[0] = heads_of(q, B, N, Hq, dtype);
+    job.in[1] = heads_of(k, B, N, Hk, dtype);
+    job.dy[0] = heads_of(dq_out, B, N, Hq, dtype);
+    job.dy[1] = heads_of(dk_out, B, N, Hk, dtype);
+    job.out[0] = heads_of(dq, B, N, Hq, dtype);
+    job.out[1] = heads_of(dk, B, N, Hk, dtype);
+    job.w[0] = wq;
+    job.w[1] = wk;
+    job.part[0] = part[0];
+    job.part[1] = part[1];
+    job.eps = eps;
+    job.inv_d = 1.f / (float)d;
+    ADALN_TRY(enqueue<kNormBwd>(job, rot->layout, grid, dtype,
+                                (hipStream_t)stream,
+                                "adaln_qk_norm_rope_bwd launch"));
+  }
+  // the sums over the workgroups' partial rows, in index order (a missing
+  // tensor's column takes the other one's)
+  const int a = Hq > 0 ? 0 : 1, b = Hk > 0 ? 1 : 0;
+  float *dw[2] = {dwq, dwk};
+  const hipError_t e =
+      launch_dmod_finish(part[a], part[b], dw[a], dw[b], 1, (int32_t)d,
+                         (int32_t)grid, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "adaln_qk_norm_rope_bwd finish");
+  return ok();
+}

@@ -287,6 +287,100 @@ int adaln_bwd_segments(const void *dy, const void *x, const void *scale,
                        int64_t D, int dtype, void *stream);
 
 /*
+ * Rotary positions and the norms of queries and keys.
+ *
+ * The heads of a block's queries and keys are [B, N, H, d] in `dtype`, in any
+ * order of memory in which a head's d features are contiguous: slices of one
+ * projection's output, or the [B, H, N, d] that an attention kernel takes.
+ * adaln_heads describes one such tensor: its first element and the distances,
+ * in elements, between samples, tokens and heads (multiples of 8 for bf16, 4
+ * for f32; the distance along a dimension of size one is not read).  Inputs
+ * may repeat (a distance of 0); the heads of an output must not overlap.  An
+ * output may be its own input, with the same distances; any other overlap of
+ * an output with an input is an error that the library cannot see.
+ */
+typedef struct adaln_heads {
+  void *data; /* device, 16-byte aligned; NULL if there are no heads */
+  int64_t batch_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+} adaln_heads_t;
+
+/*
+ * The rotation: pair j < pairs of every head of token n of sample b turns by
+ *     angle = sum_a pos[b, n, a] * freqs[a * pairs + j]          (radians)
+ *     (u, v) -> (u cos - v sin, u sin + v cos)
+ * so an axis that does not move a pair has a zero there (time, height and
+ * width with a run of pairs each: a block matrix).  Pair j is the features
+ * (2j, 2j + 1) of the head, or (j, j + pairs); the features from 2 * pairs on
+ * pass through.  The angle is reduced exactly for every 32-bit position.
+ */
+#define ADALN_ROPE_INTERLEAVED 0 /* pairs (2j, 2j + 1) */
+#define ADALN_ROPE_HALF 1        /* pairs (j, j + pairs); pairs a multiple of
+                                    8 (bf16) or 4 (f32) */
+typedef struct adaln_rotation {
+  const int32_t *pos;       /* device [N, axes] or [B, N, axes] */
+  int64_t pos_batch_stride; /* elements between samples' positions; 0: shared */
+  const double *freqs;      /* host [axes, pairs], each within +-1e6; read
+                               during the call only */
+  int32_t axes;             /* 1 .. 4; axes * pairs <= 384 */
+  int32_t pairs;            /* 1 .. d / 2 */
+  int32_t layout;
+} adaln_rotation_t;
+
+/*
+ * Rotates q [B, N, Hq, d] and k [B, N, Hk, d] in one launch; either may have
+ * no heads (NULL).  d is a multiple of 8 (bf16) or 4 (f32), at most 512; at
+ * most 4096 heads; B * N < 2^31.  adaln_rope_bwd is its gradient, the
+ * rotation by the negative angle: dq = rot^-1(dq_out).
+ */
+int adaln_rope_fwd(const adaln_heads_t *q, const adaln_heads_t *k,
+                   const adaln_rotation_t *rot, const adaln_heads_t *q_out,
+                   const adaln_heads_t *k_out, int64_t B, int64_t N,
+                   int64_t Hq, int64_t Hk, int64_t d, int dtype, void *stream);
+
+int adaln_rope_bwd(const adaln_heads_t *dq_out, const adaln_heads_t *dk_out,
+                   const adaln_rotation_t *rot, const adaln_heads_t *dq,
+                   const adaln_heads_t *dk, int64_t B, int64_t N, int64_t Hq,
+                   int64_t Hk, int64_t d, int dtype, void *stream);
+
+/*
+ * The RMS norm of each head, then the rotation, in one pass over q and k:
+ *     r = 1 / sqrt(mean_d x^2 + eps)      y = rot(x * r * w)
+ *   wq, wk  [d] dtype, one weight vector for all heads of q and of k
+ * The sizes of adaln_rope_fwd.  Nothing is saved for the backward.
+ */
+int adaln_qk_norm_rope_fwd(const adaln_heads_t *q, const adaln_heads_t *k,
+                           const void *wq, const void *wk, float eps,
+                           const adaln_rotation_t *rot,
+                           const adaln_heads_t *q_out,
+                           const adaln_heads_t *k_out, int64_t B, int64_t N,
+                           int64_t Hq, int64_t Hk, int64_t d, int dtype,
+                           void *stream);
+
+/* Bytes of device workspace of adaln_qk_norm_rope_bwd (partial sums of the
+ * weights' gradients).  A pure function of its arguments; 0 for invalid ones. */
+size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq,
+                                              int64_t Hk, int64_t d, int dtype);
+
+/*
+ * Its gradient, with t = rot^-1(dy), g = t * w, xh = x * r:
+ *     dx = r * (g - xh * mean_d(g * xh))     dw = sum over tokens, heads of t * xh
+ *   q, k       the forward's inputs;  dq_out, dk_out: gradients of its outputs
+ *   dq, dk     [B, N, H, d] dtype out
+ *   dwq, dwk   [d] f32 out (overwritten; zero if there are no tokens)
+ * One launch and a fixed-order sum of the workgroups' partial rows: results
+ * are bitwise reproducible.
+ */
+int adaln_qk_norm_rope_bwd(
+    const adaln_heads_t *dq_out, const adaln_heads_t *dk_out,
+    const adaln_heads_t *q, const adaln_heads_t *k, const void *wq,
+    const void *wk, float eps, const adaln_rotation_t *rot,
+    const adaln_heads_t *dq, const adaln_heads_t *dk, float *dwq, float *dwk,
+    void *workspace, size_t workspace_bytes, int64_t B, int64_t N, int64_t Hq,
+    int64_t Hk, int64_t d, int dtype, void *stream);
+
+/*
  * Dual-constraint bucket batch size of section 2.A:
  *     max(1, min(floor(m_mem / S), floor(m_comp / S^p)))
  * in exact integer arithmetic.  When S^p exceeds the int64 range the compute
