@@ -80,6 +80,11 @@ SIGNATURES = {
     "adaln_qk_norm_rope_bwd": (_INT, [_HP, _HP, _HP, _HP, _VP, _VP, _F, _RP,
                                       _HP, _HP, _VP, _VP, _VP, _SZ, _I64,
                                       _I64, _I64, _I64, _I64, _INT, _VP]),
+    "adaln_glu_fwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT,
+                             _INT, _VP]),
+    "adaln_glu_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
+    "adaln_glu_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
+                             _I64, _I64, _I64, _INT, _INT, _VP]),
     "adaln_bshape": (_I64, [_I64, _I64, _I64, ctypes.c_int32]),
     "adaln_bshape_real": (_I64, [_I64, _I64, ctypes.c_double,
                                  ctypes.c_double]),

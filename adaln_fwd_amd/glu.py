@@ -1,0 +1,108 @@
+"""Binding of the gated feed-forward (adaln_glu_*) for torch tensors: bfloat16
+token rows [M, D] or [B, N, D], weights [F, D] as a linear layer keeps them.
+Checks, streams and allocation are those of :mod:`adaln_fwd_amd.ops`."""
+
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .ops import _DTYPES, _check, _on, _ptr, _stream
+
+_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _shapes(x, wg, wu, act):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"unsupported dtype {x.dtype}; use bfloat16")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [M, D] or [B, N, D], got shape "
+                         f"{tuple(x.shape)}")
+    if act not in _ACTS:
+        raise ValueError(f"act must be 'silu' or 'gelu', got {act!r}")
+    lead, D = tuple(x.shape[:-1]), x.shape[-1]
+    F = wg.shape[0] if isinstance(wg, torch.Tensor) and wg.dim() == 2 else -1
+    _check(x, "x", lead + (D,), x.dtype, x.device)
+    _check(wg, "wg", (F, D), x.dtype, x.device)
+    _check(wu, "wu", (F, D), x.dtype, x.device)
+    M = 1
+    for n in lead:
+        M *= n
+    return lead, M, D, F
+
+
+def glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, *,
+            act: str = "silu", save: bool = False,
+            h: Optional[torch.Tensor] = None,
+            saved: Optional[torch.Tensor] = None, stream=None):
+    """h = act(x wg^T) * (x wu^T), act "silu" or "gelu" (tanh form); returns
+    h, or with ``save=True`` (h, saved), `saved` being what the backward
+    needs to skip the two products: both projections in float32 [2, M, F]."""
+    lead, M, D, F = _shapes(x, wg, wu, act)
+    dev = x.device
+    lib = _lib.load()
+    with _on(dev, stream):
+        if h is None:
+            h = torch.empty(lead + (F,), dtype=x.dtype, device=dev)
+        _check(h, "h", lead + (F,), x.dtype, dev)
+        if not save and saved is not None:
+            raise ValueError("saved was given without save=True")
+        if save and saved is None:
+            saved = torch.empty(2, M, F, dtype=torch.float32, device=dev)
+        if save:
+            _check(saved, "saved", (2, M, F), torch.float32, dev)
+        rc = lib.adaln_glu_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(h),
+                               _ptr(saved), M, D, F, _ACTS[act],
+                               _DTYPES[x.dtype], _stream(dev, stream))
+    _lib.check(rc, "adaln_glu_fwd")
+    return (h, saved) if save else h
+
+
+def glu_bwd_workspace_bytes(M: int, D: int, F: int) -> int:
+    return int(_lib.load().adaln_glu_bwd_workspace_bytes(M, D, F, _lib.BF16))
+
+
+def glu_bwd(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor,
+            wu: torch.Tensor, saved: Optional[torch.Tensor] = None, *,
+            act: str = "silu", dx: Optional[torch.Tensor] = None,
+            dwg: Optional[torch.Tensor] = None,
+            dwu: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of :func:`glu_fwd`; returns (dx, dwg, dwu) in bfloat16.
+    Without `saved` both projections are computed again.  The workspace
+    (bytes from :func:`glu_bwd_workspace_bytes`) is allocated if not given."""
+    lead, M, D, F = _shapes(x, wg, wu, act)
+    dev, dt = x.device, x.dtype
+    _check(dh, "dh", lead + (F,), dt, dev)
+    if saved is not None:
+        _check(saved, "saved", (2, M, F), torch.float32, dev)
+    lib = _lib.load()
+    need = int(lib.adaln_glu_bwd_workspace_bytes(M, D, F, _DTYPES[dt]))
+    with _on(dev, stream):
+        if dx is None:
+            dx = torch.empty_like(x)
+        if dwg is None:
+            dwg = torch.empty_like(wg)
+        if dwu is None:
+            dwu = torch.empty_like(wu)
+        _check(dx, "dx", lead + (D,), dt, dev)
+        _check(dwg, "dwg", (F, D), dt, dev)
+        _check(dwu, "dwu", (F, D), dt, dev)
+        if workspace is None:
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8,
+                                    device=dev)
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on "
+                             f"{dev}")
+        rc = lib.adaln_glu_bwd(_ptr(dh), _ptr(x), _ptr(wg), _ptr(wu),
+                               _ptr(saved), _ptr(dx), _ptr(dwg), _ptr(dwu),
+                               _ptr(workspace),
+                               workspace.numel() * workspace.element_size(),
+                               M, D, F, _ACTS[act], _DTYPES[dt],
+                               _stream(dev, stream))
+    _lib.check(rc, "adaln_glu_bwd")
+    return dx, dwg, dwu

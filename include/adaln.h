@@ -381,6 +381,45 @@ int adaln_qk_norm_rope_bwd(
     int64_t Hk, int64_t d, int dtype, void *stream);
 
 /*
+ * Gated feed-forward (both projections, the activation and the product):
+ *     G = x Wg^T, U = x Wu^T         h = act(G) * U
+ *   x      [M, D] dtype in   token rows (an AdaLN output, flattened)
+ *   wg, wu [F, D] dtype in   the gate's and the other projection's weights
+ *   h      [M, F] dtype out
+ *   saved  [2, M, F] f32 out, or NULL: G, then U, for the backward
+ * dtype is ADALN_BF16 (the matrix cores' operands; sums, G and U are
+ * float32); D and F are multiples of 8, at most 65536 and 262144; M <= 2^24.
+ * M == 0 is a successful no-op.
+ */
+#define ADALN_ACT_SILU 0 /* g / (1 + exp(-g)) */
+#define ADALN_ACT_GELU 1 /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+int adaln_glu_fwd(const void *x, const void *wg, const void *wu, void *h,
+                  float *saved, int64_t M, int64_t D, int64_t F, int act,
+                  int dtype, void *stream);
+
+/* Bytes of device workspace of adaln_glu_bwd.  A pure function of its
+ * arguments; 0 for invalid ones and for M == 0. */
+size_t adaln_glu_bwd_workspace_bytes(int64_t M, int64_t D, int64_t F,
+                                     int dtype);
+
+/*
+ * Its gradient:
+ *     dU = dh * act(G), dG = dh * U * act'(G)     (rounded to dtype)
+ *     dx = dG Wg + dU Wu    dWg = dG^T x    dWu = dU^T x
+ *   dh       [M, F] dtype in;  x, wg, wu: the forward's inputs
+ *   saved    the forward's [2, M, F], or NULL to compute G and U again (half
+ *            as many operations more, and no 8 M F bytes kept)
+ *   dx       [M, D], dwg, dwu [F, D] dtype out (overwritten; with M == 0 the
+ *            weights' gradients are zero)
+ * Results are bitwise reproducible.
+ */
+int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
+                  const void *wu, const float *saved, void *dx, void *dwg,
+                  void *dwu, void *workspace, size_t workspace_bytes,
+                  int64_t M, int64_t D, int64_t F, int act, int dtype,
+                  void *stream);
+
+/*
  * Dual-constraint bucket batch size of section 2.A:
  *     max(1, min(floor(m_mem / S), floor(m_comp / S^p)))
  * in exact integer arithmetic.  When S^p exceeds the int64 range the compute
