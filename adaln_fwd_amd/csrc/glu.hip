@@ -87,12 +87,14 @@ __device__ __forceinline__ void arrive() {
 
 // An operand whose summed dimension is contiguous: ROWS rows of kStep
 // elements, 128 bytes each, 8 pieces of 16.  Row r keeps its piece c at
-// c ^ ((r >> 1) & 7): 16 consecutive rows then cover all banks.
+// c ^ ((r >> 1) & 7): 16 consecutive rows then cover all banks.  Rows past
+// the operand's last repeat it (their products are not stored); elements past
+// the end of the sum are loaded as zeros.
 template <int ROWS, int WAVES>
 struct Along {
   static constexpr int kBytes = ROWS * kStep * 2;
   static constexpr int kLoads = ROWS / (8 * WAVES);
-  static constexpr int kRowsPerLoad = 8 * WAVES;
+  uint32_t off[kLoads];  // byte offsets of the lane's loads from the base
 
   static __device__ __forceinline__ int lane_row() {
     return wave_id() * 8 + lane_id() / 8;
@@ -100,20 +102,28 @@ struct Along {
   static __device__ __forceinline__ int lane_piece() {
     return (lane_id() % 8) ^ ((lane_row() >> 1) & 7);
   }
-  // Load i of the step at k0 of rows [row0, row0 + kRowsPerLoad) of p.
-  static __device__ __forceinline__ void load(uint32_t lds, int i,
-                                              const bf16 *p, int64_t pitch,
-                                              int row0, int rows, int k0,
-                                              int K) {
-    lds += (i * WAVES + wave_id()) * 1024;
-    if (row0 + kRowsPerLoad <= rows && k0 + kStep <= K) {
-      dma(lds, p + row0 * pitch + k0,
-          (uint32_t)(lane_row() * (int)pitch + lane_piece() * 8) * 2);
+  // Rows from row0 of an operand of `rows` rows.
+  __device__ __forceinline__ void start(int row0, int rows, int pitch) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      off[i] = (uint32_t)min(i * 8 * WAVES + lane_row(), rows - 1 - row0) *
+                   (uint32_t)pitch * 2 +
+               lane_piece() * 16;
+  }
+  // The step at k0; p: row row0 of the operand.
+  __device__ __forceinline__ void load(uint32_t lds, const bf16 *p, int pitch,
+                                       int k0, int K) const {
+    lds += wave_id() * 1024;
+    const char *base = (const char *)(p + k0);
+    if (k0 + kStep <= K) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma(lds + i * WAVES * 1024, base, off[i]);
     } else {
-      const int r = min(row0 + lane_row(), rows - 1);
-      const int k = k0 + lane_piece() * 8;
-      dma_at(lds, k < K ? (const void *)(p + r * pitch + k)
-                        : (const void *)&kZeros);
+      const bool in = k0 + lane_piece() * 8 < K;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma_at(lds + i * WAVES * 1024, in ? base + off[i] : (const char *)&kZeros);
     }
   }
   // Fragment of 32 rows from `row`, elements 16 * kk ...: lane l holds row
@@ -131,33 +141,41 @@ struct Along {
 // An operand stored across the summed dimension: kStep rows of COLS columns,
 // COLS / 8 pieces of 16 bytes; row k keeps its piece c at c ^ ((k & 3) << 2),
 // so that the four rows that a transposing read takes lie in distinct banks.
+// Columns past the last repeat the last eight.
 template <int COLS, int WAVES>
 struct Across {
   static constexpr int kBytes = COLS * kStep * 2;
   static constexpr int kPieces = COLS / 8;
-  static constexpr int kRowsPerWave = 64 / kPieces;
-  static constexpr int kLoads = kStep / (kRowsPerWave * WAVES);
+  static constexpr int kRows = 64 / kPieces * WAVES;  // rows per load
+  static constexpr int kLoads = kStep / kRows;
+  uint32_t off;
 
   static __device__ __forceinline__ int lane_row() {
-    return wave_id() * kRowsPerWave + lane_id() / kPieces;
+    return (wave_id() * 64 + lane_id()) / kPieces;
   }
   static __device__ __forceinline__ int lane_piece() {
     return (lane_id() % kPieces) ^ ((lane_row() & 3) << 2);
   }
-  static __device__ __forceinline__ void load(uint32_t lds, int i,
-                                              const bf16 *p, int64_t pitch,
-                                              int col0, int cols, int k0,
-                                              int K) {
-    lds += (i * WAVES + wave_id()) * 1024;
-    const int kr = k0 + i * kRowsPerWave * WAVES;
-    if (col0 + COLS <= cols && k0 + kStep <= K) {
-      dma(lds, p + kr * pitch + col0,
-          (uint32_t)(lane_row() * (int)pitch + lane_piece() * 8) * 2);
+  __device__ __forceinline__ void start(int col0, int cols, int pitch) {
+    off = (uint32_t)lane_row() * (uint32_t)pitch * 2 +
+          min(lane_piece() * 8, cols - 8 - col0) * 2;
+  }
+  // p: column col0 of the operand's row 0.
+  __device__ __forceinline__ void load(uint32_t lds, const bf16 *p, int pitch,
+                                       int k0, int K) const {
+    lds += wave_id() * 1024;
+    const char *base = (const char *)(p + (int64_t)k0 * pitch);
+    const int64_t next = (int64_t)kRows * pitch * 2;
+    if (k0 + kStep <= K) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma(lds + i * WAVES * 1024, base + i * next, off);
     } else {
-      const int c = min(col0 + lane_piece() * 8, cols - 8);
-      const int k = kr + lane_row();
-      dma_at(lds, k < K ? (const void *)(p + k * pitch + c)
-                        : (const void *)&kZeros);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma_at(lds + i * WAVES * 1024, k0 + i * kRows + lane_row() < K
+                                           ? base + i * next + off
+                                           : (const char *)&kZeros);
     }
   }
   static __device__ __forceinline__ bf16x8 frag(const char *tile, int col,
@@ -262,9 +280,12 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   static_assert(!kPair || NI == 2, "a block of G and one of U");
   using Row = std::conditional_t<FORM == kDw, Across<kTile, kWaves>,
                                  Along<kTile, kWaves>>;
-  using Col = std::conditional_t<kPair, Along<kTile, kWaves>,
+  // (of a pair, the rows of one weight)
+  using Col = std::conditional_t<kPair, Along<kTile / 2, kWaves>,
                                  Across<kTile, kWaves>>;
-  __shared__ __align__(1024) char lds[2][Row::kBytes + Col::kBytes];
+  constexpr uint32_t kColBytes = kPair ? 2 * Col::kBytes : Col::kBytes;
+  constexpr uint32_t kBuf = Row::kBytes + kColBytes;
+  __shared__ __align__(1024) char lds[2][kBuf];
 
   int id = blockIdx.x + p.block0;
   const int tiles = p.tiles_r * p.tiles_c;
@@ -282,41 +303,29 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   const int s0 = split * p.steps_per_slice;
   const int s1 = min(s0 + p.steps_per_slice, p.steps);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)&lds[0][0];
-  constexpr uint32_t kBuf = Row::kBytes + Col::kBytes;
 
+  Row row;
+  Col col;
+  row.start(row0, FORM == kDw ? F : M, FORM == kDx || FORM == kDw ? F : D);
+  col.start(col0, kPair ? F : D, D);
   auto issue = [&](int s, int buf) {
     const uint32_t at = lds0 + buf * kBuf;
     if constexpr (kPair) {
       const int k0 = s * kStep;
-#pragma unroll
-      for (int i = 0; i < Row::kLoads; ++i)
-        Row::load(at, i, p.x, D, row0 + i * Row::kRowsPerLoad, M, k0, D);
-#pragma unroll
-      for (int i = 0; i < Col::kLoads; ++i) {
-        constexpr int half = Col::kLoads / 2;
-        Col::load(at + Row::kBytes, i, p.w[i / half], D,
-                  col0 + (i % half) * Col::kRowsPerLoad, F, k0, D);
-      }
+      row.load(at, p.x + (int64_t)row0 * D, D, k0, D);
+      col.load(at + Row::kBytes, p.w[0] + (int64_t)col0 * D, D, k0, D);
+      col.load(at + Row::kBytes + Col::kBytes,
+               p.w[1] + (int64_t)col0 * D, D, k0, D);
     } else if constexpr (FORM == kDx) {
       const int per = p.steps / 2;  // steps per plane
       const int pl = s >= per;
       const int k0 = (s - pl * per) * kStep;
-      const bf16 *g = p.dgu + (int64_t)pl * M * F;
-#pragma unroll
-      for (int i = 0; i < Row::kLoads; ++i)
-        Row::load(at, i, g, F, row0 + i * Row::kRowsPerLoad, M, k0, F);
-#pragma unroll
-      for (int i = 0; i < Col::kLoads; ++i)
-        Col::load(at + Row::kBytes, i, p.w[pl], D, col0, D, k0, F);
+      row.load(at, p.dgu + ((int64_t)pl * M + row0) * F, F, k0, F);
+      col.load(at + Row::kBytes, p.w[pl] + col0, D, k0, F);
     } else {
       const int k0 = s * kStep;
-      const bf16 *g = p.dgu + (int64_t)plane * M * F;
-#pragma unroll
-      for (int i = 0; i < Row::kLoads; ++i)
-        Row::load(at, i, g, F, row0, F, k0, M);
-#pragma unroll
-      for (int i = 0; i < Col::kLoads; ++i)
-        Col::load(at + Row::kBytes, i, p.x, D, col0, D, k0, M);
+      row.load(at, p.dgu + (int64_t)plane * M * F + row0, F, k0, M);
+      col.load(at + Row::kBytes, p.x + col0, D, k0, M);
     }
   };
 
@@ -331,29 +340,53 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  if (s0 < s1) issue(s0, 0);
-  for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
-    arrive();  // step s is in LDS, and all are done with the other buffer
-    if (s + 1 < s1) issue(s + 1, buf ^ 1);
+  // Fragments of the next 16 summed elements are read while the present
+  // ones are multiplied.  The one barrier of a step stands before its last
+  // multiplications: by then its own tile has been read (so the loads of the
+  // step after next may overwrite it) and the next step's has landed, so the
+  // first fragments of that are read under the last multiplications too.
+  constexpr int KK = kStep / 16;
+  bf16x8 a[2][MI], b[2][NI];
+  auto read = [&](int buf, int kk) {
     const char *rt = lds[buf];
     const char *ct = lds[buf] + Row::kBytes;
 #pragma unroll
-    for (int kk = 0; kk < kStep / 16; ++kk) {
-      bf16x8 a[MI], b[NI];
+    for (int j = 0; j < NI; ++j)
+      b[kk & 1][j] = Col::frag(ct, kPair ? j * (kTile / 2) + wn * 32
+                                         : wn * NI * 32 + j * 32, kk);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      a[kk & 1][i] = Row::frag(rt, wrow + i * 32, kk);
+  };
+  auto multiply = [&](int kk) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NI; ++j)
-        b[j] = Col::frag(ct, kPair ? j * (kTile / 2) + wn * 32
-                                   : wn * NI * 32 + j * 32, kk);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            b[kk & 1][j], a[kk & 1][i], acc[i][j], 0, 0, 0);
+  };
+  if (s0 < s1) {
+    issue(s0, 0);
+    arrive();
+    if (s0 + 1 < s1) issue(s0 + 1, 1);
+    read(0, 0);
+  }
+  for (int s = s0; s < s1; ++s) {
+    const int buf = (s - s0) & 1;
 #pragma unroll
-      for (int i = 0; i < MI; ++i) a[i] = Row::frag(rt, wrow + i * 32, kk);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              b[j], a[i], acc[i][j], 0, 0, 0);
+    for (int kk = 0; kk < KK - 1; ++kk) {
+      read(buf, kk + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(kk);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    arrive();
+    if (s + 2 < s1) issue(s + 2, buf);
+    read(buf ^ 1, 0);  // past the last step: what lies there, not used
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(KK - 1);
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // acc[i][j][4 q + e] of lane l is row l % 32 of block i, column
