@@ -111,20 +111,15 @@ struct Along {
                lane_piece() * 16;
   }
   // The step at k0; p: row row0 of the operand.
-  __device__ __forceinline__ void load(uint32_t lds, const bf16 *p, int pitch,
-                                       int k0, int K) const {
-    lds += wave_id() * 1024;
+  __device__ __forceinline__ void load(int i, uint32_t lds, const bf16 *p,
+                                       int pitch, int k0, int K) const {
+    lds += wave_id() * 1024 + i * WAVES * 1024;
     const char *base = (const char *)(p + k0);
-    if (k0 + kStep <= K) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        dma(lds + i * WAVES * 1024, base, off[i]);
-    } else {
-      const bool in = k0 + lane_piece() * 8 < K;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        dma_at(lds + i * WAVES * 1024, in ? base + off[i] : (const char *)&kZeros);
-    }
+    if (k0 + kStep <= K)
+      dma(lds, base, off[i]);
+    else
+      dma_at(lds, k0 + lane_piece() * 8 < K ? base + off[i]
+                                            : (const char *)&kZeros);
   }
   // Fragment of 32 rows from `row`, elements 16 * kk ...: lane l holds row
   // l % 32, elements 8 * (l / 32) + [0, 8).
@@ -161,22 +156,16 @@ struct Across {
           min(lane_piece() * 8, cols - 8 - col0) * 2;
   }
   // p: column col0 of the operand's row 0.
-  __device__ __forceinline__ void load(uint32_t lds, const bf16 *p, int pitch,
-                                       int k0, int K) const {
-    lds += wave_id() * 1024;
-    const char *base = (const char *)(p + (int64_t)k0 * pitch);
-    const int64_t next = (int64_t)kRows * pitch * 2;
-    if (k0 + kStep <= K) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        dma(lds + i * WAVES * 1024, base + i * next, off);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        dma_at(lds + i * WAVES * 1024, k0 + i * kRows + lane_row() < K
-                                           ? base + i * next + off
-                                           : (const char *)&kZeros);
-    }
+  __device__ __forceinline__ void load(int i, uint32_t lds, const bf16 *p,
+                                       int pitch, int k0, int K) const {
+    lds += wave_id() * 1024 + i * WAVES * 1024;
+    const char *base =
+        (const char *)(p + (int64_t)(k0 + i * kRows) * pitch);
+    if (k0 + kStep <= K)
+      dma(lds, base, off);
+    else
+      dma_at(lds, k0 + i * kRows + lane_row() < K ? base + off
+                                                  : (const char *)&kZeros);
   }
   static __device__ __forceinline__ bf16x8 frag(const char *tile, int col,
                                                 int kk) {
@@ -308,26 +297,34 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   Col col;
   row.start(row0, FORM == kDw ? F : M, FORM == kDx || FORM == kDw ? F : D);
   col.start(col0, kPair ? F : D, D);
-  auto issue = [&](int s, int buf) {
+  // One of the 8 loads of a step: 4 of the row operand, 4 of the other.
+  auto issue = [&](int n, int s, int buf) {
     const uint32_t at = lds0 + buf * kBuf;
+    const int i = n % 4;
     if constexpr (kPair) {
       const int k0 = s * kStep;
-      row.load(at, p.x + (int64_t)row0 * D, D, k0, D);
-      col.load(at + Row::kBytes, p.w[0] + (int64_t)col0 * D, D, k0, D);
-      col.load(at + Row::kBytes + Col::kBytes,
-               p.w[1] + (int64_t)col0 * D, D, k0, D);
+      if (n < 4)
+        row.load(i, at, p.x + (int64_t)row0 * D, D, k0, D);
+      else
+        col.load(i % 2, at + Row::kBytes + i / 2 * Col::kBytes,
+                 p.w[i / 2] + (int64_t)col0 * D, D, k0, D);
     } else if constexpr (FORM == kDx) {
       const int per = p.steps / 2;  // steps per plane
       const int pl = s >= per;
       const int k0 = (s - pl * per) * kStep;
-      row.load(at, p.dgu + ((int64_t)pl * M + row0) * F, F, k0, F);
-      col.load(at + Row::kBytes, p.w[pl] + col0, D, k0, F);
+      if (n < 4)
+        row.load(i, at, p.dgu + ((int64_t)pl * M + row0) * F, F, k0, F);
+      else
+        col.load(i, at + Row::kBytes, p.w[pl] + col0, D, k0, F);
     } else {
       const int k0 = s * kStep;
-      row.load(at, p.dgu + (int64_t)plane * M * F + row0, F, k0, M);
-      col.load(at + Row::kBytes, p.x + col0, D, k0, M);
+      if (n < 4)
+        row.load(i, at, p.dgu + (int64_t)plane * M * F + row0, F, k0, M);
+      else
+        col.load(i, at + Row::kBytes, p.x + col0, D, k0, M);
     }
   };
+  static_assert(Row::kLoads == 4 && Col::kLoads == (kPair ? 2 : 4), "");
 
   const int wave = wave_id();
   const int wm = wave / kWn, wn = wave % kWn;
@@ -358,18 +355,22 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
     for (int i = 0; i < MI; ++i)
       a[kk & 1][i] = Row::frag(rt, wrow + i * 32, kk);
   };
-  auto multiply = [&](int kk) {
+  auto multiply = [&](int kk, int i0, int i1) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = i0; i < i1; ++i)
 #pragma unroll
       for (int j = 0; j < NI; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             b[kk & 1][j], a[kk & 1][i], acc[i][j], 0, 0, 0);
   };
   if (s0 < s1) {
-    issue(s0, 0);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) issue(n, s0, 0);
     arrive();
-    if (s0 + 1 < s1) issue(s0 + 1, 1);
+    if (s0 + 1 < s1) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n) issue(n, s0 + 1, 1);
+    }
     read(0, 0);
   }
   for (int s = s0; s < s1; ++s) {
@@ -378,15 +379,24 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
     for (int kk = 0; kk < KK - 1; ++kk) {
       read(buf, kk + 1);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(kk);
+      multiply(kk, 0, MI);
       __builtin_amdgcn_sched_barrier(0);
     }
     arrive();
-    if (s + 2 < s1) issue(s + 2, buf);
     read(buf ^ 1, 0);  // past the last step: what lies there, not used
     __builtin_amdgcn_sched_barrier(0);
-    multiply(KK - 1);
-    __builtin_amdgcn_sched_barrier(0);
+    const bool more = s + 2 < s1;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      multiply(KK - 1, i, i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) {
+#pragma unroll
+        for (int n = i * 8 / MI; n < (i + 1) * 8 / MI; ++n)
+          issue(n, s + 2, buf);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   // acc[i][j][4 q + e] of lane l is row l % 32 of block i, column
