@@ -110,16 +110,17 @@ struct Along {
                    (uint32_t)pitch * 2 +
                lane_piece() * 16;
   }
-  // The step at k0; p: row row0 of the operand.
-  __device__ __forceinline__ void load(int i, uint32_t lds, const bf16 *p,
-                                       int pitch, int k0, int K) const {
-    lds += wave_id() * 1024 + i * WAVES * 1024;
-    const char *base = (const char *)(p + k0);
-    if (k0 + kStep <= K)
-      dma(lds, base, off[i]);
-    else
-      dma_at(lds, k0 + lane_piece() * 8 < K ? base + off[i]
-                                            : (const char *)&kZeros);
+  // Load i of a whole step; base: the operand at row row0, element k0.
+  __device__ __forceinline__ void load(int i, uint32_t lds, const char *base,
+                                       int64_t pitch2) const {
+    dma(lds + (wave_id() + i * WAVES) * 1024, base, off[i]);
+  }
+  // The same where only `left` < kStep elements are left of the sum.
+  __device__ __forceinline__ void load_tail(int i, uint32_t lds,
+                                            const char *base, int64_t pitch2,
+                                            int left) const {
+    dma_at(lds + (wave_id() + i * WAVES) * 1024,
+           lane_piece() * 8 < left ? base + off[i] : (const char *)&kZeros);
   }
   // Fragment of 32 rows from `row`, elements 16 * kk ...: lane l holds row
   // l % 32, elements 8 * (l / 32) + [0, 8).
@@ -155,17 +156,17 @@ struct Across {
     off = (uint32_t)lane_row() * (uint32_t)pitch * 2 +
           min(lane_piece() * 8, cols - 8 - col0) * 2;
   }
-  // p: column col0 of the operand's row 0.
-  __device__ __forceinline__ void load(int i, uint32_t lds, const bf16 *p,
-                                       int pitch, int k0, int K) const {
-    lds += wave_id() * 1024 + i * WAVES * 1024;
-    const char *base =
-        (const char *)(p + (int64_t)(k0 + i * kRows) * pitch);
-    if (k0 + kStep <= K)
-      dma(lds, base, off);
-    else
-      dma_at(lds, k0 + i * kRows + lane_row() < K ? base + off
-                                                  : (const char *)&kZeros);
+  // base: the operand at row k0, column col0; pitch2: bytes per row.
+  __device__ __forceinline__ void load(int i, uint32_t lds, const char *base,
+                                       int64_t pitch2) const {
+    dma(lds + (wave_id() + i * WAVES) * 1024, base + i * kRows * pitch2, off);
+  }
+  __device__ __forceinline__ void load_tail(int i, uint32_t lds,
+                                            const char *base, int64_t pitch2,
+                                            int left) const {
+    dma_at(lds + (wave_id() + i * WAVES) * 1024,
+           i * kRows + lane_row() < left ? base + i * kRows * pitch2 + off
+                                         : (const char *)&kZeros);
   }
   static __device__ __forceinline__ bf16x8 frag(const char *tile, int col,
                                                 int kk) {
@@ -297,34 +298,64 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   Col col;
   row.start(row0, FORM == kDw ? F : M, FORM == kDx || FORM == kDw ? F : D);
   col.start(col0, kPair ? F : D, D);
-  // One of the 8 loads of a step: 4 of the row operand, 4 of the other.
-  auto issue = [&](int n, int s, int buf) {
-    const uint32_t at = lds0 + buf * kBuf;
-    const int i = n % 4;
+  // The operands of the step to be loaded next (of a pair: x, Wg, Wu), and
+  // how far apart two steps are.
+  const char *pr, *pc, *pu = nullptr;
+  const int64_t pitch_r = 2 * (int64_t)(kPair ? D : F), pitch_c = 2 * (int64_t)D;
+  const int64_t next_r = FORM == kDw ? kStep * pitch_r : 2 * kStep;
+  const int64_t next_c = kPair ? 2 * kStep : kStep * pitch_c;
+  const int K = kPair ? D : FORM == kDx ? F : M;
+  const int per = FORM == kDx ? p.steps / 2 : p.steps;  // steps per plane
+  auto seek = [&](int s) {
+    const int pl = FORM == kDx ? s >= per : 0;
+    const int64_t k = s - pl * per;
     if constexpr (kPair) {
-      const int k0 = s * kStep;
-      if (n < 4)
-        row.load(i, at, p.x + (int64_t)row0 * D, D, k0, D);
-      else
-        col.load(i % 2, at + Row::kBytes + i / 2 * Col::kBytes,
-                 p.w[i / 2] + (int64_t)col0 * D, D, k0, D);
+      pr = (const char *)(p.x + (int64_t)row0 * D) + k * next_r;
+      pc = (const char *)(p.w[0] + (int64_t)col0 * D) + k * next_c;
+      pu = (const char *)(p.w[1] + (int64_t)col0 * D) + k * next_c;
     } else if constexpr (FORM == kDx) {
-      const int per = p.steps / 2;  // steps per plane
-      const int pl = s >= per;
-      const int k0 = (s - pl * per) * kStep;
-      if (n < 4)
-        row.load(i, at, p.dgu + ((int64_t)pl * M + row0) * F, F, k0, F);
-      else
-        col.load(i, at + Row::kBytes, p.w[pl] + col0, D, k0, F);
+      pr = (const char *)(p.dgu + ((int64_t)pl * M + row0) * F) + k * next_r;
+      pc = (const char *)(p.w[pl] + col0) + k * next_c;
     } else {
-      const int k0 = s * kStep;
-      if (n < 4)
-        row.load(i, at, p.dgu + (int64_t)plane * M * F + row0, F, k0, M);
-      else
-        col.load(i, at + Row::kBytes, p.x + col0, D, k0, M);
+      pr = (const char *)(p.dgu + (int64_t)plane * M * F + row0) + k * next_r;
+      pc = (const char *)(p.x + col0) + k * next_c;
     }
   };
-  static_assert(Row::kLoads == 4 && Col::kLoads == (kPair ? 2 : 4), "");
+  // Load n of the 8 (4 of each operand) of that step, into a buffer.
+  constexpr int kLoads = Row::kLoads + (kPair ? 2 : 1) * Col::kLoads;
+  auto load = [&](int n, int buf) {
+    const uint32_t at = lds0 + buf * kBuf;
+    if (n < Row::kLoads)
+      row.load(n, at, pr, pitch_r);
+    else if (n < Row::kLoads + Col::kLoads)
+      col.load(n - Row::kLoads, at + Row::kBytes, pc, pitch_c);
+    else
+      col.load(n - Row::kLoads - Col::kLoads,
+               at + Row::kBytes + Col::kBytes, pu, pitch_c);
+  };
+  auto load_tail = [&](int left, int buf) {
+    const uint32_t at = lds0 + buf * kBuf;
+#pragma unroll
+    for (int i = 0; i < Row::kLoads; ++i)
+      row.load_tail(i, at, pr, pitch_r, left);
+#pragma unroll
+    for (int i = 0; i < Col::kLoads; ++i) {
+      col.load_tail(i, at + Row::kBytes, pc, pitch_c, left);
+      if constexpr (kPair)
+        col.load_tail(i, at + Row::kBytes + Col::kBytes, pu, pitch_c, left);
+    }
+  };
+  // Elements of the sum that step s has left, of its plane.
+  auto left = [&](int s) {
+    return K - (FORM == kDx && s >= per ? s - per : s) * kStep;
+  };
+  auto advance = [&](int s) {  // from step s to the one after it
+    pr += next_r;
+    pc += next_c;
+    if constexpr (kPair) pu += next_c;
+    if constexpr (FORM == kDx)
+      if (s + 1 == per) seek(per);
+  };
 
   const int wave = wave_id();
   const int wm = wave / kWn, wn = wave % kWn;
@@ -364,12 +395,16 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
             b[kk & 1][j], a[kk & 1][i], acc[i][j], 0, 0, 0);
   };
   if (s0 < s1) {
+    seek(s0);
+    for (int s = s0; s < min(s0 + 2, s1); ++s) {
+      if (left(s) >= kStep) {
 #pragma unroll
-    for (int n = 0; n < 8; ++n) issue(n, s0, 0);
-    arrive();
-    if (s0 + 1 < s1) {
-#pragma unroll
-      for (int n = 0; n < 8; ++n) issue(n, s0 + 1, 1);
+        for (int n = 0; n < kLoads; ++n) load(n, s - s0);
+      } else {
+        load_tail(left(s), s - s0);
+      }
+      advance(s);
+      if (s == s0) arrive();
     }
     read(0, 0);
   }
@@ -386,16 +421,21 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
     read(buf ^ 1, 0);  // past the last step: what lies there, not used
     __builtin_amdgcn_sched_barrier(0);
     const bool more = s + 2 < s1;
+    const bool whole = more && left(s + 2) >= kStep;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       multiply(KK - 1, i, i + 1);
       __builtin_amdgcn_sched_barrier(0);
-      if (more) {
+      if (whole) {
 #pragma unroll
-        for (int n = i * 8 / MI; n < (i + 1) * 8 / MI; ++n)
-          issue(n, s + 2, buf);
+        for (int n = i * kLoads / MI; n < (i + 1) * kLoads / MI; ++n)
+          load(n, buf);
       }
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if (more) {
+      if (!whole) load_tail(left(s + 2), buf);
+      advance(s + 2);
     }
   }
 
