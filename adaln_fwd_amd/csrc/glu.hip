@@ -47,13 +47,9 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kStep = 64;  // summed elements per step
 
-// What lanes past an operand's end load instead: 16 zero bytes.
-__device__ const uint4 kZeros = {0, 0, 0, 0};
-
-// 16 bytes per lane from memory to LDS at `lds` + 16 * lane.  Two forms: a
-// wave-uniform base with a 32-bit offset per lane, or an address per lane.
-// The count of outstanding loads is waited for by arrive() below, by hand:
-// the compiler does not see these loads.  (m0 takes the LDS address; nothing
+// 16 bytes per lane from memory to LDS at `lds` + 16 * lane: a wave-uniform
+// base and a 32-bit offset per lane.  Outstanding loads are waited for by
+// arrive() below, by hand: the compiler does not see these loads.  (m0 takes the LDS address; nothing
 // else in these kernels uses it.  The s_nop is the wait state that the ISA
 // asks for between writing m0 and a load to LDS.)
 __device__ __forceinline__ void dma(uint32_t lds, const void *base,
@@ -64,16 +60,6 @@ __device__ __forceinline__ void dma(uint32_t lds, const void *base,
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(offset), "s"(base)
-      : "memory");
-}
-
-__device__ __forceinline__ void dma_at(uint32_t lds, const void *p) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %1, off"
-      :
-      : "s"(lds), "v"(p)
       : "memory");
 }
 
@@ -88,13 +74,15 @@ __device__ __forceinline__ void arrive() {
 // An operand whose summed dimension is contiguous: ROWS rows of kStep
 // elements, 128 bytes each, 8 pieces of 16.  Row r keeps its piece c at
 // c ^ ((r >> 1) & 7): 16 consecutive rows then cover all banks.  Rows past
-// the operand's last repeat it (their products are not stored); elements past
-// the end of the sum are loaded as zeros.
+// the operand's last repeat it (their products are not stored); past the end
+// of the sum, `left` elements into the step, a lane loads the last piece
+// again, and clear() puts zeros in its place.
 template <int ROWS, int WAVES>
 struct Along {
   static constexpr int kBytes = ROWS * kStep * 2;
   static constexpr int kLoads = ROWS / (8 * WAVES);
-  uint32_t off[kLoads];  // byte offsets of the lane's loads from the base
+  static constexpr int kReads = 1;  // LDS reads per fragment
+  uint32_t off[kLoads];             // byte offset of each load's row
 
   static __device__ __forceinline__ int lane_row() {
     return wave_id() * 8 + lane_id() / 8;
@@ -107,20 +95,21 @@ struct Along {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       off[i] = (uint32_t)min(i * 8 * WAVES + lane_row(), rows - 1 - row0) *
-                   (uint32_t)pitch * 2 +
-               lane_piece() * 16;
+               (uint32_t)pitch * 2;
   }
-  // Load i of a whole step; base: the operand at row row0, element k0.
+  // Load i of a step; base: the operand at row row0, element k0.
   __device__ __forceinline__ void load(int i, uint32_t lds, const char *base,
-                                       int64_t pitch2) const {
-    dma(lds + (wave_id() + i * WAVES) * 1024, base, off[i]);
+                                       uint32_t pitch2, int left) const {
+    dma(lds + (wave_id() + i * WAVES) * 1024, base,
+        off[i] + min(lane_piece() * 16, (left - 8) * 2));
   }
-  // The same where only `left` < kStep elements are left of the sum.
-  __device__ __forceinline__ void load_tail(int i, uint32_t lds,
-                                            const char *base, int64_t pitch2,
-                                            int left) const {
-    dma_at(lds + (wave_id() + i * WAVES) * 1024,
-           lane_piece() * 8 < left ? base + off[i] : (const char *)&kZeros);
+  static __device__ __forceinline__ void clear(char *tile, int left) {
+    if (lane_piece() * 8 >= left) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        store_vec(tile + (wave_id() + i * WAVES) * 1024 + lane_id() * 16,
+                  vzero());
+    }
   }
   // Fragment of 32 rows from `row`, elements 16 * kk ...: lane l holds row
   // l % 32, elements 8 * (l / 32) + [0, 8).
@@ -137,14 +126,16 @@ struct Along {
 // An operand stored across the summed dimension: kStep rows of COLS columns,
 // COLS / 8 pieces of 16 bytes; row k keeps its piece c at c ^ ((k & 3) << 2),
 // so that the four rows that a transposing read takes lie in distinct banks.
-// Columns past the last repeat the last eight.
+// Columns past the last repeat the last eight; rows past the end of the sum
+// repeat the last, and are cleared.
 template <int COLS, int WAVES>
 struct Across {
   static constexpr int kBytes = COLS * kStep * 2;
   static constexpr int kPieces = COLS / 8;
   static constexpr int kRows = 64 / kPieces * WAVES;  // rows per load
   static constexpr int kLoads = kStep / kRows;
-  uint32_t off;
+  static constexpr int kReads = 2;
+  uint32_t off;  // byte offset of the lane's columns
 
   static __device__ __forceinline__ int lane_row() {
     return (wave_id() * 64 + lane_id()) / kPieces;
@@ -153,20 +144,20 @@ struct Across {
     return (lane_id() % kPieces) ^ ((lane_row() & 3) << 2);
   }
   __device__ __forceinline__ void start(int col0, int cols, int pitch) {
-    off = (uint32_t)lane_row() * (uint32_t)pitch * 2 +
-          min(lane_piece() * 8, cols - 8 - col0) * 2;
+    off = (uint32_t)min(lane_piece() * 8, cols - 8 - col0) * 2;
   }
   // base: the operand at row k0, column col0; pitch2: bytes per row.
   __device__ __forceinline__ void load(int i, uint32_t lds, const char *base,
-                                       int64_t pitch2) const {
-    dma(lds + (wave_id() + i * WAVES) * 1024, base + i * kRows * pitch2, off);
+                                       uint32_t pitch2, int left) const {
+    dma(lds + (wave_id() + i * WAVES) * 1024, base,
+        off + (uint32_t)min(i * kRows + lane_row(), left - 1) * pitch2);
   }
-  __device__ __forceinline__ void load_tail(int i, uint32_t lds,
-                                            const char *base, int64_t pitch2,
-                                            int left) const {
-    dma_at(lds + (wave_id() + i * WAVES) * 1024,
-           i * kRows + lane_row() < left ? base + i * kRows * pitch2 + off
-                                         : (const char *)&kZeros);
+  static __device__ __forceinline__ void clear(char *tile, int left) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (i * kRows + lane_row() >= left)
+        store_vec(tile + (wave_id() + i * WAVES) * 1024 + lane_id() * 16,
+                  vzero());
   }
   static __device__ __forceinline__ bf16x8 frag(const char *tile, int col,
                                                 int kk) {
@@ -188,20 +179,28 @@ struct Across {
 
 enum { kSilu = 0, kGeluTanh = 1 };
 
+// 4 / (1 + exp(-v)).  The hardware's reciprocal (one unit in the last place
+// of float32, before results are rounded to bfloat16; a correctly rounded
+// quotient takes ten instructions more per element) gives zero for quotients
+// below 2^-126: a quarter of 1 + exp(-v) has none.
+__device__ __forceinline__ float logistic4(float v) {
+  return __builtin_amdgcn_rcpf(fmaf(__expf(-v), 0.25f, 0.25f));
+}
+
 // act(g) and act'(g).  Both are g times a logistic function s, of g or of
 // twice the tanh form's polynomial v: (1 + tanh(v)) / 2 = 1 / (1 + exp(-2v))
 // keeps its digits where 1 + tanh(v) cancels, and both ends saturate.
 template <int ACT>
 __device__ __forceinline__ void activate(float g, float &a, float &da) {
   if constexpr (ACT == kSilu) {
-    const float s = 1.f / (1.f + __expf(-g));
-    a = g * s;
+    const float s4 = logistic4(g), s = 0.25f * s4;
+    a = 0.25f * g * s4;
     da = s * (1.f + g * (1.f - s));
   } else {
     constexpr float c = 0.7978845608028654f, e = 0.044715f;
     const float g2 = g * g;
-    const float s = 1.f / (1.f + __expf(-2.f * c * g * (1.f + e * g2)));
-    a = g * s;
+    const float s4 = logistic4(2.f * c * g * (1.f + e * g2)), s = 0.25f * s4;
+    a = 0.25f * g * s4;
     da = s + 2.f * g * s * (1.f - s) * c * (1.f + 3.f * e * g2);
   }
 }
@@ -212,6 +211,60 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
   u.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2));
   u.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2));
   return u;
+}
+
+__device__ __forceinline__ bf16 round_bf16(float f) {
+  const f32x2 v = {f, f};
+  const uint32_t w =
+      __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  return bf16{(uint16_t)w};
+}
+
+// ------------------------------------------------------- storing a block
+
+// A 32 x 32 block as the matrix cores leave it (lane l: row l % 32, columns
+// 8 q + 4 (l / 32) + e in register 4 q + e) to memory, in row order: through
+// LDS of the wavefront's own, so that 8 lanes write a whole 128-byte line
+// (float32) or 4 lanes half of one (bf16) at a time instead of 32 lanes 32
+// pieces of lines.  The rows' pitch keeps both sides free of bank conflicts.
+// n_r, n_c: rows and columns of the block that exist.  Forward of 24960 x
+// 1536 -> 4096 with G and U saved, on MI355X: 952 -> 673 us.
+constexpr int kStageBytes = 32 * (32 * 4 + 16);
+
+__device__ __forceinline__ void store_block(char *stage, const f32x16 &v,
+                                            float *out, int64_t pitch, int n_r,
+                                            int n_c) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f32x4 f = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    *reinterpret_cast<f32x4 *>(stage + (lane % 32) * 144 +
+                               (8 * q + 4 * (lane / 32)) * 4) = f;
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int r = t * 8 + lane / 8, c = lane % 8 * 4;
+    const Vec f = load_vec(stage + r * 144 + c * 4);
+    if (r < n_r && c < n_c) store_stream(out + r * pitch + c, f);
+  }
+}
+
+__device__ __forceinline__ void store_block(char *stage, const f32x16 &v,
+                                            bf16 *out, int64_t pitch, int n_r,
+                                            int n_c) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float f[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    *reinterpret_cast<uint2 *>(stage + (lane % 32) * 80 +
+                               (8 * q + 4 * (lane / 32)) * 2) = pack4(f);
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int r = t * 16 + lane / 4, c = lane % 4 * 8;
+    const Vec f = load_vec(stage + r * 80 + c * 2);
+    if (r < n_r && c < n_c) store_vec(out + r * pitch + c, f);
+  }
 }
 
 // ------------------------------------------------------------- the products
@@ -231,21 +284,28 @@ struct Product {
   const bf16 *dh;         // [M, F]
   bf16 *dgu;              // dG, dU [2, M, F]
   bf16 *out[2];           // dx, or dWg and dWu
-  float *part;            // partial sums [slices, 2 or 1, rows, cols], or NULL
+  float *part;            // partial tiles [slices, rem, tile, tile]
   int32_t M, D, F;
-  int32_t tiles_r, tiles_c;
-  int32_t slices, steps_per_slice, steps;
+  int32_t tiles_r, tiles_c;  // of a plane
+  int32_t steps;
+  int32_t full, rem;         // tiles computed whole, and those that follow,
+  int32_t slices, per_slice; // in so many slices of so many steps
   int32_t block0;         // first block of this launch
 };
 
-// Tile of the calling workgroup.  Workgroups go to the eight XCDs in turn;
-// this gives each XCD a contiguous run of tiles, and orders the run in bands
-// of 8 tile rows, so that the tiles that run together share operands in the
-// XCD's L2.
-__device__ __forceinline__ void tile_of(int id, int total, int tiles_r,
-                                        int tiles_c, int &tr, int &tc) {
+// Workgroups go to the eight XCDs in turn: item `id` of `total` in an order
+// that gives each XCD a contiguous run of items.
+__device__ __forceinline__ int xcd_run(int id, int total) {
   const int per = total / 8;
-  const int n = id < per * 8 ? (id % 8) * per + id / 8 : id;
+  return id < per * 8 ? (id % 8) * per + id / 8 : id;
+}
+
+// Tile n of the plan: its plane, row and column.  In bands of 8 tile rows, so
+// that tiles that run together share operands in an XCD's L2.
+__device__ __forceinline__ void tile_of(int n, int tiles_r, int tiles_c,
+                                        int &plane, int &tr, int &tc) {
+  plane = n / (tiles_r * tiles_c);
+  n -= plane * tiles_r * tiles_c;
   constexpr int kBand = 8;
   const int band = n / (kBand * tiles_c);
   const int in = n - band * kBand * tiles_c;
@@ -258,16 +318,16 @@ __device__ __forceinline__ void tile_of(int id, int total, int tiles_r,
 // by 4 (2 x 2, each 64 x 64).  Columns of kHidden and kGrads: half of them of
 // G, half the same ones of U, so that a lane holds both of an element.
 template <int FORM, bool BIG, int ACT>
-__global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
+__global__ __launch_bounds__(BIG ? 512 : 256, 2) void product_kernel(
     Product p) {
   constexpr int kWaves = BIG ? 8 : 4;
   constexpr int kTile = BIG ? 256 : 128;
-  constexpr int kWn = BIG ? 4 : 2;          // wavefronts across the columns
+  constexpr int kWn = kWaves / 2;          // wavefronts across the columns
   constexpr int MI = kTile / 2 / 32;        // 32-row blocks of a wavefront
   constexpr int NI = kTile / kWn / 32;      // 32-column blocks
   constexpr bool kPair = FORM == kHidden || FORM == kGrads;
   constexpr int kCols = kPair ? kTile / 2 : kTile;
-  static_assert(!kPair || NI == 2, "a block of G and one of U");
+  constexpr int NP = NI / 2;  // of a pair: blocks of G, then as many of U
   using Row = std::conditional_t<FORM == kDw, Across<kTile, kWaves>,
                                  Along<kTile, kWaves>>;
   // (of a pair, the rows of one weight)
@@ -277,21 +337,23 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   constexpr uint32_t kBuf = Row::kBytes + kColBytes;
   __shared__ __align__(1024) char lds[2][kBuf];
 
-  int id = blockIdx.x + p.block0;
-  const int tiles = p.tiles_r * p.tiles_c;
-  const int slice = id / tiles;  // slices, then planes, outermost
-  id -= slice * tiles;
-  int tr, tc;
-  tile_of(id, tiles, p.tiles_r, p.tiles_c, tr, tc);
-  int plane = 0, split = slice;
-  if constexpr (FORM == kDw) {
-    plane = slice & 1;
-    split = slice >> 1;
+  // The first `full` blocks compute a tile each; the rest, slices of the
+  // sums of the last `rem` tiles.
+  const int id = blockIdx.x + p.block0;
+  int n, split = 0;
+  if (id < p.full) {
+    n = xcd_run(id, p.full);
+  } else {
+    split = (id - p.full) / p.rem;
+    n = p.full + xcd_run(id - p.full - split * p.rem, p.rem);
   }
+  const bool partial = id >= p.full && p.slices > 1;
+  int plane, tr, tc;
+  tile_of(n, p.tiles_r, p.tiles_c, plane, tr, tc);
   const int row0 = tr * kTile, col0 = tc * kCols;
   const int M = p.M, D = p.D, F = p.F;
-  const int s0 = split * p.steps_per_slice;
-  const int s1 = min(s0 + p.steps_per_slice, p.steps);
+  const int s0 = partial ? split * p.per_slice : 0;
+  const int s1 = partial ? min(s0 + p.per_slice, p.steps) : p.steps;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)&lds[0][0];
 
   Row row;
@@ -301,9 +363,10 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   // The operands of the step to be loaded next (of a pair: x, Wg, Wu), and
   // how far apart two steps are.
   const char *pr, *pc, *pu = nullptr;
-  const int64_t pitch_r = 2 * (int64_t)(kPair ? D : F), pitch_c = 2 * (int64_t)D;
-  const int64_t next_r = FORM == kDw ? kStep * pitch_r : 2 * kStep;
-  const int64_t next_c = kPair ? 2 * kStep : kStep * pitch_c;
+  const uint32_t pitch_r = 2 * (uint32_t)(kPair ? D : F);
+  const uint32_t pitch_c = 2 * (uint32_t)D;
+  const int64_t next_r = FORM == kDw ? kStep * (int64_t)pitch_r : 2 * kStep;
+  const int64_t next_c = kPair ? 2 * kStep : kStep * (int64_t)pitch_c;
   const int K = kPair ? D : FORM == kDx ? F : M;
   const int per = FORM == kDx ? p.steps / 2 : p.steps;  // steps per plane
   auto seek = [&](int s) {
@@ -321,40 +384,44 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
       pc = (const char *)(p.x + col0) + k * next_c;
     }
   };
-  // Load n of the 8 (4 of each operand) of that step, into a buffer.
-  constexpr int kLoads = Row::kLoads + (kPair ? 2 : 1) * Col::kLoads;
-  auto load = [&](int n, int buf) {
-    const uint32_t at = lds0 + buf * kBuf;
-    if (n < Row::kLoads)
-      row.load(n, at, pr, pitch_r);
-    else if (n < Row::kLoads + Col::kLoads)
-      col.load(n - Row::kLoads, at + Row::kBytes, pc, pitch_c);
-    else
-      col.load(n - Row::kLoads - Col::kLoads,
-               at + Row::kBytes + Col::kBytes, pu, pitch_c);
-  };
-  auto load_tail = [&](int left, int buf) {
-    const uint32_t at = lds0 + buf * kBuf;
-#pragma unroll
-    for (int i = 0; i < Row::kLoads; ++i)
-      row.load_tail(i, at, pr, pitch_r, left);
-#pragma unroll
-    for (int i = 0; i < Col::kLoads; ++i) {
-      col.load_tail(i, at + Row::kBytes, pc, pitch_c, left);
-      if constexpr (kPair)
-        col.load_tail(i, at + Row::kBytes + Col::kBytes, pu, pitch_c, left);
-    }
-  };
   // Elements of the sum that step s has left, of its plane.
   auto left = [&](int s) {
     return K - (FORM == kDx && s >= per ? s - per : s) * kStep;
   };
-  auto advance = [&](int s) {  // from step s to the one after it
-    pr += next_r;
-    pc += next_c;
-    if constexpr (kPair) pu += next_c;
-    if constexpr (FORM == kDx)
-      if (s + 1 == per) seek(per);
+  // On to step s, the one after the last loaded; past the end, the last step
+  // is loaded again, into a buffer that nobody reads any more.
+  int pl_left = 0;
+  auto advance = [&](int s) {
+    if (s < s1) {
+      pr += next_r;
+      pc += next_c;
+      if constexpr (kPair) pu += next_c;
+      if constexpr (FORM == kDx)
+        if (s == per) seek(per);
+      pl_left = left(s);
+    }
+  };
+  // Load n of that step, into a buffer.
+  constexpr int kLoads = Row::kLoads + (kPair ? 2 : 1) * Col::kLoads;
+  auto load = [&](int n, int buf) {
+    const uint32_t at = lds0 + buf * kBuf;
+    if (n < Row::kLoads)
+      row.load(n, at, pr, pitch_r, pl_left);
+    else if (n < Row::kLoads + Col::kLoads)
+      col.load(n - Row::kLoads, at + Row::kBytes, pc, pitch_c, pl_left);
+    else
+      col.load(n - Row::kLoads - Col::kLoads,
+               at + Row::kBytes + Col::kBytes, pu, pitch_c, pl_left);
+  };
+  // Zeros past the end of the sum in the tile of step s, which has landed.
+  auto clear = [&](int s, int buf) {
+    if (s < s1 && left(s) < kStep) {
+      Row::clear(lds[buf], left(s));
+      Col::clear(lds[buf] + Row::kBytes, left(s));
+      if constexpr (kPair)
+        Col::clear(lds[buf] + Row::kBytes + Col::kBytes, left(s));
+      __syncthreads();
+    }
   };
 
   const int wave = wave_id();
@@ -375,142 +442,135 @@ __global__ __launch_bounds__(BIG ? 512 : 256, BIG ? 2 : 2) void product_kernel(
   // first fragments of that are read under the last multiplications too.
   constexpr int KK = kStep / 16;
   bf16x8 a[2][MI], b[2][NI];
-  auto read = [&](int buf, int kk) {
+  // Fragment n of the NI + MI of sub-step kk.
+  auto read = [&](int n, int buf, int kk) {
     const char *rt = lds[buf];
     const char *ct = lds[buf] + Row::kBytes;
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-      b[kk & 1][j] = Col::frag(ct, kPair ? j * (kTile / 2) + wn * 32
-                                         : wn * NI * 32 + j * 32, kk);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-      a[kk & 1][i] = Row::frag(rt, wrow + i * 32, kk);
+    if (n < NI)
+      b[kk & 1][n] = Col::frag(
+          ct,
+          kPair ? n / NP * (kTile / 2) + wn * NP * 32 + n % NP * 32
+                : wn * NI * 32 + n * 32,
+          kk);
+    else
+      a[kk & 1][n - NI] = Row::frag(rt, wrow + (n - NI) * 32, kk);
   };
-  auto multiply = [&](int kk, int i0, int i1) {
-#pragma unroll
-    for (int i = i0; i < i1; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            b[kk & 1][j], a[kk & 1][i], acc[i][j], 0, 0, 0);
+  constexpr int kMul = MI * NI;
+  constexpr int kFirst = kLoads / 2;
+  auto multiply = [&](int n, int kk) {
+    const int i = n / NI, j = n % NI;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        b[kk & 1][j], a[kk & 1][i], acc[i][j], 0, 0, 0);
   };
   if (s0 < s1) {
     seek(s0);
-    for (int s = s0; s < min(s0 + 2, s1); ++s) {
-      if (left(s) >= kStep) {
+    pl_left = left(s0);
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n) load(n, s - s0);
-      } else {
-        load_tail(left(s), s - s0);
-      }
-      advance(s);
-      if (s == s0) arrive();
-    }
-    read(0, 0);
+    for (int n = 0; n < kLoads; ++n) load(n, 0);
+    arrive();
+    advance(s0 + 1);
+#pragma unroll
+    for (int n = 0; n < kFirst; ++n) load(n, 1);
+    clear(s0, 0);
+#pragma unroll
+    for (int n = 0; n < NI + MI; ++n) read(n, 0, 0);
   }
   for (int s = s0; s < s1; ++s) {
     const int buf = (s - s0) & 1;
 #pragma unroll
     for (int kk = 0; kk < KK - 1; ++kk) {
-      read(buf, kk + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(kk, 0, MI);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < kMul; ++n) {
+        multiply(n, kk);
+        if (n < NI + MI) read(n, buf, kk + 1);
+        if (kk == 0) {
+#pragma unroll
+          for (int l = kFirst + n * (kLoads - kFirst) / kMul;
+               l < kFirst + (n + 1) * (kLoads - kFirst) / kMul; ++l)
+            load(l, buf ^ 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     arrive();
-    read(buf ^ 1, 0);  // past the last step: what lies there, not used
-    __builtin_amdgcn_sched_barrier(0);
-    const bool more = s + 2 < s1;
-    const bool whole = more && left(s + 2) >= kStep;
+    clear(s + 1, buf ^ 1);
+    advance(s + 2);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      multiply(KK - 1, i, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      if (whole) {
+    for (int n = 0; n < kMul; ++n) {
+      multiply(n, KK - 1);
+      // (past the last step: what lies there, not used)
+      if (n < NI + MI) read(n, buf ^ 1, 0);
 #pragma unroll
-        for (int n = i * kLoads / MI; n < (i + 1) * kLoads / MI; ++n)
-          load(n, buf);
-      }
+      for (int l = n * kFirst / kMul; l < (n + 1) * kFirst / kMul; ++l)
+        load(l, buf);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    if (more) {
-      if (!whole) load_tail(left(s + 2), buf);
-      advance(s + 2);
     }
   }
+  arrive();  // LDS is free: nothing on its way in, nobody reading
 
   // acc[i][j][4 q + e] of lane l is row l % 32 of block i, column
-  // 8 q + 4 (l / 32) + e of block j: four neighbouring columns per store.
+  // 8 q + 4 (l / 32) + e of block j.
+  char *stage = &lds[0][0] + wave * kStageBytes;
+  static_assert(kWaves * kStageBytes <= sizeof lds, "");
   const int lane = lane_id();
+  const int rows = FORM == kDw ? F : M, cols = kPair ? F : D;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int r = row0 + wrow + i * 32 + lane % 32;
-    const int rows = FORM == kDw ? F : M;
-    if (r >= rows) continue;
-    if constexpr (kPair) {
+    const int r = row0 + wrow + i * 32;
+    if (r >= rows) break;
+    const int n_r = rows - r;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = col0 + wn * 32 + 8 * q + 4 * (lane / 32);
-        if (c >= F) continue;
-        const int64_t at = (int64_t)r * F + c;
-        const int64_t plane_size = (int64_t)M * F;
-        float v0[4], v1[4];
+    for (int j = 0; j < (kPair ? NP : NI); ++j) {
+      const int c = col0 + (wn * (kPair ? NP : NI) + j) * 32;
+      if (c >= cols) break;
+      const int n_c = cols - c;
+      const int64_t at = (int64_t)r * cols + c;
+      const int64_t plane_size = (int64_t)M * F;
+      if constexpr (kPair) {
+        const f32x16 g = acc[i][j], u = acc[i][NP + j];
+        f32x16 v0, v1;
         if constexpr (FORM == kHidden) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 16; ++e) {
             float a, da;
-            activate<ACT>(acc[i][0][4 * q + e], a, da);
-            v0[e] = a * acc[i][1][4 * q + e];
+            activate<ACT>(g[e], a, da);
+            v0[e] = a * u[e];
           }
-          *reinterpret_cast<uint2 *>(p.h + at) = pack4(v0);
+          store_block(stage, v0, p.h + at, cols, n_r, n_c);
           if (p.gu != nullptr) {
-            f32x4 g, u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              g[e] = acc[i][0][4 * q + e];
-              u[e] = acc[i][1][4 * q + e];
-            }
-            *reinterpret_cast<f32x4 *>(p.gu + at) = g;
-            *reinterpret_cast<f32x4 *>(p.gu + plane_size + at) = u;
+            store_block(stage, g, p.gu + at, cols, n_r, n_c);
+            store_block(stage, u, p.gu + plane_size + at, cols, n_r, n_c);
           }
         } else {
-          const uint2 d = *reinterpret_cast<const uint2 *>(p.dh + at);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t w = e < 2 ? d.x : d.y;
-            const float dh = __builtin_bit_cast(
-                float, (e & 1) ? (w & 0xffff0000u) : (w << 16));
-            float a, da;
-            activate<ACT>(acc[i][0][4 * q + e], a, da);
-            v0[e] = dh * acc[i][1][4 * q + e] * da;
-            v1[e] = dh * a;
+          for (int q = 0; q < 4; ++q) {
+            const int mine = 8 * q + 4 * (lane / 32);
+            uint2 d = {0, 0};
+            if (lane % 32 < n_r && mine < n_c)
+              d = *reinterpret_cast<const uint2 *>(
+                  p.dh + at + (int64_t)(lane % 32) * cols + mine);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t w = e < 2 ? d.x : d.y;
+              const float dh = __builtin_bit_cast(
+                  float, (e & 1) ? (w & 0xffff0000u) : (w << 16));
+              float a, da;
+              activate<ACT>(g[4 * q + e], a, da);
+              v0[4 * q + e] = dh * u[4 * q + e] * da;
+              v1[4 * q + e] = dh * a;
+            }
           }
-          *reinterpret_cast<uint2 *>(p.dgu + at) = pack4(v0);
-          *reinterpret_cast<uint2 *>(p.dgu + plane_size + at) = pack4(v1);
+          store_block(stage, v0, p.dgu + at, cols, n_r, n_c);
+          store_block(stage, v1, p.dgu + plane_size + at, cols, n_r, n_c);
         }
+      } else if (partial) {
+        store_block(stage, acc[i][j],
+                    p.part + (((int64_t)split * p.rem + n - p.full) * kTile +
+                              (r - row0)) * kTile + (c - col0),
+                    kTile, n_r, n_c);
+      } else {
+        store_block(stage, acc[i][j], p.out[plane] + at, cols, n_r, n_c);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c =
-              col0 + wn * NI * 32 + j * 32 + 8 * q + 4 * (lane / 32);
-          if (c >= D) continue;
-          const int64_t at = (int64_t)r * D + c;
-          if (p.part != nullptr) {
-            f32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-            *reinterpret_cast<f32x4 *>(p.part + (int64_t)slice * rows * D +
-                                       at) = v;
-          } else {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-            *reinterpret_cast<uint2 *>(p.out[plane] + at) = pack4(v);
-          }
-        }
     }
   }
 }
@@ -542,23 +602,130 @@ __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
   }
 }
 
-// Sum of the slices' partial products, in slice order; plane q of a slice
-// goes to out[q].
-__global__ __launch_bounds__(kBlock) void slices_kernel(
-    const float *__restrict__ part, bf16 *__restrict__ out0,
-    bf16 *__restrict__ out1, int64_t n, int32_t planes, int32_t slices) {
-  const int64_t stride = (int64_t)gridDim.x * kBlock * 8;
-  const int64_t total = n * planes;
-  for (int64_t at = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8;
-       at < total; at += stride) {
+// --------------------------------------------------------------- few tokens
+
+// kHidden and kGrads of up to 16 * TB tokens: bound by the weights' bytes, so
+// they go from memory to registers as matrix fragments, each read once, and
+// the tokens' fragments come from the caches.  A workgroup owns 16 hidden
+// features; its 8 wavefronts take the steps of 32 summed elements in turn (so
+// that together they read 512 contiguous bytes of every row), four steps'
+// loads in flight each, and their sums meet in LDS, added in order.
+// FEW_US
+constexpr int kFewWaves = 8;
+constexpr int kFewUnroll = 4;
+
+template <int FORM, int TB, int ACT>
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product p) {
+  __shared__ f32x4 sums[kFewWaves][2][TB][64];
+  const int lane = lane_id(), wave = wave_id();
+  const int M = p.M, D = p.D, F = p.F;
+  const int f0 = (blockIdx.x + p.block0) * 16;
+  const int64_t f = min(f0 + lane % 16, F - 1);
+  const bf16 *wg = p.w[0] + f * D, *wu = p.w[1] + f * D;
+  const bf16 *x[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t)
+    x[t] = p.x + (int64_t)min(t * 16 + lane % 16, M - 1) * D;
+  f32x4 acc[2][TB] = {};
+  const int steps = (D + 31) / 32;
+  const int whole = D / 32;  // steps that need no bounds
+  for (int s = wave; s < steps; s += kFewWaves * kFewUnroll) {
+    Vec g[kFewUnroll], u[kFewUnroll], v[kFewUnroll][TB];
+#pragma unroll
+    for (int i = 0; i < kFewUnroll; ++i) {
+      const int k0 = (s + i * kFewWaves) * 32 + lane / 16 * 8;
+      const int k = min(k0, D - 8);
+      g[i] = load_stream(wg + k);
+      u[i] = load_stream(wu + k);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) v[i][t] = load_vec(x[t] + k);
+      if (s + i * kFewWaves >= whole && k0 >= D) {
+        g[i] = u[i] = vzero();
+#pragma unroll
+        for (int t = 0; t < TB; ++t) v[i][t] = vzero();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFewUnroll; ++i)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        const bf16x8 b = __builtin_bit_cast(bf16x8, v[i][t]);
+        acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, g[i]), b, acc[0][t], 0, 0, 0);
+        acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, u[i]), b, acc[1][t], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int t = 0; t < TB; ++t) sums[wave][q][t][lane] = acc[q][t];
+  __syncthreads();
+  // lane l, register e: feature 4 (l / 16) + e, token l % 16
+  for (int n = threadIdx.x; n < 256 * TB; n += 64 * kFewWaves) {
+    const int ff = n % 16, m = n / 16;
+    if (m >= M || f0 + ff >= F) continue;
+    float gu[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      gu[q] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w)
+        gu[q] += sums[w][q][m / 16][ff / 4 * 16 + m % 16][ff % 4];
+    }
+    const int64_t at = (int64_t)m * F + f0 + ff;
+    const int64_t plane_size = (int64_t)M * F;
+    float a, da;
+    activate<ACT>(gu[0], a, da);
+    if constexpr (FORM == kHidden) {
+      p.h[at] = round_bf16(a * gu[1]);
+      if (p.gu != nullptr) {
+        p.gu[at] = gu[0];
+        p.gu[plane_size + at] = gu[1];
+      }
+    } else {
+      const float dh =
+          __builtin_bit_cast(float, (uint32_t)p.dh[at].bits << 16);
+      p.dgu[at] = round_bf16(dh * gu[1] * da);
+      p.dgu[plane_size + at] = round_bf16(dh * a);
+    }
+  }
+}
+
+// The last p.rem tiles of dx or dW: the sum of their slices, in slice order.
+template <int FORM>
+__global__ __launch_bounds__(kBlock) void slices_kernel(Product p,
+                                                        int32_t tile) {
+  const int rows = FORM == kDw ? p.F : p.M;
+  const int per_row = tile / 8;
+  const int64_t size = (int64_t)tile * tile;
+  const int64_t total = p.rem * size / 8;
+  for (int64_t at = (int64_t)blockIdx.x * kBlock + threadIdx.x; at < total;
+       at += (int64_t)gridDim.x * kBlock) {
+    const int t = (int)(at / (size / 8));
+    const int in = (int)(at - t * (size / 8));
+    int plane, tr, tc;
+    tile_of(p.full + t, p.tiles_r, p.tiles_c, plane, tr, tc);
+    const int r = tr * tile + in / per_row, c = tc * tile + in % per_row * 8;
+    if (r >= rows || c >= p.D) continue;
+    const float *src = p.part + t * size + (int64_t)in * 8;
     float v[8] = {};
-    for (int s = 0; s < slices; ++s) {
-      const Vec a = load_stream(part + s * total + at);
-      const Vec b = load_stream(part + s * total + at + 4);
+    for (int s = 0; s < p.slices; ++s) {
+      const Vec a = load_stream(src), b = load_stream(src + 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += elem<float>(e < 4 ? a : b, e % 4);
+      src += p.rem * size;
     }
-    store_vec(at < n ? out0 + at : out1 + (at - n), pack<bf16>(v));
+    store_vec(p.out[plane] + (int64_t)r * p.D + c, pack<bf16>(v));
+  }
+}
+
+__global__ __launch_bounds__(kBlock) void zero_kernel(bf16 *a, bf16 *b,
+                                                      int64_t n) {
+  for (int64_t at = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8; at < n;
+       at += (int64_t)gridDim.x * kBlock * 8) {
+    store_vec(a + at, vzero());
+    store_vec(b + at, vzero());
   }
 }
 
@@ -567,10 +734,25 @@ __global__ __launch_bounds__(kBlock) void slices_kernel(
 struct GluPlan {
   bool big = false;
   int32_t tiles_r = 0, tiles_c = 0;
-  int32_t steps = 0, slices = 1, per_slice = 0;
+  int32_t steps = 0;
+  int32_t full = 0, rem = 0, slices = 1, per_slice = 0;
   int64_t blocks = 0;
+  int tile() const { return big ? 256 : 128; }
+  size_t part_bytes() const {
+    return slices > 1 ? (size_t)slices * rem * tile() * tile() * sizeof(float)
+                      : 0;
+  }
 };
 
+// A plan's time, in microseconds, is modelled from what a tile takes: the big
+// ones run one to a CU, 1.65 per step and 5 for filling the pipeline and
+// storing; the small ones two to a CU, 1.0 and 4.  Whole rounds of tiles (as
+// many as run at a time) are computed unsplit; the tiles left over, less than
+// a round, are split into slices of the sum where that pays: s slices take
+// ceil(rem * s / slots) / s of a round, and 4 + 2 x 4 bytes per partial sum
+// at 5 TB/s for adding them up.  Measured on MI355X for the weights'
+// gradients of 24960 x 1536 x 4096 (192 big tiles, 4 slices) 654 -> 570 us,
+// dx (588, the last 76 in 3 slices) 717 -> 589 us.
 GluPlan glu_plan(int form, int64_t M, int64_t D, int64_t F) {
   const bool pair = form == kHidden || form == kGrads;
   const int64_t rows = form == kDw ? F : M, cols = pair ? F : D;
@@ -578,28 +760,38 @@ GluPlan glu_plan(int form, int64_t M, int64_t D, int64_t F) {
   const int64_t steps = pair ? (D + kStep - 1) / kStep
                         : form == kDx ? 2 * ((F + kStep - 1) / kStep)
                                       : (M + kStep - 1) / kStep;
-  auto tiles = [&](int64_t t, int64_t *r, int64_t *c) {
-    *r = (rows + t - 1) / t;
-    *c = (cols + (pair ? t / 2 : t) - 1) / (pair ? t / 2 : t);
-    return *r * *c * planes;
-  };
-  GluPlan g;
-  int64_t r, c;
-  int64_t n = tiles(256, &r, &c);
-  g.big = n >= 192;
-  if (!g.big) n = tiles(128, &r, &c);
-  g.tiles_r = (int32_t)r;
-  g.tiles_c = (int32_t)c;
-  g.steps = (int32_t)steps;
-  int64_t slices = 1;
-  if (!pair && !g.big && n < kCUs)
-    slices = std::max<int64_t>(
-        1, std::min<int64_t>(2 * kCUs / n, steps / 4));
-  g.per_slice = (int32_t)((steps + slices - 1) / slices);
-  g.slices = (int32_t)((steps + g.per_slice - 1) / std::max(g.per_slice, 1));
-  if (g.slices < 1) g.slices = 1;
-  g.blocks = n * g.slices;
-  return g;
+  GluPlan best;
+  double best_us = 0;
+  for (int big = 0; big < 2; ++big) {
+    const int64_t t = big ? 256 : 128;
+    const int64_t slots = big ? kCUs : 2 * kCUs;
+    const double step_us = big ? 1.65 : 1.0, tile_us = big ? 5 : 4;
+    const int64_t r = (rows + t - 1) / t;
+    const int64_t c = (cols + (pair ? t / 2 : t) - 1) / (pair ? t / 2 : t);
+    const int64_t n = r * c * planes;
+    const int64_t full = n / slots * slots, rem = n - full;
+    for (int64_t s = 1; s <= 16; ++s) {
+      if (s > 1 && (pair || rem == 0 || steps < 4 * s)) break;
+      const int64_t per = (steps + s - 1) / s;
+      if ((steps + per - 1) / per != s) continue;  // an empty slice
+      double us = full / slots * (steps * step_us + tile_us);
+      if (rem > 0)
+        us += (rem * s + slots - 1) / slots * (per * step_us + tile_us);
+      if (s > 1) us += 4 + 8e-6 / 5 * rem * s * t * t;
+      if (best.blocks > 0 && us >= best_us) continue;
+      best_us = us;
+      best.big = big != 0;
+      best.tiles_r = (int32_t)r;
+      best.tiles_c = (int32_t)c;
+      best.steps = (int32_t)steps;
+      best.full = (int32_t)(s > 1 ? full : n);
+      best.rem = (int32_t)(s > 1 ? rem : 0);
+      best.slices = (int32_t)s;
+      best.per_slice = (int32_t)per;
+      best.blocks = s > 1 ? full + rem * s : n;
+    }
+  }
+  return best;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -608,31 +800,53 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // of the weights (whichever needs more; they run one after the other).
 size_t glu_bwd_bytes(int64_t M, int64_t D, int64_t F, size_t *part_at) {
   const size_t dgu = align256((size_t)2 * M * F * sizeof(bf16));
-  size_t part = 0;
-  const GluPlan x = glu_plan(kDx, M, D, F), w = glu_plan(kDw, M, D, F);
-  if (x.slices > 1) part = (size_t)x.slices * M * D * sizeof(float);
-  if (w.slices > 1)
-    part = std::max(part, (size_t)w.slices * 2 * F * D * sizeof(float));
   if (part_at != nullptr) *part_at = dgu;
-  return dgu + part;
+  return dgu + std::max(glu_plan(kDx, M, D, F).part_bytes(),
+                        glu_plan(kDw, M, D, F).part_bytes());
+}
+
+// Up to this many tokens the weights' bytes bound the two projections.
+constexpr int kFewTokens = 64;
+
+template <int FORM, int ACT>
+hipError_t launch_few(Product p, hipStream_t s) {
+  const int64_t blocks = (p.F + 15) / 16;  // at most 16384
+  return p.M <= 16
+             ? launch_kernel_threads(few_kernel<FORM, 1, ACT>, blocks,
+                                     64 * kFewWaves, s, p)
+         : p.M <= 32
+             ? launch_kernel_threads(few_kernel<FORM, 2, ACT>, blocks,
+                                     64 * kFewWaves, s, p)
+             : launch_kernel_threads(few_kernel<FORM, 4, ACT>, blocks,
+                                     64 * kFewWaves, s, p);
 }
 
 template <int FORM, int ACT>
-hipError_t launch_product(const GluPlan &g, Product p, hipStream_t s) {
+hipError_t launch_product(Product p, hipStream_t s) {
+  if constexpr (FORM == kHidden || FORM == kGrads)
+    if (p.M <= kFewTokens) return launch_few<FORM, ACT>(p, s);
+  const GluPlan g = glu_plan(FORM, p.M, p.D, p.F);
   p.tiles_r = g.tiles_r;
   p.tiles_c = g.tiles_c;
-  p.slices = g.slices;
   p.steps = g.steps;
-  p.steps_per_slice = g.per_slice;
+  p.full = g.full;
+  p.rem = g.rem;
+  p.slices = g.slices;
+  p.per_slice = g.per_slice;
   hipError_t e = hipSuccess;
   for (int64_t at = 0; at < g.blocks && e == hipSuccess; at += kMaxGrid) {
     p.block0 = (int32_t)at;
-    const int64_t n = std::min(kMaxGrid, g.blocks - at);
+    const int64_t n = std::min<int64_t>(kMaxGrid, g.blocks - at);
     e = g.big ? launch_kernel_threads(product_kernel<FORM, true, ACT>, n, 512,
                                       s, p)
               : launch_kernel_threads(product_kernel<FORM, false, ACT>, n, 256,
                                       s, p);
   }
+  if constexpr (FORM == kDx || FORM == kDw)
+    if (e == hipSuccess && g.slices > 1)
+      e = launch_kernel(slices_kernel<FORM>,
+                        (int64_t)g.rem * g.tile() * g.tile() / 8 / kBlock, s,
+                        p, (int32_t)g.tile());
   return e;
 }
 
@@ -669,40 +883,20 @@ int check_ptr(const void *p, bool needed, const char *name) {
 }
 
 template <int ACT>
-hipError_t run_fwd(const Product &p, hipStream_t s) {
-  return launch_product<kHidden, ACT>(glu_plan(kHidden, p.M, p.D, p.F), p, s);
-}
-
-template <int ACT>
-hipError_t run_bwd(Product p, bf16 *dx, bf16 *dwg, bf16 *dwu, float *part,
-                   hipStream_t s) {
+hipError_t run_bwd(Product p, bf16 *dx, bf16 *dwg, bf16 *dwu, hipStream_t s) {
   const int64_t n = (int64_t)p.M * p.F;
   hipError_t e =
       p.gu != nullptr
           ? launch_kernel(gate_grads_kernel<ACT>, (n / 8 + kBlock - 1) / kBlock,
                           s, (const float *)p.gu, p.dh, p.dgu, n)
-          : launch_product<kGrads, ACT>(glu_plan(kGrads, p.M, p.D, p.F), p, s);
+          : launch_product<kGrads, ACT>(p, s);
   if (e != hipSuccess) return e;
-  const GluPlan gx = glu_plan(kDx, p.M, p.D, p.F);
-  p.part = gx.slices > 1 ? part : nullptr;
   p.out[0] = dx;
-  e = launch_product<kDx, 0>(gx, p, s);
-  const int64_t nx = (int64_t)p.M * p.D, nw = (int64_t)p.F * p.D;
-  if (e == hipSuccess && gx.slices > 1)
-    e = launch_kernel(slices_kernel, (nx / 8 + kBlock - 1) / kBlock, s,
-                      (const float *)part, dx, dx, nx, (int32_t)1,
-                      (int32_t)gx.slices);
+  e = launch_product<kDx, 0>(p, s);
   if (e != hipSuccess) return e;
-  const GluPlan gw = glu_plan(kDw, p.M, p.D, p.F);
-  p.part = gw.slices > 1 ? part : nullptr;
   p.out[0] = dwg;
   p.out[1] = dwu;
-  e = launch_product<kDw, 0>(gw, p, s);
-  if (e == hipSuccess && gw.slices > 1)
-    e = launch_kernel(slices_kernel, (2 * nw / 8 + kBlock - 1) / kBlock, s,
-                      (const float *)part, dwg, dwu, nw, (int32_t)2,
-                      (int32_t)gw.slices);
-  return e;
+  return launch_product<kDw, 0>(p, s);
 }
 
 }  // namespace
@@ -731,8 +925,8 @@ ADALN_API int adaln_glu_fwd(const void *x, const void *wg, const void *wu,
   p.D = (int32_t)D;
   p.F = (int32_t)F;
   const hipError_t e = act == ADALN_ACT_SILU
-                           ? run_fwd<kSilu>(p, (hipStream_t)stream)
-                           : run_fwd<kGeluTanh>(p, (hipStream_t)stream);
+                           ? launch_product<kHidden, kSilu>(p, (hipStream_t)stream)
+                           : launch_product<kHidden, kGeluTanh>(p, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "adaln_glu_fwd launch");
   return ok();
 }
@@ -760,12 +954,11 @@ ADALN_API int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
   ADALN_TRY(check_ptr(dwu, true, "dwu"));
   hipStream_t s = (hipStream_t)stream;
   if (!rows) {
-    // no tokens: the weights' gradients are empty sums (no slices to add)
+    // no tokens: the weights' gradients are empty sums
     const int64_t nw = F * D;
-    const hipError_t e = launch_kernel(
-        slices_kernel, (2 * nw / 8 + kBlock - 1) / kBlock, s,
-        (const float *)nullptr, (bf16 *)dwg, (bf16 *)dwu, nw, (int32_t)2,
-        (int32_t)0);
+    const hipError_t e =
+        launch_kernel(zero_kernel, (nw / 8 + kBlock - 1) / kBlock, s,
+                      (bf16 *)dwg, (bf16 *)dwu, nw);
     if (e != hipSuccess) return hip_fail(e, "adaln_glu_bwd launch");
     return ok();
   }
@@ -785,12 +978,11 @@ ADALN_API int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
   p.M = (int32_t)M;
   p.D = (int32_t)D;
   p.F = (int32_t)F;
-  float *part = (float *)((char *)workspace + part_at);
+  p.part = (float *)((char *)workspace + part_at);
   const hipError_t e =
       act == ADALN_ACT_SILU
-          ? run_bwd<kSilu>(p, (bf16 *)dx, (bf16 *)dwg, (bf16 *)dwu, part, s)
-          : run_bwd<kGeluTanh>(p, (bf16 *)dx, (bf16 *)dwg, (bf16 *)dwu, part,
-                               s);
+          ? run_bwd<kSilu>(p, (bf16 *)dx, (bf16 *)dwg, (bf16 *)dwu, s)
+          : run_bwd<kGeluTanh>(p, (bf16 *)dx, (bf16 *)dwg, (bf16 *)dwu, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_glu_bwd launch");
   return ok();
 }
