@@ -63,12 +63,15 @@ __device__ __forceinline__ void dma(uint32_t lds, const void *base,
       : "memory");
 }
 
-// Every load of this wavefront has landed, then every wavefront's.
+// All loads of this wavefront but the last LATER have landed, then those of
+// every wavefront.  (Loads return in order; a store among them, which may
+// not, only makes the wait longer.)
+template <int LATER>
 __device__ __forceinline__ void arrive() {
   asm volatile(
-      "s_waitcnt vmcnt(0) lgkmcnt(0)\n\t"
-      "s_barrier" ::
-          : "memory");
+      "s_waitcnt vmcnt(%0) lgkmcnt(0)\n\t"
+      "s_barrier" ::"n"(LATER)
+      : "memory");
 }
 
 // An operand whose summed dimension is contiguous: ROWS rows of kStep
@@ -314,14 +317,23 @@ __device__ __forceinline__ void tile_of(int n, int tiles_r, int tiles_c,
   tc = in / rows;
 }
 
-// BIG: 256 x 256 tiles by 8 wavefronts (2 x 4, each 128 x 64); else 128 x 128
-// by 4 (2 x 2, each 64 x 64).  Columns of kHidden and kGrads: half of them of
-// G, half the same ones of U, so that a lane holds both of an element.
-template <int FORM, bool BIG, int ACT>
-__global__ __launch_bounds__(BIG ? 512 : 256, 2) void product_kernel(
-    Product p) {
+// Three tilings.  kBig: 256 x 256 tiles by 8 wavefronts (2 x 4, each 128 x
+// 64), two steps in LDS (128 KiB); kSmall: 128 x 128 by 4 (2 x 2, each 64 x
+// 64), two steps (64 KiB, so two workgroups to a CU); kDeep: the same with
+// four steps (128 KiB), for calls of so few tiles that a CU has one at most
+// and a step's arithmetic is far shorter than its loads take to arrive.
+// Columns of kHidden and kGrads: half of them of G, half the same ones of U,
+// so that a lane holds both of an element.
+enum { kSmall = 0, kBig = 1, kDeep = 2 };
+
+template <int FORM, int TILING, int ACT>
+__global__ __launch_bounds__(TILING == kBig ? 512 : 256,
+                             TILING == kDeep ? 1 : 2) void
+product_kernel(Product p) {
+  constexpr bool BIG = TILING == kBig;
   constexpr int kWaves = BIG ? 8 : 4;
   constexpr int kTile = BIG ? 256 : 128;
+  constexpr int kBufs = TILING == kDeep ? 4 : 2;
   constexpr int kWn = kWaves / 2;          // wavefronts across the columns
   constexpr int MI = kTile / 2 / 32;        // 32-row blocks of a wavefront
   constexpr int NI = kTile / kWn / 32;      // 32-column blocks
@@ -335,7 +347,7 @@ __global__ __launch_bounds__(BIG ? 512 : 256, 2) void product_kernel(
                                  Across<kTile, kWaves>>;
   constexpr uint32_t kColBytes = kPair ? 2 * Col::kBytes : Col::kBytes;
   constexpr uint32_t kBuf = Row::kBytes + kColBytes;
-  __shared__ __align__(1024) char lds[2][kBuf];
+  __shared__ __align__(1024) char lds[kBufs][kBuf];
 
   // The first `full` blocks compute a tile each; the rest, slices of the
   // sums of the last `rem` tiles.
@@ -466,17 +478,22 @@ __global__ __launch_bounds__(BIG ? 512 : 256, 2) void product_kernel(
     seek(s0);
     pl_left = left(s0);
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n) load(n, 0);
-    arrive();
-    advance(s0 + 1);
+    for (int s = 0; s < kBufs - 1; ++s) {
 #pragma unroll
-    for (int n = 0; n < kFirst; ++n) load(n, 1);
+      for (int n = 0; n < kLoads; ++n) load(n, s);
+      advance(s0 + s + 1);
+    }
+    arrive<(kBufs - 2) * kLoads>();
+#pragma unroll
+    for (int n = 0; n < kFirst; ++n) load(n, kBufs - 1);
     clear(s0, 0);
 #pragma unroll
     for (int n = 0; n < NI + MI; ++n) read(n, 0, 0);
   }
+  int buf = 0;
   for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
+    const int before = buf == 0 ? kBufs - 1 : buf - 1;
+    const int after = buf == kBufs - 1 ? 0 : buf + 1;
 #pragma unroll
     for (int kk = 0; kk < KK - 1; ++kk) {
 #pragma unroll
@@ -487,26 +504,31 @@ __global__ __launch_bounds__(BIG ? 512 : 256, 2) void product_kernel(
 #pragma unroll
           for (int l = kFirst + n * (kLoads - kFirst) / kMul;
                l < kFirst + (n + 1) * (kLoads - kFirst) / kMul; ++l)
-            load(l, buf ^ 1);
+            load(l, before);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int n = kMul; n < NI + MI; ++n) read(n, buf, kk + 1);
     }
-    arrive();
-    clear(s + 1, buf ^ 1);
-    advance(s + 2);
+    arrive<(kBufs - 2) * kLoads>();
+    clear(s + 1, after);
+    advance(s + kBufs);
 #pragma unroll
     for (int n = 0; n < kMul; ++n) {
       multiply(n, KK - 1);
       // (past the last step: what lies there, not used)
-      if (n < NI + MI) read(n, buf ^ 1, 0);
+      if (n < NI + MI) read(n, after, 0);
 #pragma unroll
       for (int l = n * kFirst / kMul; l < (n + 1) * kFirst / kMul; ++l)
         load(l, buf);
       __builtin_amdgcn_sched_barrier(0);
     }
+#pragma unroll
+    for (int n = kMul; n < NI + MI; ++n) read(n, after, 0);
+    buf = after;
   }
-  arrive();  // LDS is free: nothing on its way in, nobody reading
+  arrive<0>();  // LDS is free: nothing on its way in, nobody reading
 
   // acc[i][j][4 q + e] of lane l is row l % 32 of block i, column
   // 8 q + 4 (l / 32) + e of block j.
@@ -609,8 +631,9 @@ __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
 // the tokens' fragments come from the caches.  A workgroup owns 16 hidden
 // features; its 8 wavefronts take the steps of 32 summed elements in turn (so
 // that together they read 512 contiguous bytes of every row), four steps'
-// loads in flight each, and their sums meet in LDS, added in order.
-// FEW_US
+// loads in flight each, and their sums meet in LDS, added in order.  (Plain
+// loads: with the streaming hint one token took 8.4 us, not 7.4, D = 1536, F =
+// 4096; 32 features per workgroup, 11.6.)
 constexpr int kFewWaves = 8;
 constexpr int kFewUnroll = 4;
 
@@ -635,8 +658,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product p) {
     for (int i = 0; i < kFewUnroll; ++i) {
       const int k0 = (s + i * kFewWaves) * 32 + lane / 16 * 8;
       const int k = min(k0, D - 8);
-      g[i] = load_stream(wg + k);
-      u[i] = load_stream(wu + k);
+      g[i] = load_vec(wg + k);
+      u[i] = load_vec(wu + k);
 #pragma unroll
       for (int t = 0; t < TB; ++t) v[i][t] = load_vec(x[t] + k);
       if (s + i * kFewWaves >= whole && k0 >= D) {
@@ -732,12 +755,12 @@ __global__ __launch_bounds__(kBlock) void zero_kernel(bf16 *a, bf16 *b,
 // ----------------------------------------------------------------- planning
 
 struct GluPlan {
-  bool big = false;
+  int tiling = kSmall;
   int32_t tiles_r = 0, tiles_c = 0;
   int32_t steps = 0;
   int32_t full = 0, rem = 0, slices = 1, per_slice = 0;
   int64_t blocks = 0;
-  int tile() const { return big ? 256 : 128; }
+  int tile() const { return tiling == kBig ? 256 : 128; }
   size_t part_bytes() const {
     return slices > 1 ? (size_t)slices * rem * tile() * tile() * sizeof(float)
                       : 0;
@@ -746,13 +769,14 @@ struct GluPlan {
 
 // A plan's time, in microseconds, is modelled from what a tile takes: the big
 // ones run one to a CU, 1.65 per step and 5 for filling the pipeline and
-// storing; the small ones two to a CU, 1.0 and 4.  Whole rounds of tiles (as
-// many as run at a time) are computed unsplit; the tiles left over, less than
-// a round, are split into slices of the sum where that pays: s slices take
-// ceil(rem * s / slots) / s of a round, and 4 + 2 x 4 bytes per partial sum
-// at 5 TB/s for adding them up.  Measured on MI355X for the weights'
-// gradients of 24960 x 1536 x 4096 (192 big tiles, 4 slices) 654 -> 570 us,
-// dx (588, the last 76 in 3 slices) 717 -> 589 us.
+// storing; the small ones two to a CU, 1.0 and 4; the deep ones one to a CU,
+// 0.5 and 4 (MI355X, D = 1536, F = 4096, forward: 256 tokens 15.7 us deep
+// against 20.5 small, 1024 tokens 31.6 against 27.7).  Whole rounds of tiles (as many as run at a time) are computed
+// unsplit; the tiles left over, less than a round, are split into slices of
+// the sum where that pays: s slices take ceil(rem * s / slots) / s of a round,
+// and 4 + 2 x 4 bytes per partial sum at 5 TB/s for adding them up.  Measured
+// on MI355X for the weights' gradients of 24960 x 1536 x 4096 (192 big tiles,
+// 4 slices) 654 -> 570 us, dx (588, the last 76 in 3 slices) 717 -> 589 us.
 GluPlan glu_plan(int form, int64_t M, int64_t D, int64_t F) {
   const bool pair = form == kHidden || form == kGrads;
   const int64_t rows = form == kDw ? F : M, cols = pair ? F : D;
@@ -762,10 +786,12 @@ GluPlan glu_plan(int form, int64_t M, int64_t D, int64_t F) {
                                       : (M + kStep - 1) / kStep;
   GluPlan best;
   double best_us = 0;
-  for (int big = 0; big < 2; ++big) {
-    const int64_t t = big ? 256 : 128;
-    const int64_t slots = big ? kCUs : 2 * kCUs;
-    const double step_us = big ? 1.65 : 1.0, tile_us = big ? 5 : 4;
+  for (int tiling = 0; tiling < 3; ++tiling) {
+    const int64_t t = tiling == kBig ? 256 : 128;
+    const int64_t slots = tiling == kSmall ? 2 * kCUs : kCUs;
+    const double step_us =
+        tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.5;
+    const double tile_us = tiling == kBig ? 5 : 4;
     const int64_t r = (rows + t - 1) / t;
     const int64_t c = (cols + (pair ? t / 2 : t) - 1) / (pair ? t / 2 : t);
     const int64_t n = r * c * planes;
@@ -780,7 +806,7 @@ GluPlan glu_plan(int form, int64_t M, int64_t D, int64_t F) {
       if (s > 1) us += 4 + 8e-6 / 5 * rem * s * t * t;
       if (best.blocks > 0 && us >= best_us) continue;
       best_us = us;
-      best.big = big != 0;
+      best.tiling = tiling;
       best.tiles_r = (int32_t)r;
       best.tiles_c = (int32_t)c;
       best.steps = (int32_t)steps;
@@ -805,8 +831,15 @@ size_t glu_bwd_bytes(int64_t M, int64_t D, int64_t F, size_t *part_at) {
                         glu_plan(kDw, M, D, F).part_bytes());
 }
 
-// Up to this many tokens the weights' bytes bound the two projections.
-constexpr int kFewTokens = 64;
+// Few tokens: few_kernel.  Past 4 tokens only where the tiles of 64 hidden
+// features leave half the CUs idle (MI355X, D = 1536, F = 4096: 1 token 7.4
+// us, 32 tokens 10.5, 64 tokens 14.9, against 15.0 by tiles for all of
+// these).  Elsewhere the tiles stream the weights as fast and its repeated
+// reads of the tokens cost more (D = 5120, F = 13824: 1 token 61 us, 16
+// tokens 80, 64 tokens 137, against 63).
+bool few_tokens(int64_t M, int64_t F) {
+  return M <= 4 || (M <= 64 && (F + 63) / 64 < kCUs / 2);
+}
 
 template <int FORM, int ACT>
 hipError_t launch_few(Product p, hipStream_t s) {
@@ -824,7 +857,7 @@ hipError_t launch_few(Product p, hipStream_t s) {
 template <int FORM, int ACT>
 hipError_t launch_product(Product p, hipStream_t s) {
   if constexpr (FORM == kHidden || FORM == kGrads)
-    if (p.M <= kFewTokens) return launch_few<FORM, ACT>(p, s);
+    if (few_tokens(p.M, p.F)) return launch_few<FORM, ACT>(p, s);
   const GluPlan g = glu_plan(FORM, p.M, p.D, p.F);
   p.tiles_r = g.tiles_r;
   p.tiles_c = g.tiles_c;
@@ -837,10 +870,14 @@ hipError_t launch_product(Product p, hipStream_t s) {
   for (int64_t at = 0; at < g.blocks && e == hipSuccess; at += kMaxGrid) {
     p.block0 = (int32_t)at;
     const int64_t n = std::min<int64_t>(kMaxGrid, g.blocks - at);
-    e = g.big ? launch_kernel_threads(product_kernel<FORM, true, ACT>, n, 512,
-                                      s, p)
-              : launch_kernel_threads(product_kernel<FORM, false, ACT>, n, 256,
-                                      s, p);
+    e = g.tiling == kBig
+            ? launch_kernel_threads(product_kernel<FORM, kBig, ACT>, n, 512, s,
+                                    p)
+        : g.tiling == kSmall
+            ? launch_kernel_threads(product_kernel<FORM, kSmall, ACT>, n, 256,
+                                    s, p)
+            : launch_kernel_threads(product_kernel<FORM, kDeep, ACT>, n, 256,
+                                    s, p);
   }
   if constexpr (FORM == kDx || FORM == kDw)
     if (e == hipSuccess && g.slices > 1)
