@@ -40,11 +40,29 @@ constexpr int kMaxTokens = 16;  // tokens per block
 
 // Frequencies in turns per unit position, as 64-bit fractions of a turn:
 // pos * turns, wrapping modulo 2^64, is the phase modulo one turn with no
-// loss for any position.  (Held as a kernel argument: 3 KiB.)
-struct Rotation {
-  uint64_t turns[kMaxFreqs];
-  int32_t axes;
-  int32_t pairs;
+// loss for any position.  They travel as kernel arguments, whose size a
+// launch pays for (MI355X: 11 us per call with 3.5 KiB of them, SMALL_US with
+// the small form), so the usual case, up to 64 pairs turned by one axis
+// each, has a form of its own.
+struct OneAxis {
+  static constexpr int kPairs = 64;
+  uint64_t turns[kPairs];
+  uint8_t axis[kPairs];
+  __device__ __forceinline__ uint64_t phase(const int32_t *pos, int j, int,
+                                            int) const {
+    return (uint64_t)(int64_t)pos[axis[j]] * turns[j];
+  }
+};
+
+struct AllAxes {
+  uint64_t turns[kMaxFreqs];  // [axes, pairs]
+  __device__ __forceinline__ uint64_t phase(const int32_t *pos, int j,
+                                            int axes, int pairs) const {
+    uint64_t p = 0;
+    for (int a = 0; a < axes; ++a)
+      p += (uint64_t)(int64_t)pos[a] * turns[a * pairs + j];
+    return p;
+  }
 };
 
 // One tensor's heads: strides in 16-byte vectors.
@@ -75,7 +93,8 @@ struct Job {
   float eps;
   float inv_d;
   float dir;              // +1: by the angle, -1: by the negative angle
-  Rotation rot;
+  int32_t axes;
+  int32_t pairs;
 };
 
 // cos and sin of a phase given as a 64-bit fraction of a turn.  The top 32
@@ -164,8 +183,16 @@ __device__ __forceinline__ void rotate(float (&xa)[E], float (&xb)[E],
 
 enum { kRope = 0, kNormFwd = 1, kNormBwd = 2 };
 
-template <typename T, int L, bool HALF, int OP>
-__global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
+// A lane's part of one row (a head of a token of the block): its vectors of
+// x, and of dy in the backward of the norm.
+struct Row {
+  Vec xa, xb, ya, yb;
+  int tok, head;
+  bool live;
+};
+
+template <typename T, int L, bool HALF, int OP, typename ROT>
+__global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
   constexpr int E = Elems<T>::value;
   constexpr int kRows = kBlock / L;   // heads a workgroup takes at a time
   constexpr int kPitch = L * E;       // table entries per token
@@ -195,18 +222,42 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
     const int b = (int)(blk / job.blocks_n);
     const int n0 = (int)(blk - (int64_t)b * job.blocks_n) * job.tb;
     const int tb = min(job.tb, job.N - n0);
+
+    auto at = [&](const Heads &h, int tok, int head) {
+      return (b * h.batch + (int64_t)(n0 + tok) * h.token +
+              (int64_t)head * h.head) * 16;
+    };
+    auto load = [&](int t, int row0) {
+      Row r;
+      const int H = job.H[t];
+      r.live = row0 + group < tb * H;
+      const int row = r.live ? row0 + group : 0;
+      r.tok = H == 1 ? row : (int)__umulhi((uint32_t)row, job.magic[t]);
+      r.head = row - r.tok * H;
+      const char *src = job.in[t].data + at(job.in[t], r.tok, r.head);
+      r.xa = load_stream(src + va * 16);
+      r.xb = load_stream(src + vb * 16);
+      if constexpr (OP == kNormBwd) {
+        const char *dy = job.dy[t].data + at(job.dy[t], r.tok, r.head);
+        r.ya = load_stream(dy + va * 16);
+        r.yb = load_stream(dy + vb * 16);
+      }
+      return r;
+    };
+
+    // the first rows are on their way while the sines are computed
+    Row next = {};
+    if (job.H[0] > 0) next = load(0, 0);
+
     // the sines of the block's tokens; pairs past the rotated ones turn by 0
-    const int32_t *pos = job.pos + b * job.pos_batch + (int64_t)n0 * job.rot.axes;
+    const int32_t *pos = job.pos + b * job.pos_batch + (int64_t)n0 * job.axes;
     for (int i = tid; i < tb * kPitch; i += kBlock) {
       const int tok = i / kPitch;
       const int j = i % kPitch;
       float2 cs = {1.f, 0.f};
-      if (j < job.rot.pairs) {
-        uint64_t phase = 0;
-        for (int a = 0; a < job.rot.axes; ++a)
-          phase += (uint64_t)(int64_t)pos[tok * job.rot.axes + a] *
-                   job.rot.turns[a * job.rot.pairs + j];
-        cos_sin(phase, cs.x, cs.y);
+      if (j < job.pairs) {
+        cos_sin(rot.phase(pos + tok * job.axes, j, job.axes, job.pairs), cs.x,
+                cs.y);
         cs.y *= job.dir;
       }
       table[i] = cs;
@@ -215,17 +266,8 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int H = job.H[t];
-      const int rows = tb * H;
+      const int rows = tb * job.H[t];
       if (rows == 0) continue;
-      const char *in = job.in[t].data +
-                       (b * job.in[t].batch + n0 * job.in[t].token) * 16;
-      const char *dy = OP != kNormBwd
-                           ? nullptr
-                           : job.dy[t].data + (b * job.dy[t].batch +
-                                               n0 * job.dy[t].token) * 16;
-      char *out = const_cast<char *>(job.out[t].data) +
-                  (b * job.out[t].batch + n0 * job.out[t].token) * 16;
       float w[OP == kRope ? 1 : 2 * E];
       if constexpr (OP != kRope) {
         const Vec wa = load_vec((const char *)job.w[t] + va * 16);
@@ -236,35 +278,23 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
           w[E + i] = elem<T>(wb, i);
         }
       }
+      if (t == 1) next = load(1, 0);
       for (int row0 = 0; row0 < rows; row0 += kRows) {
-        const bool live = row0 + group < rows;
-        const int row = live ? row0 + group : 0;
-        const int tok = H == 1 ? row : (int)__umulhi((uint32_t)row, job.magic[t]);
-        const int head = row - tok * H;
-        const char *src = in + ((int64_t)tok * job.in[t].token +
-                                (int64_t)head * job.in[t].head) * 16;
-        Vec xa = load_stream(src + va * 16);
-        Vec xb = load_stream(src + vb * 16);
-        Vec ya = {}, yb = {};
-        if constexpr (OP == kNormBwd) {
-          const char *sdy = dy + ((int64_t)tok * job.dy[t].token +
-                                  (int64_t)head * job.dy[t].head) * 16;
-          ya = load_stream(sdy + va * 16);
-          yb = load_stream(sdy + vb * 16);
-        }
+        Row r = next;
+        if (row0 + kRows < rows) next = load(t, row0 + kRows);
         float2 cs[E];
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-          cs[i] = table[tok * kPitch + ta + i];
-          cs[E / 2 + i] = table[tok * kPitch + tbl + i];
+          cs[i] = table[r.tok * kPitch + ta + i];
+          cs[E / 2 + i] = table[r.tok * kPitch + tbl + i];
         }
-        if (!ok_a) xa = vzero(), ya = vzero();
-        if (!ok_b) xb = vzero(), yb = vzero();
+        if (!ok_a) r.xa = vzero(), r.ya = vzero();
+        if (!ok_b) r.xb = vzero(), r.yb = vzero();
         float fa[E], fb[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          fa[i] = elem<T>(xa, i);
-          fb[i] = elem<T>(xb, i);
+          fa[i] = elem<T>(r.xa, i);
+          fb[i] = elem<T>(r.xb, i);
         }
         if constexpr (OP != kRope) {
           float ss = 0.f;
@@ -274,19 +304,19 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
           for (int i = 0; i < E; ++i) ss = fmaf(fb[i], fb[i], ss);
           if constexpr (OP == kNormFwd) {
             ss = lanes_sum<L>(ss);
-            const float r = rsqrtf(fmaf(ss, job.inv_d, job.eps));
+            const float s = rsqrtf(fmaf(ss, job.inv_d, job.eps));
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-              fa[i] = fa[i] * r * w[i];
-              fb[i] = fb[i] * r * w[E + i];
+              fa[i] = fa[i] * s * w[i];
+              fb[i] = fb[i] * s * w[E + i];
             }
             rotate<E, HALF>(fa, fb, cs);
           } else {
             float ga[E], gb[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-              ga[i] = elem<T>(ya, i);
-              gb[i] = elem<T>(yb, i);
+              ga[i] = elem<T>(r.ya, i);
+              gb[i] = elem<T>(r.yb, i);
             }
             rotate<E, HALF>(ga, gb, cs);
             float sg = 0.f;
@@ -297,25 +327,25 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job) {
             }
             ss = lanes_sum<L>(ss);
             sg = lanes_sum<L>(sg);
-            const float r = rsqrtf(fmaf(ss, job.inv_d, job.eps));
-            const float m = sg * r * r * job.inv_d;  // r * mean(g * xh)
+            const float s = rsqrtf(fmaf(ss, job.inv_d, job.eps));
+            const float m = sg * s * s * job.inv_d;  // r * mean(g * xh)
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-              if (live) {
-                acc[t][i] = fmaf(ga[i], fa[i] * r, acc[t][i]);
-                acc[t][E + i] = fmaf(gb[i], fb[i] * r, acc[t][E + i]);
+              if (r.live) {
+                acc[t][i] = fmaf(ga[i], fa[i] * s, acc[t][i]);
+                acc[t][E + i] = fmaf(gb[i], fb[i] * s, acc[t][E + i]);
               }
-              fa[i] = r * (ga[i] * w[i] - fa[i] * m);
-              fb[i] = r * (gb[i] * w[E + i] - fb[i] * m);
+              fa[i] = s * (ga[i] * w[i] - fa[i] * m);
+              fb[i] = s * (gb[i] * w[E + i] - fb[i] * m);
             }
           }
         } else {
           rotate<E, HALF>(fa, fb, cs);
         }
-        char *dst = out + ((int64_t)tok * job.out[t].token +
-                           (int64_t)head * job.out[t].head) * 16;
-        if (live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
-        if (live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
+        char *dst = const_cast<char *>(job.out[t].data) +
+                    at(job.out[t], r.tok, r.head);
+        if (r.live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
+        if (r.live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
       }
     }
     __syncthreads();
@@ -489,32 +519,6 @@ int lanes_per_head(int nvec) {
   return L;
 }
 
-template <typename T, int OP, int L>
-hipError_t go(const Job &job, bool half, int64_t grid, hipStream_t stream) {
-  const size_t lds = (size_t)job.tb * L * Elems<T>::value * sizeof(float2);
-  return half ? launch_kernel_lds(heads_kernel<T, L, true, OP>, grid, kBlock,
-                                  lds, stream, job)
-              : launch_kernel_lds(heads_kernel<T, L, false, OP>, grid, kBlock,
-                                  lds, stream, job);
-}
-
-template <typename T, int OP>
-hipError_t launch_heads(const Job &job, bool half, int64_t grid,
-                        hipStream_t stream) {
-  switch (lanes_per_head(job.nvec)) {
-    case 1: return go<T, OP, 1>(job, half, grid, stream);
-    case 2: return go<T, OP, 2>(job, half, grid, stream);
-    case 4: return go<T, OP, 4>(job, half, grid, stream);
-    case 8: return go<T, OP, 8>(job, half, grid, stream);
-    case 16: return go<T, OP, 16>(job, half, grid, stream);
-    case 32: return go<T, OP, 32>(job, half, grid, stream);
-    default:
-      if constexpr (Elems<T>::value == 4)
-        return go<T, OP, 64>(job, half, grid, stream);
-      return hipErrorInvalidValue;
-  }
-}
-
 void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
               bool inverse, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
               int dtype) {
@@ -537,16 +541,67 @@ void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
   job.blocks_n = (int32_t)p.blocks_n;
   job.blocks = p.blocks;
   job.dir = inverse ? -1.f : 1.f;
-  job.rot.axes = rot->axes;
-  job.rot.pairs = rot->pairs;
-  for (int i = 0; i < rot->axes * rot->pairs; ++i) {
-    // radians -> turns; the fraction of a turn in 64 bits (long double keeps
-    // the 64 bits of the product)
-    const long double t = (long double)rot->freqs[i] *
-                          0.159154943091895335768883763372514362L;
-    long double f = t - floorl(t);
-    f = f * 18446744073709551616.0L + 0.5L;
-    job.rot.turns[i] = f >= 18446744073709551616.0L ? 0 : (uint64_t)f;
+  job.axes = rot->axes;
+  job.pairs = rot->pairs;
+}
+
+// Radians per unit position -> turns, modulo 1, in 64 bits (long double keeps
+// the 64 bits of the product).
+uint64_t turns_of(double radians) {
+  const long double t =
+      (long double)radians * 0.159154943091895335768883763372514362L;
+  // the whole turns go: |t| < 2^18, so truncation to an integer is exact
+  const long double f = t - (long double)(int64_t)t;  // in (-1, 1)
+  const long double g = (f < 0 ? f + 1 : f) * 18446744073709551616.0L;
+  return g >= 18446744073709551615.0L ? 0 : (uint64_t)(g + 0.5L);
+}
+
+// The small form, where it holds the rotation.
+bool fill(OneAxis &r, const adaln_rotation_t *rot) {
+  if (rot->pairs > OneAxis::kPairs) return false;
+  for (int j = 0; j < rot->pairs; ++j) {
+    int axis = -1;
+    for (int a = 0; a < rot->axes; ++a)
+      if (rot->freqs[a * rot->pairs + j] != 0) {
+        if (axis >= 0) return false;
+        axis = a;
+      }
+    r.axis[j] = (uint8_t)std::max(axis, 0);
+    r.turns[j] =
+        axis < 0 ? 0 : turns_of(rot->freqs[axis * rot->pairs + j]);
+  }
+  return true;
+}
+
+void fill(AllAxes &r, const adaln_rotation_t *rot) {
+  for (int i = 0; i < rot->axes * rot->pairs; ++i)
+    r.turns[i] = turns_of(rot->freqs[i]);
+}
+
+template <typename T, int OP, int L, typename ROT>
+hipError_t go(const Job &job, const ROT &rot, bool half, int64_t grid,
+              hipStream_t stream) {
+  const size_t lds = (size_t)job.tb * L * Elems<T>::value * sizeof(float2);
+  return half ? launch_kernel_lds(heads_kernel<T, L, true, OP, ROT>, grid,
+                                  kBlock, lds, stream, job, rot)
+              : launch_kernel_lds(heads_kernel<T, L, false, OP, ROT>, grid,
+                                  kBlock, lds, stream, job, rot);
+}
+
+template <typename T, int OP, typename ROT>
+hipError_t launch_heads(const Job &job, const ROT &rot, bool half,
+                        int64_t grid, hipStream_t stream) {
+  switch (lanes_per_head(job.nvec)) {
+    case 1: return go<T, OP, 1>(job, rot, half, grid, stream);
+    case 2: return go<T, OP, 2>(job, rot, half, grid, stream);
+    case 4: return go<T, OP, 4>(job, rot, half, grid, stream);
+    case 8: return go<T, OP, 8>(job, rot, half, grid, stream);
+    case 16: return go<T, OP, 16>(job, rot, half, grid, stream);
+    case 32: return go<T, OP, 32>(job, rot, half, grid, stream);
+    default:
+      if constexpr (Elems<T>::value == 4)
+        return go<T, OP, 64>(job, rot, half, grid, stream);
+      return hipErrorInvalidValue;
   }
 }
 
@@ -555,12 +610,24 @@ int hip_fail(hipError_t e, const char *what) {
 }
 
 template <int OP>
-int enqueue(const Job &job, int layout, int64_t grid, int dtype,
-            hipStream_t stream, const char *what) {
-  const bool half = layout == ADALN_ROPE_HALF;
-  const hipError_t e = dtype == ADALN_BF16
-                           ? launch_heads<bf16, OP>(job, half, grid, stream)
-                           : launch_heads<float, OP>(job, half, grid, stream);
+int enqueue(const Job &job, const adaln_rotation_t *rot, int64_t grid,
+            int dtype, hipStream_t stream, const char *what) {
+  const bool half = rot->layout == ADALN_ROPE_HALF;
+  auto run = [&](const auto &r) {
+    return dtype == ADALN_BF16 ? launch_heads<bf16, OP>(job, r, half, grid,
+                                                        stream)
+                               : launch_heads<float, OP>(job, r, half, grid,
+                                                         stream);
+  };
+  OneAxis one;
+  hipError_t e;
+  if (fill(one, rot)) {
+    e = run(one);
+  } else {
+    AllAxes all;
+    fill(all, rot);
+    e = run(all);
+  }
   return e == hipSuccess ? ADALN_OK : hip_fail(e, what);
 }
 
@@ -592,7 +659,7 @@ int rope(const adaln_heads_t *q, const adaln_heads_t *k,
   job.in[1] = heads_of(k, B, N, Hk, dtype);
   job.out[0] = heads_of(q_out, B, N, Hq, dtype);
   job.out[1] = heads_of(k_out, B, N, Hk, dtype);
-  ADALN_TRY(enqueue<kRope>(job, rot->layout, p.grid, dtype,
+  ADALN_TRY(enqueue<kRope>(job, rot, p.grid, dtype,
                            (hipStream_t)stream, what));
   return ok();
 }
@@ -650,7 +717,7 @@ ADALN_API int adaln_qk_norm_rope_fwd(
   job.w[1] = wk;
   job.eps = eps;
   job.inv_d = 1.f / (float)d;
-  ADALN_TRY(enqueue<kNormFwd>(job, rot->layout, p.grid, dtype,
+  ADALN_TRY(enqueue<kNormFwd>(job, rot, p.grid, dtype,
                               (hipStream_t)stream,
                               "adaln_qk_norm_rope_fwd launch"));
   return ok();
@@ -714,7 +781,7 @@ ADALN_API int adaln_qk_norm_rope_bwd(
     job.part[1] = part[1];
     job.eps = eps;
     job.inv_d = 1.f / (float)d;
-    ADALN_TRY(enqueue<kNormBwd>(job, rot->layout, grid, dtype,
+    ADALN_TRY(enqueue<kNormBwd>(job, rot, grid, dtype,
                                 (hipStream_t)stream,
                                 "adaln_qk_norm_rope_bwd launch"));
   }

@@ -118,7 +118,8 @@ class _Call:
                 raise ValueError("an output was given for a missing input")
             return None
         if t is None:
-            t = torch.empty(like.shape, dtype=self.dt, device=self.dev)
+            t = torch.empty_like(like,
+                                 memory_format=torch.contiguous_format)
         return t
 
     def sizes(self, stream):
