@@ -37,11 +37,14 @@ constexpr int kMaxFreqs = 384;  // entries of the [axes, pairs] table
 constexpr int kMaxAxes = 4;
 constexpr int kMaxHead = 512;   // features per head
 constexpr int kMaxTokens = 16;  // tokens per block
+constexpr int kBlockRows = 4;   // rows of a block per lane group, about
+constexpr int kFillBlocks = 4;  // blocks per CU before blocks get longer
+constexpr int kBwdPerCu = 6;    // workgroups per CU of the norm's backward
 
 // Frequencies in turns per unit position, as 64-bit fractions of a turn:
 // pos * turns, wrapping modulo 2^64, is the phase modulo one turn with no
 // loss for any position.  They travel as kernel arguments, whose size a
-// launch pays for (MI355X: 11 us per call with 3.5 KiB of them, SMALL_US with
+// launch pays for (MI355X: 11 us per call with 3.5 KiB of them, 4.7 with
 // the small form), so the usual case, up to 64 pairs turned by one axis
 // each, has a form of its own.
 struct OneAxis {
@@ -78,11 +81,12 @@ struct Job {
   Heads dy[2];            // backward of the norm only
   Heads out[2];
   const void *w[2];       // norm weights
-  float *part[2];         // backward: partial rows of dw, [grid, d]
+  float *part[2];         // backward: partial rows of dw, [workgroups, d]
   const int32_t *pos;
   int64_t pos_batch;      // elements
   int32_t H[2];
   uint32_t magic[2];      // ceil(2^32 / H)
+  int32_t grid_q;         // workgroups of q; the rest are k's
   int32_t N;
   int32_t d;
   int32_t nvec;           // vectors per head
@@ -90,6 +94,7 @@ struct Job {
   int32_t tb;             // tokens per block
   int32_t blocks_n;       // blocks per sample
   int64_t blocks;
+  int32_t cached;         // plain loads (else the streaming hint)
   float eps;
   float inv_d;
   float dir;              // +1: by the angle, -1: by the negative angle
@@ -191,12 +196,27 @@ struct Row {
   bool live;
 };
 
+// A block of tokens: tb of them (fewer at a sample's end) from n0 of sample b.
+struct Block {
+  int b, n0, tb;
+  __device__ __forceinline__ Block(const Job &job, int64_t blk) {
+    b = (int)(blk / job.blocks_n);
+    n0 = (int)(blk - (int64_t)b * job.blocks_n) * job.tb;
+    tb = min(job.tb, job.N - n0);
+  }
+  __device__ __forceinline__ int64_t at(const Heads &h, int tok,
+                                        int head) const {
+    return (b * h.batch + (int64_t)(n0 + tok) * h.token +
+            (int64_t)head * h.head) * 16;
+  }
+};
+
 template <typename T, int L, bool HALF, int OP, typename ROT>
 __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
   constexpr int E = Elems<T>::value;
   constexpr int kRows = kBlock / L;   // heads a workgroup takes at a time
   constexpr int kPitch = L * E;       // table entries per token
-  extern __shared__ float2 table[];   // [tb][kPitch]
+  extern __shared__ float2 tables[];  // 2 x [tb][kPitch]
   const int tid = threadIdx.x;
   const int slot = tid % L;
   const int group = tid / L;
@@ -210,48 +230,58 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
   const int ta = HALF ? slot * E : (ok_a ? va : 0) * (E / 2);
   const int tbl = HALF ? slot * E + E / 2 : (ok_b ? vb : 0) * (E / 2);
 
-  float acc[OP == kNormBwd ? 2 : 1][OP == kNormBwd ? 2 * E : 1];
-  if constexpr (OP == kNormBwd) {
+  // the workgroups of q, then those of k
+  const int t = blockIdx.x >= job.grid_q;
+  const int wg = blockIdx.x - (t ? job.grid_q : 0);
+  const int wgs = t ? gridDim.x - job.grid_q : job.grid_q;
+  const int H = job.H[t];
+  const uint32_t magic = job.magic[t];
+  const Heads in = job.in[t], out = job.out[t];
+
+  float w[OP == kRope ? 1 : 2 * E];
+  if constexpr (OP != kRope) {
+    const Vec wa = load_vec((const char *)job.w[t] + va * 16);
+    const Vec wb = load_vec((const char *)job.w[t] + vb * 16);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 2 * E; ++i) acc[t][i] = 0.f;
+    for (int i = 0; i < E; ++i) {
+      w[i] = elem<T>(wa, i);
+      w[E + i] = elem<T>(wb, i);
+    }
   }
+  float acc[OP == kNormBwd ? 2 * E : 1] = {};
 
-  for (int64_t blk = blockIdx.x; blk < job.blocks; blk += gridDim.x) {
-    const int b = (int)(blk / job.blocks_n);
-    const int n0 = (int)(blk - (int64_t)b * job.blocks_n) * job.tb;
-    const int tb = min(job.tb, job.N - n0);
-
-    auto at = [&](const Heads &h, int tok, int head) {
-      return (b * h.batch + (int64_t)(n0 + tok) * h.token +
-              (int64_t)head * h.head) * 16;
-    };
-    auto load = [&](int t, int row0) {
-      Row r;
-      const int H = job.H[t];
-      r.live = row0 + group < tb * H;
-      const int row = r.live ? row0 + group : 0;
-      r.tok = H == 1 ? row : (int)__umulhi((uint32_t)row, job.magic[t]);
-      r.head = row - r.tok * H;
-      const char *src = job.in[t].data + at(job.in[t], r.tok, r.head);
+  auto load = [&](const Block &k, int row0) {
+    Row r;
+    r.live = row0 + group < k.tb * H;
+    const int row = r.live ? row0 + group : 0;
+    r.tok = H == 1 ? row : (int)__umulhi((uint32_t)row, magic);
+    r.head = row - r.tok * H;
+    const char *src = in.data + k.at(in, r.tok, r.head);
+    const char *dy = nullptr;
+    if constexpr (OP == kNormBwd)
+      dy = job.dy[t].data + k.at(job.dy[t], r.tok, r.head);
+    if (job.cached) {
+      r.xa = load_vec(src + va * 16);
+      r.xb = load_vec(src + vb * 16);
+      if constexpr (OP == kNormBwd) {
+        r.ya = load_vec(dy + va * 16);
+        r.yb = load_vec(dy + vb * 16);
+      }
+    } else {
       r.xa = load_stream(src + va * 16);
       r.xb = load_stream(src + vb * 16);
       if constexpr (OP == kNormBwd) {
-        const char *dy = job.dy[t].data + at(job.dy[t], r.tok, r.head);
         r.ya = load_stream(dy + va * 16);
         r.yb = load_stream(dy + vb * 16);
       }
-      return r;
-    };
-
-    // the first rows are on their way while the sines are computed
-    Row next = {};
-    if (job.H[0] > 0) next = load(0, 0);
-
-    // the sines of the block's tokens; pairs past the rotated ones turn by 0
-    const int32_t *pos = job.pos + b * job.pos_batch + (int64_t)n0 * job.axes;
-    for (int i = tid; i < tb * kPitch; i += kBlock) {
+    }
+    return r;
+  };
+  // the sines of a block's tokens; pairs past the rotated ones turn by 0
+  auto sines = [&](const Block &k, float2 *table) {
+    const int32_t *pos =
+        job.pos + k.b * job.pos_batch + (int64_t)k.n0 * job.axes;
+    for (int i = tid; i < k.tb * kPitch; i += kBlock) {
       const int tok = i / kPitch;
       const int j = i % kPitch;
       float2 cs = {1.f, 0.f};
@@ -262,120 +292,161 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
       }
       table[i] = cs;
     }
-    __syncthreads();
+  };
 
+  // One barrier per block: the sines of the next one go to the other half of
+  // the table, and its first rows are on their way, before the present one is
+  // done.
+  Block k(job, wg);
+  Row next = load(k, 0);
+  sines(k, tables);
+  int half = 0;
+  for (int64_t blk = wg; blk < job.blocks; blk += wgs) {
+    const float2 *table = tables + half * job.tb * kPitch;
+    half ^= 1;
+    __syncthreads();
+    const bool more = blk + wgs < job.blocks;
+    const Block after(job, more ? blk + wgs : blk);
+    if (more) sines(after, tables + half * job.tb * kPitch);
+    const int rows = k.tb * H;
+    for (int row0 = 0; row0 < rows; row0 += kRows) {
+      Row r = next;
+      if (row0 + kRows < rows)
+        next = load(k, row0 + kRows);
+      else if (more)
+        next = load(after, 0);
+      float2 cs[E];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int rows = tb * job.H[t];
-      if (rows == 0) continue;
-      float w[OP == kRope ? 1 : 2 * E];
-      if constexpr (OP != kRope) {
-        const Vec wa = load_vec((const char *)job.w[t] + va * 16);
-        const Vec wb = load_vec((const char *)job.w[t] + vb * 16);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          w[i] = elem<T>(wa, i);
-          w[E + i] = elem<T>(wb, i);
-        }
+      for (int i = 0; i < E / 2; ++i) {
+        cs[i] = table[r.tok * kPitch + ta + i];
+        cs[E / 2 + i] = table[r.tok * kPitch + tbl + i];
       }
-      if (t == 1) next = load(1, 0);
-      for (int row0 = 0; row0 < rows; row0 += kRows) {
-        Row r = next;
-        if (row0 + kRows < rows) next = load(t, row0 + kRows);
-        float2 cs[E];
+      if (!ok_a) r.xa = vzero(), r.ya = vzero();
+      if (!ok_b) r.xb = vzero(), r.yb = vzero();
+      float fa[E], fb[E];
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          cs[i] = table[r.tok * kPitch + ta + i];
-          cs[E / 2 + i] = table[r.tok * kPitch + tbl + i];
-        }
-        if (!ok_a) r.xa = vzero(), r.ya = vzero();
-        if (!ok_b) r.xb = vzero(), r.yb = vzero();
-        float fa[E], fb[E];
+      for (int i = 0; i < E; ++i) {
+        fa[i] = elem<T>(r.xa, i);
+        fb[i] = elem<T>(r.xb, i);
+      }
+      if constexpr (OP != kRope) {
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          fa[i] = elem<T>(r.xa, i);
-          fb[i] = elem<T>(r.xb, i);
-        }
-        if constexpr (OP != kRope) {
-          float ss = 0.f;
+        for (int i = 0; i < E; ++i) ss = fmaf(fa[i], fa[i], ss);
 #pragma unroll
-          for (int i = 0; i < E; ++i) ss = fmaf(fa[i], fa[i], ss);
+        for (int i = 0; i < E; ++i) ss = fmaf(fb[i], fb[i], ss);
+        if constexpr (OP == kNormFwd) {
+          ss = lanes_sum<L>(ss);
+          const float s = rsqrtf(fmaf(ss, job.inv_d, job.eps));
 #pragma unroll
-          for (int i = 0; i < E; ++i) ss = fmaf(fb[i], fb[i], ss);
-          if constexpr (OP == kNormFwd) {
-            ss = lanes_sum<L>(ss);
-            const float s = rsqrtf(fmaf(ss, job.inv_d, job.eps));
+          for (int i = 0; i < E; ++i) {
+            fa[i] = fa[i] * s * w[i];
+            fb[i] = fb[i] * s * w[E + i];
+          }
+          rotate<E, HALF>(fa, fb, cs);
+        } else {
+          float ga[E], gb[E];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              fa[i] = fa[i] * s * w[i];
-              fb[i] = fb[i] * s * w[E + i];
-            }
-            rotate<E, HALF>(fa, fb, cs);
-          } else {
-            float ga[E], gb[E];
+          for (int i = 0; i < E; ++i) {
+            ga[i] = elem<T>(r.ya, i);
+            gb[i] = elem<T>(r.yb, i);
+          }
+          rotate<E, HALF>(ga, gb, cs);
+          // t * x is what both sums need
+          float pa[E], pb[E], sg = 0.f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              ga[i] = elem<T>(r.ya, i);
-              gb[i] = elem<T>(r.yb, i);
-            }
-            rotate<E, HALF>(ga, gb, cs);
-            float sg = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-              sg = fmaf(ga[i] * w[i], fa[i], sg);
-              sg = fmaf(gb[i] * w[E + i], fb[i], sg);
-            }
-            ss = lanes_sum<L>(ss);
-            sg = lanes_sum<L>(sg);
-            const float s = rsqrtf(fmaf(ss, job.inv_d, job.eps));
-            const float m = sg * s * s * job.inv_d;  // r * mean(g * xh)
+          for (int i = 0; i < E; ++i) {
+            pa[i] = ga[i] * fa[i];
+            pb[i] = gb[i] * fb[i];
+            sg = fmaf(pa[i], w[i], sg);
+            sg = fmaf(pb[i], w[E + i], sg);
+          }
+          ss = lanes_sum<L>(ss);
+          sg = lanes_sum<L>(sg);
+          const float s = rsqrtf(fmaf(ss, job.inv_d, job.eps));
+          const float m = sg * s * s * job.inv_d;  // r * mean(g * xh)
+          if (r.live) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-              if (r.live) {
-                acc[t][i] = fmaf(ga[i], fa[i] * s, acc[t][i]);
-                acc[t][E + i] = fmaf(gb[i], fb[i] * s, acc[t][E + i]);
-              }
-              fa[i] = s * (ga[i] * w[i] - fa[i] * m);
-              fb[i] = s * (gb[i] * w[E + i] - fb[i] * m);
+              acc[i] = fmaf(pa[i], s, acc[i]);
+              acc[E + i] = fmaf(pb[i], s, acc[E + i]);
             }
           }
-        } else {
-          rotate<E, HALF>(fa, fb, cs);
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            fa[i] = s * (ga[i] * w[i] - fa[i] * m);
+            fb[i] = s * (gb[i] * w[E + i] - fb[i] * m);
+          }
         }
-        char *dst = const_cast<char *>(job.out[t].data) +
-                    at(job.out[t], r.tok, r.head);
-        if (r.live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
-        if (r.live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
+      } else {
+        rotate<E, HALF>(fa, fb, cs);
       }
+      char *dst = const_cast<char *>(out.data) + k.at(out, r.tok, r.head);
+      if (r.live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
+      if (r.live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
     }
-    __syncthreads();
+    k = after;
   }
 
   // One partial row of dw per workgroup: the lane groups of a wavefront are
   // added by a butterfly, the four wavefronts in order through LDS.
   if constexpr (OP == kNormBwd) {
-    __shared__ float stage[4][2][2 * L * E];
+    __shared__ float stage[4][2 * L * E];
     const int wave = wave_id();
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < 2 * E; ++i) {
+      float v = acc[i];
 #pragma unroll
-      for (int i = 0; i < 2 * E; ++i) {
-        float v = acc[t][i];
-#pragma unroll
-        for (int o = L; o < kWave; o *= 2) v += __shfl_xor(v, o);
-        const bool ok = i < E ? ok_a : ok_b;
-        if (ok && lane_id() < L)
-          stage[wave][t][(i < E ? va : vb) * E + i % E] = v;
-      }
-    __syncthreads();
-    for (int i = tid; i < 2 * job.d; i += kBlock) {
-      const int t = i >= job.d;
-      const int c = i - t * job.d;
-      if (job.H[t] > 0)
-        job.part[t][(int64_t)blockIdx.x * job.d + c] =
-            ((stage[0][t][c] + stage[1][t][c]) + stage[2][t][c]) +
-            stage[3][t][c];
+      for (int o = L; o < kWave; o *= 2) v += __shfl_xor(v, o);
+      const bool ok = i < E ? ok_a : ok_b;
+      if (ok && lane_id() < L) stage[wave][(i < E ? va : vb) * E + i % E] = v;
     }
+    __syncthreads();
+    float *part = job.part[t] + (int64_t)wg * job.d;
+    for (int c = tid; c < job.d; c += kBlock)
+      part[c] = ((stage[0][c] + stage[1][c]) + stage[2][c]) + stage[3][c];
+  }
+}
+
+// dw = the sum of a tensor's partial rows, in a fixed order: slice s of 64
+// adds rows s, s + 64, ..., then the slices are added in order.  A workgroup
+// per tensor and 16 features; zero where there are no rows.
+constexpr int kSumSlices = 64;
+constexpr int kSumCols = 16;
+
+struct Sums {
+  const float *part[2];
+  float *dw[2];
+  int32_t rows[2];
+  int32_t d;
+};
+
+__global__ __launch_bounds__(kSumSlices * kSumCols) void sum_kernel(Sums p) {
+  __shared__ float stage[kSumSlices][kSumCols];
+  const int per = (p.d + kSumCols - 1) / kSumCols;
+  const int t = blockIdx.x / per;
+  if (p.dw[t] == nullptr) return;
+  const int c = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
+  const int f = (blockIdx.x - t * per) * kSumCols + c;
+  float v = 0.f;
+  if (f < p.d) {
+    const float *src = p.part[t] + f;
+    int r = slice;
+    for (; r + 3 * kSumSlices < p.rows[t]; r += 4 * kSumSlices) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = src[(int64_t)(r + i * kSumSlices) * p.d];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v += x[i];
+    }
+    for (; r < p.rows[t]; r += kSumSlices) v += src[(int64_t)r * p.d];
+  }
+  stage[slice][c] = v;
+  __syncthreads();
+  if (slice == 0 && f < p.d) {
+    for (int s = 1; s < kSumSlices; ++s) v += stage[s][c];
+    p.dw[t][f] = v;
   }
 }
 
@@ -488,40 +559,63 @@ Heads heads_of(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
   return h;
 }
 
-// Tokens per block.
-int block_tokens(int64_t B, int64_t N) {
-  int tb = kMaxTokens;
-  while (tb > 1 && B * ((N + tb - 1) / tb) < 4 * kCUs) tb /= 2;
-  return tb;
-}
-
-struct HeadsPlan {
-  int tb;
-  int64_t blocks_n;
-  int64_t blocks;
-  int64_t grid;
-};
-
-// The backward of the norm runs a persistent grid of 4 workgroups per CU, so
-// that each adds up dw over many blocks before it writes its partial row.
-HeadsPlan heads_plan(int64_t B, int64_t N, bool bwd) {
-  HeadsPlan p;
-  p.tb = block_tokens(B, N);
-  p.blocks_n = (N + p.tb - 1) / p.tb;
-  p.blocks = B * p.blocks_n;
-  p.grid = std::min<int64_t>(p.blocks, bwd ? 4 * kCUs : kMaxGrid);
-  return p;
-}
-
 int lanes_per_head(int nvec) {
   int L = 1;
   while (2 * L < nvec) L *= 2;
   return L;
 }
 
+struct HeadsPlan {
+  int tb;            // tokens per block
+  int64_t blocks_n;  // blocks per sample
+  int64_t blocks;
+  int64_t grid[2];   // workgroups of q and of k
+};
+
+// A block has up to kBlockRows rows for each lane group of a workgroup, and
+// fewer where the GPU would not be filled: short blocks keep the window of
+// memory that is read and written at a time small.  Measured on MI355X (bf16,
+// 128 features): 32760 tokens x 24 heads rotated, 16 tokens per block 74.6
+// us, 8 (96 rows of 32 lane groups) 69.0; norm and rotation of 75600 x 80
+// heads, 16 tokens 583 us, 4 (160 rows) 536, 2 (80 rows) 534.
+// The backward of the norm runs a persistent grid, so that each workgroup
+// adds up dw over many blocks before it writes its partial row: 6 per CU,
+// twice what its registers admit at a time, evens out the end (75600 x 80
+// heads: 3 per CU 817 us, 6 per CU 807).  q and k share it by their numbers
+// of heads.
+HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
+                     int dtype, bool bwd) {
+  HeadsPlan p;
+  const int rows = kBlock / lanes_per_head((int)(d / elems_per_vec(dtype)));
+  const int tensors = (Hq > 0) + (Hk > 0);
+  p.tb = kMaxTokens;
+  while (p.tb > 1 && (p.tb * std::max(Hq, Hk) > kBlockRows * rows ||
+                      tensors * B * ((N + p.tb - 1) / p.tb) <
+                          kFillBlocks * kCUs))
+    p.tb /= 2;
+  p.blocks_n = (N + p.tb - 1) / p.tb;
+  p.blocks = B * p.blocks_n;
+  const int64_t most = bwd ? kBwdPerCu * kCUs : kMaxGrid;
+  const int64_t all = std::min(most, tensors * p.blocks);
+  p.grid[0] = Hq == 0 ? 0 : Hk == 0 ? all : all * Hq / (Hq + Hk);
+  if (Hq > 0) p.grid[0] = std::max<int64_t>(1, std::min(p.grid[0], p.blocks));
+  p.grid[1] = Hk == 0 ? 0
+                      : std::max<int64_t>(
+                            1, std::min(all - p.grid[0], p.blocks));
+  return p;
+}
+
+// Inputs that another kernel has just written may still lie in the 256 MB
+// Infinity Cache; the streaming hint reads past it.  Up to twice its size of
+// bytes read and written, plain loads win (MI355X: backward of 24960 tokens x
+// 24 heads of 128 bf16, 460 MB, 86 -> 80 us; of 3554 tokens x 15 heads of 72
+// f32 17 -> 13 us); past it the hint does (75600 tokens x 80 heads, 4.6 GB:
+// 837 -> 806 us).
+constexpr int64_t kCachedBytes = int64_t(512) << 20;
+
 void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
-              bool inverse, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
-              int dtype) {
+              bool inverse, int tensors, int64_t B, int64_t N, int64_t Hq,
+              int64_t Hk, int64_t d, int dtype) {
   const int E = elems_per_vec(dtype);
   const int64_t H[2] = {Hq, Hk};
   for (int t = 0; t < 2; ++t) {
@@ -538,8 +632,10 @@ void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
   job.nvec = (int32_t)(d / E);
   job.rot_vecs = rot->layout == ADALN_ROPE_HALF ? rot->pairs / E : 0;
   job.tb = p.tb;
+  job.grid_q = (int32_t)p.grid[0];
   job.blocks_n = (int32_t)p.blocks_n;
   job.blocks = p.blocks;
+  job.cached = B * N * (Hq + Hk) * d * (16 / E) * tensors <= kCachedBytes;
   job.dir = inverse ? -1.f : 1.f;
   job.axes = rot->axes;
   job.pairs = rot->pairs;
@@ -581,7 +677,8 @@ void fill(AllAxes &r, const adaln_rotation_t *rot) {
 template <typename T, int OP, int L, typename ROT>
 hipError_t go(const Job &job, const ROT &rot, bool half, int64_t grid,
               hipStream_t stream) {
-  const size_t lds = (size_t)job.tb * L * Elems<T>::value * sizeof(float2);
+  const size_t lds =
+      (size_t)2 * job.tb * L * Elems<T>::value * sizeof(float2);
   return half ? launch_kernel_lds(heads_kernel<T, L, true, OP, ROT>, grid,
                                   kBlock, lds, stream, job, rot)
               : launch_kernel_lds(heads_kernel<T, L, false, OP, ROT>, grid,
@@ -652,14 +749,14 @@ int rope(const adaln_heads_t *q, const adaln_heads_t *k,
   ADALN_TRY(check_heads(q_out, B, N, Hq, d, dtype, true, "q_out"));
   ADALN_TRY(check_heads(k_out, B, N, Hk, d, dtype, true, "k_out"));
   if (!rows) return ok();
-  const HeadsPlan p = heads_plan(B, N, false);
+  const HeadsPlan p = heads_plan(B, N, Hq, Hk, d, dtype, false);
   Job job = {};
-  fill_job(job, p, rot, inverse, N, Hq, Hk, d, dtype);
+  fill_job(job, p, rot, inverse, 2, B, N, Hq, Hk, d, dtype);
   job.in[0] = heads_of(q, B, N, Hq, dtype);
   job.in[1] = heads_of(k, B, N, Hk, dtype);
   job.out[0] = heads_of(q_out, B, N, Hq, dtype);
   job.out[1] = heads_of(k_out, B, N, Hk, dtype);
-  ADALN_TRY(enqueue<kRope>(job, rot, p.grid, dtype,
+  ADALN_TRY(enqueue<kRope>(job, rot, p.grid[0] + p.grid[1], dtype,
                            (hipStream_t)stream, what));
   return ok();
 }
@@ -706,9 +803,9 @@ ADALN_API int adaln_qk_norm_rope_fwd(
   ADALN_TRY(check_weight(wq, rows && Hq > 0, "wq"));
   ADALN_TRY(check_weight(wk, rows && Hk > 0, "wk"));
   if (!rows) return ok();
-  const HeadsPlan p = heads_plan(B, N, false);
+  const HeadsPlan p = heads_plan(B, N, Hq, Hk, d, dtype, false);
   Job job = {};
-  fill_job(job, p, rot, false, N, Hq, Hk, d, dtype);
+  fill_job(job, p, rot, false, 2, B, N, Hq, Hk, d, dtype);
   job.in[0] = heads_of(q, B, N, Hq, dtype);
   job.in[1] = heads_of(k, B, N, Hk, dtype);
   job.out[0] = heads_of(q_out, B, N, Hq, dtype);
@@ -717,7 +814,7 @@ ADALN_API int adaln_qk_norm_rope_fwd(
   job.w[1] = wk;
   job.eps = eps;
   job.inv_d = 1.f / (float)d;
-  ADALN_TRY(enqueue<kNormFwd>(job, rot, p.grid, dtype,
+  ADALN_TRY(enqueue<kNormFwd>(job, rot, p.grid[0] + p.grid[1], dtype,
                               (hipStream_t)stream,
                               "adaln_qk_norm_rope_fwd launch"));
   return ok();
@@ -727,8 +824,9 @@ ADALN_API size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N,
                                                         int64_t Hq, int64_t Hk,
                                                         int64_t d, int dtype) {
   if (check_sizes(B, N, Hq, Hk, d, dtype) != ADALN_OK) return 0;
-  if (B * N == 0) return 0;
-  return (size_t)heads_plan(B, N, true).grid * 2 * (size_t)d * sizeof(float);
+  if (B * N == 0 || Hq + Hk == 0) return 0;
+  const HeadsPlan p = heads_plan(B, N, Hq, Hk, d, dtype, true);
+  return (size_t)(p.grid[0] + p.grid[1]) * (size_t)d * sizeof(float);
 }
 
 ADALN_API int adaln_qk_norm_rope_bwd(
@@ -754,9 +852,10 @@ ADALN_API int adaln_qk_norm_rope_bwd(
   ADALN_TRY(check_weight(dwq, Hq > 0, "dwq"));
   ADALN_TRY(check_weight(dwk, Hk > 0, "dwk"));
   if (Hq + Hk == 0) return ok();
-  const HeadsPlan p = heads_plan(B, N, true);
-  const int64_t grid = rows ? p.grid : 0;
-  const size_t need = (size_t)grid * 2 * (size_t)d * sizeof(float);
+  HeadsPlan p = {};
+  if (rows) p = heads_plan(B, N, Hq, Hk, d, dtype, true);
+  const size_t need =
+      (size_t)(p.grid[0] + p.grid[1]) * (size_t)d * sizeof(float);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
       return fail(ADALN_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s",
@@ -765,10 +864,10 @@ ADALN_API int adaln_qk_norm_rope_bwd(
     ADALN_TRY(check_weight(workspace, true, "workspace"));
   }
   float *part[2] = {static_cast<float *>(workspace),
-                    static_cast<float *>(workspace) + grid * d};
+                    static_cast<float *>(workspace) + p.grid[0] * d};
   if (rows) {
     Job job = {};
-    fill_job(job, p, rot, true, N, Hq, Hk, d, dtype);
+    fill_job(job, p, rot, true, 3, B, N, Hq, Hk, d, dtype);
     job.in[0] = heads_of(q, B, N, Hq, dtype);
     job.in[1] = heads_of(k, B, N, Hk, dtype);
     job.dy[0] = heads_of(dq_out, B, N, Hq, dtype);
@@ -781,17 +880,17 @@ ADALN_API int adaln_qk_norm_rope_bwd(
     job.part[1] = part[1];
     job.eps = eps;
     job.inv_d = 1.f / (float)d;
-    ADALN_TRY(enqueue<kNormBwd>(job, rot, grid, dtype,
+    ADALN_TRY(enqueue<kNormBwd>(job, rot, p.grid[0] + p.grid[1], dtype,
                                 (hipStream_t)stream,
                                 "adaln_qk_norm_rope_bwd launch"));
   }
-  // the sums over the workgroups' partial rows, in index order (a missing
-  // tensor's column takes the other one's)
-  const int a = Hq > 0 ? 0 : 1, b = Hk > 0 ? 1 : 0;
-  float *dw[2] = {dwq, dwk};
-  const hipError_t e =
-      launch_dmod_finish(part[a], part[b], dw[a], dw[b], 1, (int32_t)d,
-                         (int32_t)grid, (hipStream_t)stream);
+  Sums sums = {{part[0], part[1]},
+               {Hq > 0 ? dwq : nullptr, Hk > 0 ? dwk : nullptr},
+               {(int32_t)p.grid[0], (int32_t)p.grid[1]},
+               (int32_t)d};
+  const hipError_t e = launch_kernel_threads(
+      sum_kernel, 2 * ((d + kSumCols - 1) / kSumCols), kSumSlices * kSumCols,
+      (hipStream_t)stream, sums);
   if (e != hipSuccess) return hip_fail(e, "adaln_qk_norm_rope_bwd finish");
   return ok();
 }

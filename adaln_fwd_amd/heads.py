@@ -111,16 +111,17 @@ class _Call:
                              f"{tuple(like.shape)}")
         return _heads(t, name, self.lead, self.d, self.dt, self.dev)
 
-    def new(self, t, like):
-        """An output: as given, or a contiguous one."""
+    def out(self, t, like, name):
+        """An output and its descriptor: as given, or a contiguous one."""
         if like is None:
             if t is not None:
-                raise ValueError("an output was given for a missing input")
-            return None
-        if t is None:
-            t = torch.empty_like(like,
-                                 memory_format=torch.contiguous_format)
-        return t
+                raise ValueError(f"{name} was given for a missing input")
+            return None, None
+        if t is not None:
+            return t, self.heads(t, name, like)
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        row = like.shape[-2] * self.d
+        return t, _lib.Heads(_ptr(t), self.N * row, row, self.d)
 
     def sizes(self, stream):
         return (self.B, self.N, self.Hq, self.Hk, self.d, self.code,
@@ -135,11 +136,10 @@ def _rope(entry, q, k, pos, freqs, layout, q_out, k_out, stream):
     c = _Call(q, k, pos, freqs, layout)
     lib = _lib.load()
     with _on(c.dev, stream):
-        q_out, k_out = c.new(q_out, q), c.new(k_out, k)
-        rc = getattr(lib, entry)(
-            _ref(c.q), _ref(c.k), ctypes.byref(c.rot),
-            _ref(c.heads(q_out, "q_out", q)), _ref(c.heads(k_out, "k_out", k)),
-            *c.sizes(stream))
+        q_out, ho = c.out(q_out, q, "q_out")
+        k_out, hk = c.out(k_out, k, "k_out")
+        rc = getattr(lib, entry)(_ref(c.q), _ref(c.k), ctypes.byref(c.rot),
+                                 _ref(ho), _ref(hk), *c.sizes(stream))
     _lib.check(rc, entry)
     return q_out, k_out
 
@@ -181,11 +181,11 @@ def qk_norm_rope_fwd(q, k, wq, wk, pos: torch.Tensor, freqs, *,
     _weights(c, wq, wk)
     lib = _lib.load()
     with _on(c.dev, stream):
-        q_out, k_out = c.new(q_out, q), c.new(k_out, k)
+        q_out, ho = c.out(q_out, q, "q_out")
+        k_out, hk = c.out(k_out, k, "k_out")
         rc = lib.adaln_qk_norm_rope_fwd(
             _ref(c.q), _ref(c.k), _ptr(wq), _ptr(wk), eps, ctypes.byref(c.rot),
-            _ref(c.heads(q_out, "q_out", q)), _ref(c.heads(k_out, "k_out", k)),
-            *c.sizes(stream))
+            _ref(ho), _ref(hk), *c.sizes(stream))
     _lib.check(rc, "adaln_qk_norm_rope_fwd")
     return q_out, k_out
 
@@ -215,7 +215,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos: torch.Tensor, freqs, *,
     need = int(lib.adaln_qk_norm_rope_bwd_workspace_bytes(
         c.B, c.N, c.Hq, c.Hk, c.d, c.code))
     with _on(c.dev, stream):
-        dq, dk = c.new(dq, q), c.new(dk, k)
+        dq, ho = c.out(dq, q, "dq")
+        dk, ko = c.out(dk, k, "dk")
         if q is not None and dwq is None:
             dwq = torch.empty(c.d, dtype=torch.float32, device=c.dev)
         if k is not None and dwk is None:
@@ -231,8 +232,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos: torch.Tensor, freqs, *,
                              f"{c.dev}")
         rc = lib.adaln_qk_norm_rope_bwd(
             _ref(hq), _ref(hk), _ref(c.q), _ref(c.k), _ptr(wq), _ptr(wk), eps,
-            ctypes.byref(c.rot), _ref(c.heads(dq, "dq", q)),
-            _ref(c.heads(dk, "dk", k)), _ptr(dwq), _ptr(dwk), _ptr(workspace),
+            ctypes.byref(c.rot), _ref(ho), _ref(ko), _ptr(dwq), _ptr(dwk),
+            _ptr(workspace),
             workspace.numel() * workspace.element_size(), *c.sizes(stream))
     _lib.check(rc, "adaln_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
