@@ -200,8 +200,9 @@ struct Row {
 struct Block {
   int b, n0, tb;
   __device__ __forceinline__ Block(const Job &job, int64_t blk) {
-    b = (int)(blk / job.blocks_n);
-    n0 = (int)(blk - (int64_t)b * job.blocks_n) * job.tb;
+    // (fewer than 2^31 blocks: as many tokens)
+    b = (int)((uint32_t)blk / (uint32_t)job.blocks_n);
+    n0 = ((int)blk - b * job.blocks_n) * job.tb;
     tb = min(job.tb, job.N - n0);
   }
   __device__ __forceinline__ int64_t at(const Heads &h, int tok,

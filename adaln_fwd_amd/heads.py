@@ -43,18 +43,20 @@ def _heads(t, name, lead, d, dtype, device) -> Optional[_lib.Heads]:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if device.type != "cuda":
-        raise ValueError(f"{name} must be a GPU tensor, got {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.dim() != len(lead) + 2 or tuple(t.shape[:-2]) != lead \
-            or t.shape[-1] != d:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"{lead + ('H', d)}")
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    shape, st = t.shape, t.stride()
+    # (one condition for calls that are right; which one failed comes after)
+    if not (t.dtype is dtype and t.device == device and t.is_cuda
+            and len(shape) == len(lead) + 2 and shape[:-2] == lead
+            and shape[-1] == d and (st[-1] == 1 or d == 1)):
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor, got {device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != d:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected "
+                             f"{tuple(lead) + ('H', d)}")
         raise ValueError(f"{name}: the features of a head must be contiguous")
     return _lib.Heads(_ptr(t), st[0] if len(lead) == 2 else 0, st[-3], st[-2])
 
@@ -72,14 +74,15 @@ class _Call:
         if ref.dim() not in (3, 4):
             raise ValueError("q and k must be [B, N, H, d] or [T, H, d], got "
                              f"shape {tuple(ref.shape)}")
+        shape = ref.shape
         self.dev, self.dt = ref.device, ref.dtype
         self.code = _code(ref)
-        self.lead, self.d = tuple(ref.shape[:-2]), ref.shape[-1]
-        self.B = self.lead[0] if len(self.lead) == 2 else 1
-        self.N = self.lead[-1]
+        self.lead, self.d = shape[:-2], shape[-1]
+        self.B = shape[0] if len(shape) == 4 else 1
+        self.N = N = shape[-3]
+        self.q = _heads(q, "q", self.lead, self.d, self.dt, self.dev)
+        self.k = _heads(k, "k", self.lead, self.d, self.dt, self.dev)
         self.Hq = q.shape[-2] if q is not None else 0
-        self.q = self.heads(q, "q")
-        self.k = self.heads(k, "k")
         self.Hk = k.shape[-2] if k is not None else 0
         if layout not in _LAYOUTS:
             raise ValueError("layout must be 'interleaved' or 'half', got "
@@ -97,13 +100,12 @@ class _Call:
         axes, pairs = self.freqs.shape
         if not isinstance(pos, torch.Tensor):
             raise TypeError("pos must be a torch.Tensor")
-        shared = tuple(pos.shape) == (self.N, axes)
-        _check(pos, "pos",
-               (self.N, axes) if shared or len(self.lead) == 1
-               else (self.B, self.N, axes), torch.int32, self.dev)
-        self.rot = _lib.Rotation(_ptr(pos), 0 if shared else self.N * axes,
-                                 self.freqs.ctypes.data, axes, pairs,
-                                 _LAYOUTS[layout])
+        shared = pos.dim() == 2 or len(shape) == 3
+        _check(pos, "pos", (N, axes) if shared else (self.B, N, axes),
+               torch.int32, self.dev)
+        self.rot = _lib.Rotation(_ptr(pos), 0 if shared else N * axes,
+                                 self.freqs.__array_interface__["data"][0],
+                                 axes, pairs, _LAYOUTS[layout])
 
     def heads(self, t, name, like=None):
         if like is not None and t is not None and t.shape != like.shape:
@@ -172,6 +174,18 @@ def _weights(c, wq, wk):
         _check(wk, "wk", (c.d,), c.dt, c.dev)
 
 
+def _dw(dw, w, name, x, c):
+    """A weight's gradient: as given, or a new one; None for a missing x."""
+    if x is None:
+        if dw is not None:
+            raise ValueError(f"{name} was given for a missing input")
+        return None
+    if dw is None:
+        return w.new_empty(c.d, dtype=torch.float32)
+    _check(dw, name, (c.d,), torch.float32, c.dev)
+    return dw
+
+
 def qk_norm_rope_fwd(q, k, wq, wk, pos: torch.Tensor, freqs, *,
                      eps: float = 1e-6, layout: str = "interleaved",
                      q_out=None, k_out=None, stream=None):
@@ -217,23 +231,20 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, pos: torch.Tensor, freqs, *,
     with _on(c.dev, stream):
         dq, ho = c.out(dq, q, "dq")
         dk, ko = c.out(dk, k, "dk")
-        if q is not None and dwq is None:
-            dwq = torch.empty(c.d, dtype=torch.float32, device=c.dev)
-        if k is not None and dwk is None:
-            dwk = torch.empty(c.d, dtype=torch.float32, device=c.dev)
-        for t, name in ((dwq, "dwq"), (dwk, "dwk")):
-            if t is not None:
-                _check(t, name, (c.d,), torch.float32, c.dev)
+        dwq = _dw(dwq, wq, "dwq", q, c)
+        dwk = _dw(dwk, wk, "dwk", k, c)
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8,
-                                    device=c.dev)
-        if workspace.device != c.dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on "
-                             f"{c.dev}")
+            wbytes = max(need, 1)
+            workspace = (q if q is not None else k).new_empty(
+                wbytes, dtype=torch.uint8)
+        else:
+            if workspace.device != c.dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on "
+                                 f"{c.dev}")
+            wbytes = workspace.numel() * workspace.element_size()
         rc = lib.adaln_qk_norm_rope_bwd(
             _ref(hq), _ref(hk), _ref(c.q), _ref(c.k), _ptr(wq), _ptr(wk), eps,
             ctypes.byref(c.rot), _ref(ho), _ref(ko), _ptr(dwq), _ptr(dwk),
-            _ptr(workspace),
-            workspace.numel() * workspace.element_size(), *c.sizes(stream))
+            _ptr(workspace), wbytes, *c.sizes(stream))
     _lib.check(rc, "adaln_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk

@@ -295,9 +295,11 @@ int adaln_bwd_segments(const void *dy, const void *x, const void *scale,
  * adaln_heads describes one such tensor: its first element and the distances,
  * in elements, between samples, tokens and heads (multiples of 8 for bf16, 4
  * for f32; the distance along a dimension of size one is not read).  Inputs
- * may repeat (a distance of 0); the heads of an output must not overlap.  An
- * output may be its own input, with the same distances; any other overlap of
- * an output with an input is an error that the library cannot see.
+ * may repeat (a distance of 0; a gradient is then that of each repetition, for
+ * the caller to add); the heads of an output must not overlap.  An output may
+ * be its own input with the same distances: q_out may be q, dq may be dq_out
+ * or q, and so for k.  Any other overlap of an output with an input or with
+ * the other output is an error that the library cannot see.
  */
 typedef struct adaln_heads {
   void *data; /* device, 16-byte aligned; NULL if there are no heads */

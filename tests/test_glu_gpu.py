@@ -251,3 +251,56 @@ def test_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(outs, other):
             assert torch.equal(a, b), i
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share nothing but their inputs."""
+    _say("two streams")
+    dh, x, wg, wu = [t.cuda() for t in _real(500, 512, 776, 6)]
+
+    def run(x, **kw):
+        h, saved = A.glu_fwd(x, wg, wu, save=True, **kw)
+        return [h, *A.glu_bwd(dh, x, wg, wu, saved, **kw)]
+
+    y = x.flip(0).contiguous()
+    want = [run(x), run(y)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, v in enumerate((x, y)):
+            got[i].append(run(v, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            for a, b in zip(r, want[i]):
+                assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 hidden elements: the last tokens' outputs, and the
+    weights' gradients of the last hidden features, exactly."""
+    M, D, F = 270000, 64, 16384
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    _say(f"M*F = {M * F}")
+    _, x, wg, wu = [t.cuda() for t in _whole(1000, D, F, 5)]
+    x = x.repeat(M // 1000, 1)
+    dh = torch.randint(-1, 2, (1000, F), device="cuda",
+                       dtype=torch.int8).to(torch.bfloat16)
+    dh = dh.repeat(M // 1000, 1)
+    h = A.glu_fwd(x, wg, wu)
+    dx, dwg, dwu = A.glu_bwd(dh, x, wg, wu)
+    last = slice(M - 1000, M)
+    xf, wgf, wuf, df = [t.double() for t in (x[last], wg, wu, dh[last])]
+    G, U = xf @ wgf.t(), xf @ wuf.t()
+    assert torch.equal(h[last], (G * U).to(torch.bfloat16))
+    assert torch.equal(h[:1000], h[last])
+    want = (df * U) @ wgf + (df * G) @ wuf
+    assert torch.equal(dx[last], want.float().to(torch.bfloat16))
+    assert torch.equal(dx[:1000], dx[last])
+    # every thousand tokens are alike: 270 times the sums of one thousand
+    for got, l in ((dwg, df * U), (dwu, df * G)):
+        want = 270 * (l.t() @ xf)
+        assert want.abs().max() < 2 ** 24
+        assert torch.equal(got, want.float().to(torch.bfloat16))

@@ -343,3 +343,62 @@ def test_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(outs, other if i == 1 else want):
             assert torch.equal(a, b), i
+
+
+def test_backward_in_place():
+    """dq written over dq_out, dk over k."""
+    _say("backward in place")
+    h = _inputs(2, 501, 3, 2, 72, "bf16")
+    x = {n: v.cuda() for n, v in h.items()}
+    pos = torch.arange(501, dtype=torch.int32).reshape(-1, 1).cuda()
+    f = _freqs(36, 1)
+    args = [x[n] for n in ("dq", "dk", "q", "k", "wq", "wk")]
+    want = A.qk_norm_rope_bwd(*args, pos, f)
+    got = A.qk_norm_rope_bwd(*args, pos, f, dq=x["dq"], dk=x["k"])
+    assert got[0] is x["dq"] and got[1] is x["k"]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_more_frequencies_than_the_small_form_holds():
+    """Pairs turned by several axes at once, and more than 64 pairs: the same
+    angles whichever way the table travels."""
+    _say("dense table")
+    h = _inputs(1, 60, 2, 1, 128, "f32")
+    q, k = h["q"].cuda(), h["k"].cuda()
+    g = torch.Generator().manual_seed(8)
+    pos = torch.randint(0, 64, (60, 3), generator=g, dtype=torch.int32)
+    dense = torch.rand(3, 64, generator=g, dtype=torch.float64).numpy() - 0.5
+    got = A.rope_fwd(q, k, pos.cuda(), dense)
+    ang = R.angles(pos, dense)
+    for a, n in zip(got, "qk"):
+        f = h[n].double()
+        _close(a, R.rotate(f, ang, "interleaved"), _rows_max(f), n, 200)
+    # one axis split over two columns of positions: the sum is the same angle
+    one = _freqs(64, 1)
+    two = np.concatenate([one, one])
+    a = A.rope_fwd(q, k, pos[:, :1].contiguous().cuda() * 2, one)
+    b = A.rope_fwd(q, k, pos[:, :1].expand(60, 2).contiguous().cuda(), two)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams share nothing."""
+    _say("two streams")
+    h = _inputs(1, 3000, 8, 8, 128, "bf16")
+    x = [h[n].cuda() for n in ("q", "k", "dq", "dk", "wq", "wk")]
+    y = [t.flip(0, 1).contiguous() if t.dim() == 4 else t for t in x]
+    pos = torch.arange(3000, dtype=torch.int32).reshape(-1, 1).cuda()
+    f = _freqs(64, 1)
+    want = [_everything(*v, pos, f, "half") for v in (x, y)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, v in enumerate((x, y)):
+            got[i].append(_everything(*v, pos, f, "half", stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            for a, b in zip(run, want[i]):
+                assert torch.equal(a, b)
