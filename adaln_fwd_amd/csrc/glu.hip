@@ -5,17 +5,18 @@
 //     dU = dh * act(G), dG = dh * U * act'(G)
 //     dx = dG Wg + dU Wu,  dWg = dG^T x,  dWu = dU^T x
 //
-// Four products of one shape of loop, all on the matrix cores (bf16 operands,
-// float32 sums): a workgroup computes a tile of rows x columns, walking the
-// summed dimension in steps of 64.  Each step's two operand tiles go from
+// Four products of one shape of loop, all on the matrix cores (bf16 or f32
+// operands, float32 sums): a workgroup computes a tile of rows x columns,
+// walking the summed dimension in steps of 128 bytes.  Each step's two operand tiles go from
 // memory straight to LDS (16 bytes per lane, no registers), double-buffered:
 // the loads of step s + 1 are in flight while step s is multiplied.
 //
 // An operand is stored with the summed dimension contiguous (x and W in the
 // forward) or across it (W in dx; both in dW).  Its LDS tile keeps the
-// memory's order, 128-byte rows of 64 summed elements or rows of 128 or 256
+// memory's order, 128-byte rows of summed elements or rows of 128 or 256
 // columns, and the fragment reads do the rest: 16 bytes of a row as they are,
-// or 4 x 16 blocks transposed by the LDS read itself.  The 16-byte pieces of
+// or, across, 4 x 16 blocks of bf16 transposed by the LDS read itself, or f32
+// elements one by one.  The 16-byte pieces of
 // a row are permuted by an exclusive or with bits of the row's number, so
 // that the lanes of a read meet distinct banks; the loads apply the same
 // permutation to the addresses they read from, since they can only fill LDS
@@ -38,14 +39,15 @@ namespace adaln {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kStep = 64;  // summed elements per step
+// Summed elements per step: 128 bytes of them.
+template <typename T>
+constexpr int kStep = 128 / sizeof(T);
 
 // 16 bytes per lane from memory to LDS at `lds` + 16 * lane: a wave-uniform
 // base and a 32-bit offset per lane.  Outstanding loads are waited for by
@@ -74,18 +76,47 @@ __device__ __forceinline__ void arrive() {
       : "memory");
 }
 
-// An operand whose summed dimension is contiguous: ROWS rows of kStep
-// elements, 128 bytes each, 8 pieces of 16.  Row r keeps its piece c at
-// c ^ ((r >> 1) & 7): 16 consecutive rows then cover all banks.  Rows past
-// the operand's last repeat it (their products are not stored); past the end
-// of the sum, `left` elements into the step, a lane loads the last piece
-// again, and clear() puts zeros in its place.
-template <int ROWS, int WAVES>
+// A lane's part of a fragment of 32 rows or columns: 16 bytes, the elements
+// 8 (l / 32) + [0, 8) of 16 (bf16) or 4 (l / 32) + [0, 4) of 8 (f32) of row
+// l % 32.
+template <typename T>
+struct Frag;
+template <>
+struct Frag<bf16> {
+  bf16x8 v;
+};
+template <>
+struct Frag<float> {
+  f32x4 v;
+};
+
+// acc += a b^T over the fragments' summed elements.  (f32: the cores take two
+// elements at a time, one of each half of the lanes; any pairing of elements
+// does as long as both operands have the same.)
+__device__ __forceinline__ void multiply_add(f32x16 &acc, const Frag<bf16> &a,
+                                             const Frag<bf16> &b) {
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void multiply_add(f32x16 &acc,
+                                             const Frag<float> &a,
+                                             const Frag<float> &b) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[c], b.v[c], acc, 0, 0, 0);
+}
+
+// An operand whose summed dimension is contiguous: ROWS rows of a step's 128
+// bytes, 8 pieces of 16.  Row r keeps its piece c at c ^ ((r >> 1) & 7): 16
+// consecutive rows then cover all banks.  Rows past the operand's last repeat
+// it (their products are not stored); past the end of the sum, `left`
+// elements into the step, a lane loads the last piece again, and clear() puts
+// zeros in its place.
+template <typename T, int ROWS, int WAVES>
 struct Along {
-  static constexpr int kBytes = ROWS * kStep * 2;
+  static constexpr int E = Elems<T>::value;
+  static constexpr int kBytes = ROWS * 128;
   static constexpr int kLoads = ROWS / (8 * WAVES);
-  static constexpr int kReads = 1;  // LDS reads per fragment
-  uint32_t off[kLoads];             // byte offset of each load's row
+  uint32_t off[kLoads];  // byte offset of each load's row
 
   static __device__ __forceinline__ int lane_row() {
     return wave_id() * 8 + lane_id() / 8;
@@ -98,62 +129,67 @@ struct Along {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       off[i] = (uint32_t)min(i * 8 * WAVES + lane_row(), rows - 1 - row0) *
-               (uint32_t)pitch * 2;
+               (uint32_t)pitch * (uint32_t)sizeof(T);
   }
   // Load i of a step; base: the operand at row row0, element k0.
   __device__ __forceinline__ void load(int i, uint32_t lds, const char *base,
-                                       uint32_t pitch2, int left) const {
+                                       uint32_t, int left) const {
     dma(lds + (wave_id() + i * WAVES) * 1024, base,
-        off[i] + min(lane_piece() * 16, (left - 8) * 2));
+        off[i] + min(lane_piece() * 16, (left - E) * (int)sizeof(T)));
   }
   static __device__ __forceinline__ void clear(char *tile, int left) {
-    if (lane_piece() * 8 >= left) {
+    if (lane_piece() * E >= left) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
         store_vec(tile + (wave_id() + i * WAVES) * 1024 + lane_id() * 16,
                   vzero());
     }
   }
-  // Fragment of 32 rows from `row`, elements 16 * kk ...: lane l holds row
-  // l % 32, elements 8 * (l / 32) + [0, 8).
-  static __device__ __forceinline__ bf16x8 frag(const char *tile, int row,
-                                                int kk) {
+  // Fragment of 32 rows from `row`, sub-step kk of 4.
+  static __device__ __forceinline__ Frag<T> frag(const char *tile, int row,
+                                                 int kk) {
     const int l = lane_id();
     const int r = l % 32;
     const int piece = (kk * 2 + l / 32) ^ ((r >> 1) & 7);
-    return *reinterpret_cast<const bf16x8 *>(tile + row * 128 + r * 128 +
-                                             piece * 16);
+    return *reinterpret_cast<const Frag<T> *>(tile + row * 128 + r * 128 +
+                                              piece * 16);
   }
 };
 
-// An operand stored across the summed dimension: kStep rows of COLS columns,
-// COLS / 8 pieces of 16 bytes; row k keeps its piece c at c ^ ((k & 3) << 2),
-// so that the four rows that a transposing read takes lie in distinct banks.
-// Columns past the last repeat the last eight; rows past the end of the sum
+// An operand stored across the summed dimension: a step's rows of COLS
+// columns, in pieces of 16 bytes; row k keeps its piece c at c ^ turn(k), so
+// that what a read takes of several rows lies in distinct banks: of bf16 the
+// four rows of a transposing read, of f32 the rows of the two lane halves.
+// Columns past the last repeat the last piece; rows past the end of the sum
 // repeat the last, and are cleared.
-template <int COLS, int WAVES>
+template <typename T, int COLS, int WAVES>
 struct Across {
-  static constexpr int kBytes = COLS * kStep * 2;
-  static constexpr int kPieces = COLS / 8;
+  static constexpr int E = Elems<T>::value;
+  static constexpr int kPitch = COLS * sizeof(T);
+  static constexpr int kBytes = kPitch * kStep<T>;
+  static constexpr int kPieces = COLS / E;
   static constexpr int kRows = 64 / kPieces * WAVES;  // rows per load
-  static constexpr int kLoads = kStep / kRows;
-  static constexpr int kReads = 2;
+  static constexpr int kLoads = kStep<T> / kRows;
   uint32_t off;  // byte offset of the lane's columns
 
+  static __device__ __forceinline__ int turn(int k) {
+    return sizeof(T) == 2 ? (k & 3) << 2 : (k >> 2 & 1) << 3;
+  }
   static __device__ __forceinline__ int lane_row() {
     return (wave_id() * 64 + lane_id()) / kPieces;
   }
   static __device__ __forceinline__ int lane_piece() {
-    return (lane_id() % kPieces) ^ ((lane_row() & 3) << 2);
+    return (lane_id() % kPieces) ^ turn(lane_row());
   }
-  __device__ __forceinline__ void start(int col0, int cols, int pitch) {
-    off = (uint32_t)min(lane_piece() * 8, cols - 8 - col0) * 2;
+  __device__ __forceinline__ void start(int col0, int cols, int) {
+    off = (uint32_t)min(lane_piece() * E, cols - E - col0) *
+          (uint32_t)sizeof(T);
   }
-  // base: the operand at row k0, column col0; pitch2: bytes per row.
+  // base: the operand at row k0, column col0; pitch: its bytes per row.
   __device__ __forceinline__ void load(int i, uint32_t lds, const char *base,
-                                       uint32_t pitch2, int left) const {
+                                       uint32_t pitch, int left) const {
     dma(lds + (wave_id() + i * WAVES) * 1024, base,
-        off + (uint32_t)min(i * kRows + lane_row(), left - 1) * pitch2);
+        off + (uint32_t)min(i * kRows + lane_row(), left - 1) * pitch);
   }
   static __device__ __forceinline__ void clear(char *tile, int left) {
 #pragma unroll
@@ -162,19 +198,31 @@ struct Across {
         store_vec(tile + (wave_id() + i * WAVES) * 1024 + lane_id() * 16,
                   vzero());
   }
-  static __device__ __forceinline__ bf16x8 frag(const char *tile, int col,
-                                                int kk) {
+  // Fragment of 32 columns from `col`, sub-step kk of 4.
+  static __device__ __forceinline__ Frag<T> frag(const char *tile, int col,
+                                                 int kk) {
     const int l = lane_id();
-    const int k = kk * 16 + (l / 32) * 8 + (l % 16) / 4;
-    const int piece =
-        (col / 8 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1)) ^ ((k & 3) << 2);
-    const char *p = tile + k * COLS * 2 + piece * 16 + (l & 1) * 8;
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_s16x4 *)(p + 4 * COLS * 2));
-    const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    return __builtin_bit_cast(bf16x8, v);
+    Frag<T> f;
+    if constexpr (sizeof(T) == 2) {
+      const int k = kk * 16 + (l / 32) * 8 + (l % 16) / 4;
+      const int piece =
+          (col / 8 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1)) ^ turn(k);
+      const char *p = tile + k * kPitch + piece * 16 + (l & 1) * 8;
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4 *)(p + 4 * kPitch));
+      const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      f.v = __builtin_bit_cast(bf16x8, v);
+    } else {
+      const int k = kk * 8 + (l / 32) * 4, c = col + l % 32;
+      const char *p =
+          tile + k * kPitch + ((c / 4) ^ turn(k)) * 16 + c % 4 * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f.v[i] = *reinterpret_cast<const float *>(p + i * kPitch);
+    }
+    return f;
   }
 };
 
@@ -216,11 +264,42 @@ __device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
   return u;
 }
 
-__device__ __forceinline__ bf16 round_bf16(float f) {
+__device__ __forceinline__ void store_one(bf16 *p, float f) {
   const f32x2 v = {f, f};
   const uint32_t w =
       __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-  return bf16{(uint16_t)w};
+  *p = bf16{(uint16_t)w};
+}
+__device__ __forceinline__ void store_one(float *p, float f) { *p = f; }
+
+__device__ __forceinline__ float load_one(const bf16 *p) {
+  return __builtin_bit_cast(float, (uint32_t)p->bits << 16);
+}
+__device__ __forceinline__ float load_one(const float *p) { return *p; }
+
+// Four neighbouring elements.
+__device__ __forceinline__ void load4(const bf16 *p, float (&f)[4]) {
+  const uint2 d = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = e < 2 ? d.x : d.y;
+    f[e] = __builtin_bit_cast(float, (e & 1) ? (w & 0xffff0000u) : (w << 16));
+  }
+}
+__device__ __forceinline__ void load4(const float *p, float (&f)[4]) {
+  const Vec v = load_vec(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = elem<float>(v, e);
+}
+
+// Eight neighbouring elements, 16-byte aligned.
+__device__ __forceinline__ void store8(bf16 *p, const float (&f)[8]) {
+  store_vec(p, pack<bf16>(f));
+}
+__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
+  const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+  store_vec(p, pack<float>(a));
+  store_vec(p + 4, pack<float>(b));
 }
 
 // ------------------------------------------------------- storing a block
@@ -279,14 +358,15 @@ enum {
   kDw = 3       // dWg, dWu: rows hidden features, columns features, sum over M
 };
 
+template <typename T>
 struct Product {
-  const bf16 *x;          // [M, D]
-  const bf16 *w[2];       // Wg, Wu [F, D]
-  bf16 *h;                // [M, F]
+  const T *x;             // [M, D]
+  const T *w[2];          // Wg, Wu [F, D]
+  T *h;                   // [M, F]
   float *gu;              // saved G, U [2, M, F] (or NULL)
-  const bf16 *dh;         // [M, F]
-  bf16 *dgu;              // dG, dU [2, M, F]
-  bf16 *out[2];           // dx, or dWg and dWu
+  const T *dh;            // [M, F]
+  T *dgu;                 // dG, dU [2, M, F]
+  T *out[2];              // dx, or dWg and dWu
   float *part;            // partial tiles [slices, rem, tile, tile]
   int32_t M, D, F;
   int32_t tiles_r, tiles_c;  // of a plane
@@ -326,10 +406,10 @@ __device__ __forceinline__ void tile_of(int n, int tiles_r, int tiles_c,
 // so that a lane holds both of an element.
 enum { kSmall = 0, kBig = 1, kDeep = 2 };
 
-template <int FORM, int TILING, int ACT>
+template <typename T, int FORM, int TILING, int ACT>
 __global__ __launch_bounds__(TILING == kBig ? 512 : 256,
                              TILING == kDeep ? 1 : 2) void
-product_kernel(Product p) {
+product_kernel(Product<T> p) {
   constexpr bool BIG = TILING == kBig;
   constexpr int kWaves = BIG ? 8 : 4;
   constexpr int kTile = BIG ? 256 : 128;
@@ -340,11 +420,11 @@ product_kernel(Product p) {
   constexpr bool kPair = FORM == kHidden || FORM == kGrads;
   constexpr int kCols = kPair ? kTile / 2 : kTile;
   constexpr int NP = NI / 2;  // of a pair: blocks of G, then as many of U
-  using Row = std::conditional_t<FORM == kDw, Across<kTile, kWaves>,
-                                 Along<kTile, kWaves>>;
+  using Row = std::conditional_t<FORM == kDw, Across<T, kTile, kWaves>,
+                                 Along<T, kTile, kWaves>>;
   // (of a pair, the rows of one weight)
-  using Col = std::conditional_t<kPair, Along<kTile / 2, kWaves>,
-                                 Across<kTile, kWaves>>;
+  using Col = std::conditional_t<kPair, Along<T, kTile / 2, kWaves>,
+                                 Across<T, kTile, kWaves>>;
   constexpr uint32_t kColBytes = kPair ? 2 * Col::kBytes : Col::kBytes;
   constexpr uint32_t kBuf = Row::kBytes + kColBytes;
   __shared__ __align__(1024) char lds[kBufs][kBuf];
@@ -375,10 +455,11 @@ product_kernel(Product p) {
   // The operands of the step to be loaded next (of a pair: x, Wg, Wu), and
   // how far apart two steps are.
   const char *pr, *pc, *pu = nullptr;
-  const uint32_t pitch_r = 2 * (uint32_t)(kPair ? D : F);
-  const uint32_t pitch_c = 2 * (uint32_t)D;
-  const int64_t next_r = FORM == kDw ? kStep * (int64_t)pitch_r : 2 * kStep;
-  const int64_t next_c = kPair ? 2 * kStep : kStep * (int64_t)pitch_c;
+  constexpr int S = kStep<T>;
+  const uint32_t pitch_r = sizeof(T) * (uint32_t)(kPair ? D : F);
+  const uint32_t pitch_c = sizeof(T) * (uint32_t)D;
+  const int64_t next_r = FORM == kDw ? S * (int64_t)pitch_r : 128;
+  const int64_t next_c = kPair ? 128 : S * (int64_t)pitch_c;
   const int K = kPair ? D : FORM == kDx ? F : M;
   const int per = FORM == kDx ? p.steps / 2 : p.steps;  // steps per plane
   auto seek = [&](int s) {
@@ -398,7 +479,7 @@ product_kernel(Product p) {
   };
   // Elements of the sum that step s has left, of its plane.
   auto left = [&](int s) {
-    return K - (FORM == kDx && s >= per ? s - per : s) * kStep;
+    return K - (FORM == kDx && s >= per ? s - per : s) * S;
   };
   // On to step s, the one after the last loaded; past the end, the last step
   // is loaded again, into a buffer that nobody reads any more.
@@ -427,7 +508,7 @@ product_kernel(Product p) {
   };
   // Zeros past the end of the sum in the tile of step s, which has landed.
   auto clear = [&](int s, int buf) {
-    if (s < s1 && left(s) < kStep) {
+    if (s < s1 && left(s) < S) {
       Row::clear(lds[buf], left(s));
       Col::clear(lds[buf] + Row::kBytes, left(s));
       if constexpr (kPair)
@@ -452,8 +533,8 @@ product_kernel(Product p) {
   // multiplications: by then its own tile has been read (so the loads of the
   // step after next may overwrite it) and the next step's has landed, so the
   // first fragments of that are read under the last multiplications too.
-  constexpr int KK = kStep / 16;
-  bf16x8 a[2][MI], b[2][NI];
+  constexpr int KK = 4;
+  Frag<T> a[2][MI], b[2][NI];
   // Fragment n of the NI + MI of sub-step kk.
   auto read = [&](int n, int buf, int kk) {
     const char *rt = lds[buf];
@@ -471,8 +552,7 @@ product_kernel(Product p) {
   constexpr int kFirst = kLoads / 2;
   auto multiply = [&](int n, int kk) {
     const int i = n / NI, j = n % NI;
-    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        b[kk & 1][j], a[kk & 1][i], acc[i][j], 0, 0, 0);
+    multiply_add(acc[i][j], b[kk & 1][j], a[kk & 1][i]);
   };
   if (s0 < s1) {
     seek(s0);
@@ -567,19 +647,15 @@ product_kernel(Product p) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int mine = 8 * q + 4 * (lane / 32);
-            uint2 d = {0, 0};
+            float dh[4] = {};
             if (lane % 32 < n_r && mine < n_c)
-              d = *reinterpret_cast<const uint2 *>(
-                  p.dh + at + (int64_t)(lane % 32) * cols + mine);
+              load4(p.dh + at + (int64_t)(lane % 32) * cols + mine, dh);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t w = e < 2 ? d.x : d.y;
-              const float dh = __builtin_bit_cast(
-                  float, (e & 1) ? (w & 0xffff0000u) : (w << 16));
               float a, da;
               activate<ACT>(g[4 * q + e], a, da);
-              v0[4 * q + e] = dh * u[4 * q + e] * da;
-              v1[4 * q + e] = dh * a;
+              v0[4 * q + e] = dh[e] * u[4 * q + e] * da;
+              v1[4 * q + e] = dh[e] * a;
             }
           }
           store_block(stage, v0, p.dgu + at, cols, n_r, n_c);
@@ -598,14 +674,17 @@ product_kernel(Product p) {
 }
 
 // dG, dU from the saved G, U: one pass, 8 elements per thread.
-template <int ACT>
+template <typename T, int ACT>
 __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
-    const float *__restrict__ gu, const bf16 *__restrict__ dh,
-    bf16 *__restrict__ dgu, int64_t n) {
+    const float *__restrict__ gu, const T *__restrict__ dh,
+    T *__restrict__ dgu, int64_t n) {
   const int64_t stride = (int64_t)gridDim.x * kBlock * 8;
   for (int64_t at = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8; at < n;
        at += stride) {
-    const Vec d = load_stream(dh + at);
+    Vec d[8 / Elems<T>::value];
+#pragma unroll
+    for (int i = 0; i < 8 / Elems<T>::value; ++i)
+      d[i] = load_stream(dh + at + i * Elems<T>::value);
     const Vec g0 = load_stream(gu + at), g1 = load_stream(gu + at + 4);
     const Vec u0 = load_stream(gu + n + at), u1 = load_stream(gu + n + at + 4);
     float dg[8], du[8];
@@ -613,14 +692,14 @@ __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
     for (int e = 0; e < 8; ++e) {
       const float g = elem<float>(e < 4 ? g0 : g1, e % 4);
       const float u = elem<float>(e < 4 ? u0 : u1, e % 4);
-      const float t = elem<bf16>(d, e);
+      const float t = elem<T>(d[e / Elems<T>::value], e % Elems<T>::value);
       float a, da;
       activate<ACT>(g, a, da);
       dg[e] = t * u * da;
       du[e] = t * a;
     }
-    store_vec(dgu + at, pack<bf16>(dg));
-    store_vec(dgu + n + at, pack<bf16>(du));
+    store8(dgu + at, dg);
+    store8(dgu + n + at, du);
   }
 }
 
@@ -629,35 +708,53 @@ __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
 // kHidden and kGrads of up to 16 * TB tokens: bound by the weights' bytes, so
 // they go from memory to registers as matrix fragments, each read once, and
 // the tokens' fragments come from the caches.  A workgroup owns 16 hidden
-// features; its 8 wavefronts take the steps of 32 summed elements in turn (so
-// that together they read 512 contiguous bytes of every row), four steps'
+// features; its 8 wavefronts take the steps of 64 bytes of the sum in turn (so that
+// together they read 512 contiguous bytes of every row), four steps'
 // loads in flight each, and their sums meet in LDS, added in order.  (Plain
 // loads: with the streaming hint one token took 8.4 us, not 7.4, D = 1536, F =
 // 4096; 32 features per workgroup, 11.6.)
+template <typename T>
+__device__ __forceinline__ void multiply_few(f32x4 &acc, const Vec &a,
+                                             const Vec &b) {
+  if constexpr (sizeof(T) == 2) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0,
+        0, 0);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(elem<float>(a, c),
+                                                 elem<float>(b, c), acc, 0, 0,
+                                                 0);
+  }
+}
+
 constexpr int kFewWaves = 8;
 constexpr int kFewUnroll = 4;
 
-template <int FORM, int TB, int ACT>
-__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product p) {
+template <typename T, int FORM, int TB, int ACT>
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product<T> p) {
+  constexpr int E = Elems<T>::value;
+  constexpr int S = 4 * E;  // summed elements per step
   __shared__ f32x4 sums[kFewWaves][2][TB][64];
   const int lane = lane_id(), wave = wave_id();
   const int M = p.M, D = p.D, F = p.F;
   const int f0 = (blockIdx.x + p.block0) * 16;
   const int64_t f = min(f0 + lane % 16, F - 1);
-  const bf16 *wg = p.w[0] + f * D, *wu = p.w[1] + f * D;
-  const bf16 *x[TB];
+  const T *wg = p.w[0] + f * D, *wu = p.w[1] + f * D;
+  const T *x[TB];
 #pragma unroll
   for (int t = 0; t < TB; ++t)
     x[t] = p.x + (int64_t)min(t * 16 + lane % 16, M - 1) * D;
   f32x4 acc[2][TB] = {};
-  const int steps = (D + 31) / 32;
-  const int whole = D / 32;  // steps that need no bounds
+  const int steps = (D + S - 1) / S;
+  const int whole = D / S;  // steps that need no bounds
   for (int s = wave; s < steps; s += kFewWaves * kFewUnroll) {
     Vec g[kFewUnroll], u[kFewUnroll], v[kFewUnroll][TB];
 #pragma unroll
     for (int i = 0; i < kFewUnroll; ++i) {
-      const int k0 = (s + i * kFewWaves) * 32 + lane / 16 * 8;
-      const int k = min(k0, D - 8);
+      const int k0 = (s + i * kFewWaves) * S + lane / 16 * E;
+      const int k = min(k0, D - E);
       g[i] = load_vec(wg + k);
       u[i] = load_vec(wu + k);
 #pragma unroll
@@ -672,11 +769,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product p) {
     for (int i = 0; i < kFewUnroll; ++i)
 #pragma unroll
       for (int t = 0; t < TB; ++t) {
-        const bf16x8 b = __builtin_bit_cast(bf16x8, v[i][t]);
-        acc[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, g[i]), b, acc[0][t], 0, 0, 0);
-        acc[1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, u[i]), b, acc[1][t], 0, 0, 0);
+        multiply_few<T>(acc[0][t], g[i], v[i][t]);
+        multiply_few<T>(acc[1][t], u[i], v[i][t]);
       }
   }
 #pragma unroll
@@ -701,23 +795,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product p) {
     float a, da;
     activate<ACT>(gu[0], a, da);
     if constexpr (FORM == kHidden) {
-      p.h[at] = round_bf16(a * gu[1]);
+      store_one(p.h + at, a * gu[1]);
       if (p.gu != nullptr) {
         p.gu[at] = gu[0];
         p.gu[plane_size + at] = gu[1];
       }
     } else {
-      const float dh =
-          __builtin_bit_cast(float, (uint32_t)p.dh[at].bits << 16);
-      p.dgu[at] = round_bf16(dh * gu[1] * da);
-      p.dgu[plane_size + at] = round_bf16(dh * a);
+      const float dh = load_one(p.dh + at);
+      store_one(p.dgu + at, dh * gu[1] * da);
+      store_one(p.dgu + plane_size + at, dh * a);
     }
   }
 }
 
 // The last p.rem tiles of dx or dW: the sum of their slices, in slice order.
-template <int FORM>
-__global__ __launch_bounds__(kBlock) void slices_kernel(Product p,
+template <typename T, int FORM>
+__global__ __launch_bounds__(kBlock) void slices_kernel(Product<T> p,
                                                         int32_t tile) {
   const int rows = FORM == kDw ? p.F : p.M;
   const int per_row = tile / 8;
@@ -739,14 +832,14 @@ __global__ __launch_bounds__(kBlock) void slices_kernel(Product p,
       for (int e = 0; e < 8; ++e) v[e] += elem<float>(e < 4 ? a : b, e % 4);
       src += p.rem * size;
     }
-    store_vec(p.out[plane] + (int64_t)r * p.D + c, pack<bf16>(v));
+    store8(p.out[plane] + (int64_t)r * p.D + c, v);
   }
 }
 
-__global__ __launch_bounds__(kBlock) void zero_kernel(bf16 *a, bf16 *b,
+__global__ __launch_bounds__(kBlock) void zero_kernel(char *a, char *b,
                                                       int64_t n) {
-  for (int64_t at = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8; at < n;
-       at += (int64_t)gridDim.x * kBlock * 8) {
+  for (int64_t at = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 16; at < n;
+       at += (int64_t)gridDim.x * kBlock * 16) {
     store_vec(a + at, vzero());
     store_vec(b + at, vzero());
   }
@@ -767,7 +860,8 @@ struct GluPlan {
   }
 };
 
-// A plan's time, in microseconds, is modelled from what a tile takes: the big
+// A plan's time, in microseconds, is modelled from what a tile takes (bf16;
+// of f32 a step has half the elements at a sixteenth of the rate): the big
 // ones run one to a CU, 1.65 per step and 5 for filling the pipeline and
 // storing; the small ones two to a CU, 1.0 and 4; the deep ones one to a CU,
 // 0.5 and 4 (MI355X, D = 1536, F = 4096, forward: 256 tokens 15.7 us deep
@@ -777,20 +871,23 @@ struct GluPlan {
 // and 4 + 2 x 4 bytes per partial sum at 5 TB/s for adding them up.  Measured
 // on MI355X for the weights' gradients of 24960 x 1536 x 4096 (192 big tiles,
 // 4 slices) 654 -> 570 us, dx (588, the last 76 in 3 slices) 717 -> 589 us.
-GluPlan glu_plan(int form, int64_t M, int64_t D, int64_t F) {
+GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F) {
+  const bool f32 = dtype == ADALN_F32;
+  const int S = f32 ? kStep<float> : kStep<bf16>;
   const bool pair = form == kHidden || form == kGrads;
   const int64_t rows = form == kDw ? F : M, cols = pair ? F : D;
   const int64_t planes = form == kDw ? 2 : 1;
-  const int64_t steps = pair ? (D + kStep - 1) / kStep
-                        : form == kDx ? 2 * ((F + kStep - 1) / kStep)
-                                      : (M + kStep - 1) / kStep;
+  const int64_t steps = pair ? (D + S - 1) / S
+                        : form == kDx ? 2 * ((F + S - 1) / S)
+                                      : (M + S - 1) / S;
   GluPlan best;
   double best_us = 0;
   for (int tiling = 0; tiling < 3; ++tiling) {
     const int64_t t = tiling == kBig ? 256 : 128;
     const int64_t slots = tiling == kSmall ? 2 * kCUs : kCUs;
     const double step_us =
-        tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.5;
+        f32 ? (tiling == kBig ? 9 : tiling == kSmall ? 4.5 : 2.3)
+            : (tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.5);
     const double tile_us = tiling == kBig ? 5 : 4;
     const int64_t r = (rows + t - 1) / t;
     const int64_t c = (cols + (pair ? t / 2 : t) - 1) / (pair ? t / 2 : t);
@@ -824,11 +921,13 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace of the backward: dG and dU, then the partial products of dx or
 // of the weights (whichever needs more; they run one after the other).
-size_t glu_bwd_bytes(int64_t M, int64_t D, int64_t F, size_t *part_at) {
-  const size_t dgu = align256((size_t)2 * M * F * sizeof(bf16));
+size_t glu_bwd_bytes(int dtype, int64_t M, int64_t D, int64_t F,
+                     size_t *part_at) {
+  const size_t dgu =
+      align256((size_t)2 * M * F * (dtype == ADALN_F32 ? 4 : 2));
   if (part_at != nullptr) *part_at = dgu;
-  return dgu + std::max(glu_plan(kDx, M, D, F).part_bytes(),
-                        glu_plan(kDw, M, D, F).part_bytes());
+  return dgu + std::max(glu_plan(kDx, dtype, M, D, F).part_bytes(),
+                        glu_plan(kDw, dtype, M, D, F).part_bytes());
 }
 
 // Few tokens: few_kernel.  Past 4 tokens only where the tiles of 64 hidden
@@ -841,24 +940,26 @@ bool few_tokens(int64_t M, int64_t F) {
   return M <= 4 || (M <= 64 && (F + 63) / 64 < kCUs / 2);
 }
 
-template <int FORM, int ACT>
-hipError_t launch_few(Product p, hipStream_t s) {
+template <typename T>
+constexpr int kDtype = sizeof(T) == 2 ? ADALN_BF16 : ADALN_F32;
+
+template <typename T, int FORM, int ACT>
+hipError_t launch_few(Product<T> p, hipStream_t s) {
   const int64_t blocks = (p.F + 15) / 16;  // at most 16384
-  return p.M <= 16
-             ? launch_kernel_threads(few_kernel<FORM, 1, ACT>, blocks,
-                                     64 * kFewWaves, s, p)
-         : p.M <= 32
-             ? launch_kernel_threads(few_kernel<FORM, 2, ACT>, blocks,
-                                     64 * kFewWaves, s, p)
-             : launch_kernel_threads(few_kernel<FORM, 4, ACT>, blocks,
-                                     64 * kFewWaves, s, p);
+  const int threads = 64 * kFewWaves;
+  return p.M <= 16 ? launch_kernel_threads(few_kernel<T, FORM, 1, ACT>, blocks,
+                                           threads, s, p)
+         : p.M <= 32 ? launch_kernel_threads(few_kernel<T, FORM, 2, ACT>,
+                                             blocks, threads, s, p)
+                     : launch_kernel_threads(few_kernel<T, FORM, 4, ACT>,
+                                             blocks, threads, s, p);
 }
 
-template <int FORM, int ACT>
-hipError_t launch_product(Product p, hipStream_t s) {
+template <typename T, int FORM, int ACT>
+hipError_t launch_product(Product<T> p, hipStream_t s) {
   if constexpr (FORM == kHidden || FORM == kGrads)
-    if (few_tokens(p.M, p.F)) return launch_few<FORM, ACT>(p, s);
-  const GluPlan g = glu_plan(FORM, p.M, p.D, p.F);
+    if (few_tokens(p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
+  const GluPlan g = glu_plan(FORM, kDtype<T>, p.M, p.D, p.F);
   p.tiles_r = g.tiles_r;
   p.tiles_c = g.tiles_c;
   p.steps = g.steps;
@@ -871,17 +972,17 @@ hipError_t launch_product(Product p, hipStream_t s) {
     p.block0 = (int32_t)at;
     const int64_t n = std::min<int64_t>(kMaxGrid, g.blocks - at);
     e = g.tiling == kBig
-            ? launch_kernel_threads(product_kernel<FORM, kBig, ACT>, n, 512, s,
-                                    p)
-        : g.tiling == kSmall
-            ? launch_kernel_threads(product_kernel<FORM, kSmall, ACT>, n, 256,
+            ? launch_kernel_threads(product_kernel<T, FORM, kBig, ACT>, n, 512,
                                     s, p)
-            : launch_kernel_threads(product_kernel<FORM, kDeep, ACT>, n, 256,
-                                    s, p);
+        : g.tiling == kSmall
+            ? launch_kernel_threads(product_kernel<T, FORM, kSmall, ACT>, n,
+                                    256, s, p)
+            : launch_kernel_threads(product_kernel<T, FORM, kDeep, ACT>, n,
+                                    256, s, p);
   }
   if constexpr (FORM == kDx || FORM == kDw)
     if (e == hipSuccess && g.slices > 1)
-      e = launch_kernel(slices_kernel<FORM>,
+      e = launch_kernel(slices_kernel<T, FORM>,
                         (int64_t)g.rem * g.tile() * g.tile() / 8 / kBlock, s,
                         p, (int32_t)g.tile());
   return e;
@@ -892,9 +993,8 @@ int hip_fail(hipError_t e, const char *what) {
 }
 
 int check_glu(int64_t M, int64_t D, int64_t F, int act, int dtype) {
-  if (dtype != ADALN_BF16)
-    return fail(ADALN_ERR_DTYPE, "the gated feed-forward takes bf16 only, got "
-                "dtype code %d", dtype);
+  if (dtype != ADALN_F32 && dtype != ADALN_BF16)
+    return fail(ADALN_ERR_DTYPE, "unknown dtype code %d", dtype);
   if (act != ADALN_ACT_SILU && act != ADALN_ACT_GELU)
     return fail(ADALN_ERR_INVALID, "unknown activation %d", act);
   if (M < 0 || D <= 0 || F <= 0)
@@ -919,21 +1019,61 @@ int check_ptr(const void *p, bool needed, const char *name) {
   return ADALN_OK;
 }
 
-template <int ACT>
-hipError_t run_bwd(Product p, bf16 *dx, bf16 *dwg, bf16 *dwu, hipStream_t s) {
+template <typename T>
+Product<T> product_of(const void *x, const void *wg, const void *wu, int64_t M,
+                      int64_t D, int64_t F) {
+  Product<T> p = {};
+  p.x = (const T *)x;
+  p.w[0] = (const T *)wg;
+  p.w[1] = (const T *)wu;
+  p.M = (int32_t)M;
+  p.D = (int32_t)D;
+  p.F = (int32_t)F;
+  return p;
+}
+
+template <typename T>
+hipError_t run_fwd(const void *x, const void *wg, const void *wu, void *h,
+                   float *saved, int64_t M, int64_t D, int64_t F, int act,
+                   hipStream_t s) {
+  Product<T> p = product_of<T>(x, wg, wu, M, D, F);
+  p.h = (T *)h;
+  p.gu = saved;
+  return act == ADALN_ACT_SILU ? launch_product<T, kHidden, kSilu>(p, s)
+                               : launch_product<T, kHidden, kGeluTanh>(p, s);
+}
+
+template <typename T, int ACT>
+hipError_t run_bwd(Product<T> p, void *dx, void *dwg, void *dwu,
+                   hipStream_t s) {
   const int64_t n = (int64_t)p.M * p.F;
   hipError_t e =
       p.gu != nullptr
-          ? launch_kernel(gate_grads_kernel<ACT>, (n / 8 + kBlock - 1) / kBlock,
-                          s, (const float *)p.gu, p.dh, p.dgu, n)
-          : launch_product<kGrads, ACT>(p, s);
+          ? launch_kernel(gate_grads_kernel<T, ACT>,
+                          (n / 8 + kBlock - 1) / kBlock, s,
+                          (const float *)p.gu, p.dh, p.dgu, n)
+          : launch_product<T, kGrads, ACT>(p, s);
   if (e != hipSuccess) return e;
-  p.out[0] = dx;
-  e = launch_product<kDx, 0>(p, s);
+  p.out[0] = (T *)dx;
+  e = launch_product<T, kDx, 0>(p, s);
   if (e != hipSuccess) return e;
-  p.out[0] = dwg;
-  p.out[1] = dwu;
-  return launch_product<kDw, 0>(p, s);
+  p.out[0] = (T *)dwg;
+  p.out[1] = (T *)dwu;
+  return launch_product<T, kDw, 0>(p, s);
+}
+
+template <typename T>
+hipError_t run_bwd(const void *dh, const void *x, const void *wg,
+                   const void *wu, const float *saved, void *dx, void *dwg,
+                   void *dwu, void *workspace, size_t part_at, int64_t M,
+                   int64_t D, int64_t F, int act, hipStream_t s) {
+  Product<T> p = product_of<T>(x, wg, wu, M, D, F);
+  p.gu = const_cast<float *>(saved);
+  p.dh = (const T *)dh;
+  p.dgu = (T *)workspace;
+  p.part = (float *)((char *)workspace + part_at);
+  return act == ADALN_ACT_SILU ? run_bwd<T, kSilu>(p, dx, dwg, dwu, s)
+                               : run_bwd<T, kGeluTanh>(p, dx, dwg, dwu, s);
 }
 
 }  // namespace
@@ -952,18 +1092,11 @@ ADALN_API int adaln_glu_fwd(const void *x, const void *wg, const void *wu,
   ADALN_TRY(check_ptr(h, rows, "h"));
   ADALN_TRY(check_ptr(saved, rows && saved != nullptr, "saved"));
   if (!rows) return ok();
-  Product p = {};
-  p.x = (const bf16 *)x;
-  p.w[0] = (const bf16 *)wg;
-  p.w[1] = (const bf16 *)wu;
-  p.h = (bf16 *)h;
-  p.gu = saved;
-  p.M = (int32_t)M;
-  p.D = (int32_t)D;
-  p.F = (int32_t)F;
-  const hipError_t e = act == ADALN_ACT_SILU
-                           ? launch_product<kHidden, kSilu>(p, (hipStream_t)stream)
-                           : launch_product<kHidden, kGeluTanh>(p, (hipStream_t)stream);
+  hipStream_t s = (hipStream_t)stream;
+  const hipError_t e =
+      dtype == ADALN_BF16
+          ? run_fwd<bf16>(x, wg, wu, h, saved, M, D, F, act, s)
+          : run_fwd<float>(x, wg, wu, h, saved, M, D, F, act, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_glu_fwd launch");
   return ok();
 }
@@ -971,7 +1104,7 @@ ADALN_API int adaln_glu_fwd(const void *x, const void *wg, const void *wu,
 ADALN_API size_t adaln_glu_bwd_workspace_bytes(int64_t M, int64_t D, int64_t F,
                                                int dtype) {
   if (check_glu(M, D, F, ADALN_ACT_SILU, dtype) != ADALN_OK || M == 0) return 0;
-  return glu_bwd_bytes(M, D, F, nullptr);
+  return glu_bwd_bytes(dtype, M, D, F, nullptr);
 }
 
 ADALN_API int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
@@ -992,34 +1125,25 @@ ADALN_API int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
   hipStream_t s = (hipStream_t)stream;
   if (!rows) {
     // no tokens: the weights' gradients are empty sums
-    const int64_t nw = F * D;
+    const int64_t bytes = F * D * (dtype == ADALN_BF16 ? 2 : 4);
     const hipError_t e =
-        launch_kernel(zero_kernel, (nw / 8 + kBlock - 1) / kBlock, s,
-                      (bf16 *)dwg, (bf16 *)dwu, nw);
+        launch_kernel(zero_kernel, (bytes / 16 + kBlock - 1) / kBlock, s,
+                      (char *)dwg, (char *)dwu, bytes);
     if (e != hipSuccess) return hip_fail(e, "adaln_glu_bwd launch");
     return ok();
   }
   size_t part_at = 0;
-  const size_t need = glu_bwd_bytes(M, D, F, &part_at);
+  const size_t need = glu_bwd_bytes(dtype, M, D, F, &part_at);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(ADALN_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s",
                 need, workspace_bytes, workspace == nullptr ? " (NULL)" : "");
   ADALN_TRY(check_ptr(workspace, true, "workspace"));
-  Product p = {};
-  p.x = (const bf16 *)x;
-  p.w[0] = (const bf16 *)wg;
-  p.w[1] = (const bf16 *)wu;
-  p.gu = const_cast<float *>(saved);
-  p.dh = (const bf16 *)dh;
-  p.dgu = (bf16 *)workspace;
-  p.M = (int32_t)M;
-  p.D = (int32_t)D;
-  p.F = (int32_t)F;
-  p.part = (float *)((char *)workspace + part_at);
   const hipError_t e =
-      act == ADALN_ACT_SILU
-          ? run_bwd<kSilu>(p, (bf16 *)dx, (bf16 *)dwg, (bf16 *)dwu, s)
-          : run_bwd<kGeluTanh>(p, (bf16 *)dx, (bf16 *)dwg, (bf16 *)dwu, s);
+      dtype == ADALN_BF16
+          ? run_bwd<bf16>(dh, x, wg, wu, saved, dx, dwg, dwu, workspace,
+                          part_at, M, D, F, act, s)
+          : run_bwd<float>(dh, x, wg, wu, saved, dx, dwg, dwu, workspace,
+                           part_at, M, D, F, act, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_glu_bwd launch");
   return ok();
 }

@@ -1,5 +1,5 @@
-"""Binding of the gated feed-forward (adaln_glu_*) for torch tensors: bfloat16
-token rows [M, D] or [B, N, D], weights [F, D] as a linear layer keeps them.
+"""Binding of the gated feed-forward (adaln_glu_*) for torch tensors: token
+rows [M, D] or [B, N, D], weights [F, D] as a linear layer keeps them.
 Checks, streams and allocation are those of :mod:`adaln_fwd_amd.ops`."""
 
 from __future__ import annotations
@@ -9,7 +9,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .ops import _DTYPES, _check, _on, _ptr, _stream
+from .ops import _DTYPES, _check, _code, _on, _ptr, _stream
 
 _ACTS = {"silu": 0, "gelu": 1}
 
@@ -17,8 +17,7 @@ _ACTS = {"silu": 0, "gelu": 1}
 def _shapes(x, wg, wu, act):
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"unsupported dtype {x.dtype}; use bfloat16")
+    code = _code(x)
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be [M, D] or [B, N, D], got shape "
                          f"{tuple(x.shape)}")
@@ -32,7 +31,7 @@ def _shapes(x, wg, wu, act):
     M = 1
     for n in lead:
         M *= n
-    return lead, M, D, F
+    return lead, M, D, F, code
 
 
 def glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, *,
@@ -42,7 +41,7 @@ def glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, *,
     """h = act(x wg^T) * (x wu^T), act "silu" or "gelu" (tanh form); returns
     h, or with ``save=True`` (h, saved), `saved` being what the backward
     needs to skip the two products: both projections in float32 [2, M, F]."""
-    lead, M, D, F = _shapes(x, wg, wu, act)
+    lead, M, D, F, code = _shapes(x, wg, wu, act)
     dev = x.device
     lib = _lib.load()
     with _on(dev, stream):
@@ -56,14 +55,16 @@ def glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, *,
         if save:
             _check(saved, "saved", (2, M, F), torch.float32, dev)
         rc = lib.adaln_glu_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(h),
-                               _ptr(saved), M, D, F, _ACTS[act],
-                               _DTYPES[x.dtype], _stream(dev, stream))
+                               _ptr(saved), M, D, F, _ACTS[act], code,
+                               _stream(dev, stream))
     _lib.check(rc, "adaln_glu_fwd")
     return (h, saved) if save else h
 
 
-def glu_bwd_workspace_bytes(M: int, D: int, F: int) -> int:
-    return int(_lib.load().adaln_glu_bwd_workspace_bytes(M, D, F, _lib.BF16))
+def glu_bwd_workspace_bytes(M: int, D: int, F: int,
+                            dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(_lib.load().adaln_glu_bwd_workspace_bytes(
+        M, D, F, _DTYPES.get(dtype, -1)))
 
 
 def glu_bwd(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor,
@@ -72,16 +73,16 @@ def glu_bwd(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor,
             dwg: Optional[torch.Tensor] = None,
             dwu: Optional[torch.Tensor] = None,
             workspace: Optional[torch.Tensor] = None, stream=None):
-    """Backward of :func:`glu_fwd`; returns (dx, dwg, dwu) in bfloat16.
+    """Backward of :func:`glu_fwd`; returns (dx, dwg, dwu) in x's dtype.
     Without `saved` both projections are computed again.  The workspace
     (bytes from :func:`glu_bwd_workspace_bytes`) is allocated if not given."""
-    lead, M, D, F = _shapes(x, wg, wu, act)
+    lead, M, D, F, code = _shapes(x, wg, wu, act)
     dev, dt = x.device, x.dtype
     _check(dh, "dh", lead + (F,), dt, dev)
     if saved is not None:
         _check(saved, "saved", (2, M, F), torch.float32, dev)
     lib = _lib.load()
-    need = int(lib.adaln_glu_bwd_workspace_bytes(M, D, F, _DTYPES[dt]))
+    need = int(lib.adaln_glu_bwd_workspace_bytes(M, D, F, code))
     with _on(dev, stream):
         if dx is None:
             dx = torch.empty_like(x)
@@ -102,7 +103,7 @@ def glu_bwd(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor,
                                _ptr(saved), _ptr(dx), _ptr(dwg), _ptr(dwu),
                                _ptr(workspace),
                                workspace.numel() * workspace.element_size(),
-                               M, D, F, _ACTS[act], _DTYPES[dt],
+                               M, D, F, _ACTS[act], code,
                                _stream(dev, stream))
     _lib.check(rc, "adaln_glu_bwd")
     return dx, dwg, dwu

@@ -389,9 +389,8 @@ int adaln_qk_norm_rope_bwd(
  *   wg, wu [F, D] dtype in   the gate's and the other projection's weights
  *   h      [M, F] dtype out
  *   saved  [2, M, F] f32 out, or NULL: G, then U, for the backward
- * dtype is ADALN_BF16 (the matrix cores' operands; sums, G and U are
- * float32); D and F are multiples of 8, at most 65536 and 262144; M <= 2^24.
- * M == 0 is a successful no-op.
+ * Sums, G and U are float32.  D and F are multiples of 8, at most 65536 and
+ * 262144; M <= 2^24.  M == 0 is a successful no-op.
  */
 #define ADALN_ACT_SILU 0 /* g / (1 + exp(-g)) */
 #define ADALN_ACT_GELU 1 /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */

@@ -40,7 +40,7 @@ def lib():
 
 
 @pytest.mark.parametrize("M,D,F,act,dt,code", [
-    (4, 64, 64, 0, 0, _lib.ERR_DTYPE),          # f32
+    (4, 64, 64, 0, 2, _lib.ERR_DTYPE),
     (4, 64, 64, 0, 9, _lib.ERR_DTYPE),
     (4, 64, 64, 2, 1, _lib.ERR_INVALID),
     (-1, 64, 64, 0, 1, _lib.ERR_INVALID),
@@ -91,6 +91,7 @@ def test_workspace_holds_the_partial_sums(lib):
         n = lib.adaln_glu_bwd_workspace_bytes(M, D, F, 1)
         assert n >= 4 * M * F
         assert n <= 4 * M * F + 256 + 4 * 1024 * 128 * 128
+        assert lib.adaln_glu_bwd_workspace_bytes(M, D, F, 0) >= 8 * M * F
 
 
 def test_binding_refuses():
@@ -99,7 +100,7 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="GPU"):
         A.glu_fwd(x, w, w)
     with pytest.raises(TypeError):
-        A.glu_fwd(x.float(), w.float(), w.float())
+        A.glu_fwd(x.half(), w.half(), w.half())
     with pytest.raises(ValueError, match="act"):
         A.glu_fwd(x, w, w, act="relu")
     with pytest.raises(ValueError):

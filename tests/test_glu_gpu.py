@@ -52,19 +52,20 @@ SIZES = [
 ]
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("case", range(len(SIZES)))
-def test_whole_numbers_exact(case):
+def test_whole_numbers_exact(case, dt):
     M, D, F = SIZES[case]
     act = "gelu" if case % 2 else "silu"
-    _say(f"whole {SIZES[case]} {act}")
-    dh, x, wg, wu = _whole(M, D, F, case)
+    _say(f"whole {SIZES[case]} {act} {dt}")
+    dh, x, wg, wu = [t.to(dt) for t in _whole(M, D, F, case)]
     dev = [t.cuda() for t in (dh, x, wg, wu)]
     # float64 products of the same integers, on the GPU's general matrix path
     dhf, xf, wgf, wuf = [t.double() for t in dev]
     G, U = xf @ wgf.t(), xf @ wuf.t()
     assert G.min() >= 32 and G.max() < 256 and U.abs().max() < 256
     h = A.glu_fwd(*dev[1:], act=act)
-    assert torch.equal(h, (G * U).to(torch.bfloat16))
+    assert torch.equal(h, (G * U).to(dt))
     h2, saved = A.glu_fwd(*dev[1:], act=act, save=True)
     assert torch.equal(h2, h)
     assert torch.equal(saved[0].double(), G)
@@ -76,15 +77,15 @@ def test_whole_numbers_exact(case):
         for a, b, n in zip(got, want, ("dx", "dwg", "dwu")):
             # the sums are exact in float32 below 2^24
             assert b.abs().max() < 2 ** 24
-            assert torch.equal(a, b.float().to(torch.bfloat16)), (
-                n, s is None, int((a != b.float().to(torch.bfloat16)).sum()))
+            b = b.float().to(dt)
+            assert torch.equal(a, b), (n, s is None, int((a != b).sum()))
 
 
-def _real(M, D, F, seed):
+def _real(M, D, F, seed, dt=torch.bfloat16):
     g = torch.Generator().manual_seed(seed)
 
     def n(*s, std=1.0):
-        return (torch.randn(*s, generator=g) * std).to(torch.bfloat16)
+        return (torch.randn(*s, generator=g) * std).to(dt)
 
     return n(M, F, std=1e-2), n(M, D), n(F, D, std=2 * D ** -0.5), \
         n(F, D, std=D ** -0.5)
@@ -97,18 +98,19 @@ def _within(got, ref, tol, what):
                            float((err / tol.clamp_min(1e-300)).max()))
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("size", [(1, 256, 520), (7, 1536, 1024),
                                   (130, 200, 392), (513, 768, 1096)])
-def test_real_numbers(size, act):
+def test_real_numbers(size, act, dt):
     M, D, F = size
-    _say(f"real {size} {act}")
-    dh, x, wg, wu = _real(M, D, F, M)
+    _say(f"real {size} {act} {dt}")
+    dh, x, wg, wu = _real(M, D, F, M, dt)
     f = [t.double() for t in (dh, x, wg, wu)]
     ref_h, G, U = R.fwd(*f[1:], act)
     dx, dwg, dwu, dG, dU = R.bwd(*f, act)
     a, da = R.act(G, act)
-    e24, e8 = 2.0 ** -24, 2.0 ** -8
+    e24, e8 = 2.0 ** -24, torch.finfo(dt).eps / 2
     # float32 errors of G and U; of the exponential, 2^-23 (1 + |2 v|) with
     # |2 v| <= 2 |g|^3; of the rest of the activation, 16 roundings
     eG = (D + 2) * e24 * (f[1].abs() @ f[2].abs().t())
