@@ -366,14 +366,22 @@ struct Product {
   float *gu;              // saved G, U [2, M, F] (or NULL)
   const T *dh;            // [M, F]
   T *dgu;                 // dG, dU [2, M, F]
-  T *out[2];              // dx, or dWg and dWu
-  float *part;            // partial tiles [slices, rem, tile, tile]
+  T *dx;                  // [M, D]
+  T *dw[2];               // dWg, dWu [F, D]
   int32_t M, D, F;
-  int32_t tiles_r, tiles_c;  // of a plane
-  int32_t steps;
-  int32_t full, rem;         // tiles computed whole, and those that follow,
-  int32_t slices, per_slice; // in so many slices of so many steps
-  int32_t block0;         // first block of this launch
+};
+
+// How a product is cut: tiles of a plane (dW has two), `full` of them
+// computed whole, `rem` that follow in `slices` of `per_slice` steps each.
+struct Tiles {
+  float *part = nullptr;  // partial tiles [slices, rem, tile, tile]
+  int32_t tiling = 0;
+  int32_t tiles_r = 0, tiles_c = 0;
+  int32_t steps = 0;
+  int32_t full = 0, rem = 0;
+  int32_t slices = 1, per_slice = 0;
+  int32_t block0 = 0;     // first block of this launch
+  __host__ __device__ int tile() const;
 };
 
 // Workgroups go to the eight XCDs in turn: item `id` of `total` in an order
@@ -406,10 +414,21 @@ __device__ __forceinline__ void tile_of(int n, int tiles_r, int tiles_c,
 // so that a lane holds both of an element.
 enum { kSmall = 0, kBig = 1, kDeep = 2 };
 
+__host__ __device__ inline int Tiles::tile() const {
+  return tiling == kBig ? 256 : 128;
+}
+
+constexpr int tiling_threads(int tiling) { return tiling == kBig ? 512 : 256; }
+constexpr int tiling_waves(int tiling) { return tiling == kDeep ? 1 : 2; }
+// LDS: two steps' operand tiles, or four.
+constexpr int tiling_lds(int tiling) {
+  return (tiling == kDeep ? 4 : 2) * 2 * (tiling == kBig ? 256 : 128) * 128;
+}
+
+// Block `id` of a product.
 template <typename T, int FORM, int TILING, int ACT>
-__global__ __launch_bounds__(TILING == kBig ? 512 : 256,
-                             TILING == kDeep ? 1 : 2) void
-product_kernel(Product<T> p) {
+__device__ __forceinline__ void product(const Product<T> &p, const Tiles &q,
+                                        int id, char *lds) {
   constexpr bool BIG = TILING == kBig;
   constexpr int kWaves = BIG ? 8 : 4;
   constexpr int kTile = BIG ? 256 : 128;
@@ -427,26 +446,25 @@ product_kernel(Product<T> p) {
                                  Across<T, kTile, kWaves>>;
   constexpr uint32_t kColBytes = kPair ? 2 * Col::kBytes : Col::kBytes;
   constexpr uint32_t kBuf = Row::kBytes + kColBytes;
-  __shared__ __align__(1024) char lds[kBufs][kBuf];
+  static_assert(kBufs * kBuf == tiling_lds(TILING), "");
 
   // The first `full` blocks compute a tile each; the rest, slices of the
   // sums of the last `rem` tiles.
-  const int id = blockIdx.x + p.block0;
   int n, split = 0;
-  if (id < p.full) {
-    n = xcd_run(id, p.full);
+  if (id < q.full) {
+    n = xcd_run(id, q.full);
   } else {
-    split = (id - p.full) / p.rem;
-    n = p.full + xcd_run(id - p.full - split * p.rem, p.rem);
+    split = (id - q.full) / q.rem;
+    n = q.full + xcd_run(id - q.full - split * q.rem, q.rem);
   }
-  const bool partial = id >= p.full && p.slices > 1;
+  const bool partial = id >= q.full && q.slices > 1;
   int plane, tr, tc;
-  tile_of(n, p.tiles_r, p.tiles_c, plane, tr, tc);
+  tile_of(n, q.tiles_r, q.tiles_c, plane, tr, tc);
   const int row0 = tr * kTile, col0 = tc * kCols;
   const int M = p.M, D = p.D, F = p.F;
-  const int s0 = partial ? split * p.per_slice : 0;
-  const int s1 = partial ? min(s0 + p.per_slice, p.steps) : p.steps;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)&lds[0][0];
+  const int s0 = partial ? split * q.per_slice : 0;
+  const int s1 = partial ? min(s0 + q.per_slice, q.steps) : q.steps;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)lds;
 
   Row row;
   Col col;
@@ -461,7 +479,7 @@ product_kernel(Product<T> p) {
   const int64_t next_r = FORM == kDw ? S * (int64_t)pitch_r : 128;
   const int64_t next_c = kPair ? 128 : S * (int64_t)pitch_c;
   const int K = kPair ? D : FORM == kDx ? F : M;
-  const int per = FORM == kDx ? p.steps / 2 : p.steps;  // steps per plane
+  const int per = FORM == kDx ? q.steps / 2 : q.steps;  // steps per plane
   auto seek = [&](int s) {
     const int pl = FORM == kDx ? s >= per : 0;
     const int64_t k = s - pl * per;
@@ -509,10 +527,11 @@ product_kernel(Product<T> p) {
   // Zeros past the end of the sum in the tile of step s, which has landed.
   auto clear = [&](int s, int buf) {
     if (s < s1 && left(s) < S) {
-      Row::clear(lds[buf], left(s));
-      Col::clear(lds[buf] + Row::kBytes, left(s));
+      char *tile = lds + buf * kBuf;
+      Row::clear(tile, left(s));
+      Col::clear(tile + Row::kBytes, left(s));
       if constexpr (kPair)
-        Col::clear(lds[buf] + Row::kBytes + Col::kBytes, left(s));
+        Col::clear(tile + Row::kBytes + Col::kBytes, left(s));
       __syncthreads();
     }
   };
@@ -537,8 +556,8 @@ product_kernel(Product<T> p) {
   Frag<T> a[2][MI], b[2][NI];
   // Fragment n of the NI + MI of sub-step kk.
   auto read = [&](int n, int buf, int kk) {
-    const char *rt = lds[buf];
-    const char *ct = lds[buf] + Row::kBytes;
+    const char *rt = lds + buf * kBuf;
+    const char *ct = rt + Row::kBytes;
     if (n < NI)
       b[kk & 1][n] = Col::frag(
           ct,
@@ -612,8 +631,8 @@ product_kernel(Product<T> p) {
 
   // acc[i][j][4 q + e] of lane l is row l % 32 of block i, column
   // 8 q + 4 (l / 32) + e of block j.
-  char *stage = &lds[0][0] + wave * kStageBytes;
-  static_assert(kWaves * kStageBytes <= sizeof lds, "");
+  char *stage = lds + wave * kStageBytes;
+  static_assert(kWaves * kStageBytes <= kBufs * kBuf, "");
   const int lane = lane_id();
   const int rows = FORM == kDw ? F : M, cols = kPair ? F : D;
 #pragma unroll
@@ -663,14 +682,38 @@ product_kernel(Product<T> p) {
         }
       } else if (partial) {
         store_block(stage, acc[i][j],
-                    p.part + (((int64_t)split * p.rem + n - p.full) * kTile +
+                    q.part + (((int64_t)split * q.rem + n - q.full) * kTile +
                               (r - row0)) * kTile + (c - col0),
                     kTile, n_r, n_c);
       } else {
-        store_block(stage, acc[i][j], p.out[plane] + at, cols, n_r, n_c);
+        store_block(stage, acc[i][j],
+                    (FORM == kDx ? p.dx : p.dw[plane]) + at, cols, n_r, n_c);
       }
     }
   }
+}
+
+template <typename T, int FORM, int TILING, int ACT>
+__global__ __launch_bounds__(tiling_threads(TILING),
+                             tiling_waves(TILING)) void
+product_kernel(Product<T> p, Tiles q) {
+  __shared__ __align__(1024) char lds[tiling_lds(TILING)];
+  product<T, FORM, TILING, ACT>(p, q, blockIdx.x + q.block0, lds);
+}
+
+// dx and dW in one launch, for calls whose tiles of either alone leave CUs
+// idle; the product with the longer blocks comes first.
+template <typename T, int TILING>
+__global__ __launch_bounds__(tiling_threads(TILING),
+                             tiling_waves(TILING)) void
+grads_kernel(Product<T> p, Tiles x, Tiles w, int32_t first, int32_t w_first) {
+  __shared__ __align__(1024) char lds[tiling_lds(TILING)];
+  const bool second = (int)blockIdx.x >= first;
+  const int id = blockIdx.x - (second ? first : 0);
+  if (second == (w_first != 0))
+    product<T, kDx, TILING, 0>(p, x, id, lds);
+  else
+    product<T, kDw, TILING, 0>(p, w, id, lds);
 }
 
 // dG, dU from the saved G, U: one pass, 8 elements per thread.
@@ -739,7 +782,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product<T> p) {
   __shared__ f32x4 sums[kFewWaves][2][TB][64];
   const int lane = lane_id(), wave = wave_id();
   const int M = p.M, D = p.D, F = p.F;
-  const int f0 = (blockIdx.x + p.block0) * 16;
+  const int f0 = blockIdx.x * 16;
   const int64_t f = min(f0 + lane % 16, F - 1);
   const T *wg = p.w[0] + f * D, *wu = p.w[1] + f * D;
   const T *x[TB];
@@ -808,31 +851,37 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product<T> p) {
   }
 }
 
-// The last p.rem tiles of dx or dW: the sum of their slices, in slice order.
-template <typename T, int FORM>
-__global__ __launch_bounds__(kBlock) void slices_kernel(Product<T> p,
-                                                        int32_t tile) {
-  const int rows = FORM == kDw ? p.F : p.M;
-  const int per_row = tile / 8;
-  const int64_t size = (int64_t)tile * tile;
-  const int64_t total = p.rem * size / 8;
+// The tiles of dx and of dW that were computed in slices: the sum of these,
+// in slice order.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void slices_kernel(Product<T> p, Tiles x,
+                                                        Tiles w) {
+  const int64_t size_x = (int64_t)x.tile() * x.tile();
+  const int64_t size_w = (int64_t)w.tile() * w.tile();
+  const int64_t all_x = x.rem * size_x / 8;
+  const int64_t total = all_x + w.rem * size_w / 8;
   for (int64_t at = (int64_t)blockIdx.x * kBlock + threadIdx.x; at < total;
        at += (int64_t)gridDim.x * kBlock) {
-    const int t = (int)(at / (size / 8));
-    const int in = (int)(at - t * (size / 8));
+    const bool is_w = at >= all_x;
+    const Tiles &q = is_w ? w : x;
+    const int64_t size = is_w ? size_w : size_x;
+    const int64_t i = is_w ? at - all_x : at;
+    const int t = (int)(i / (size / 8));
+    const int in = (int)(i - t * (size / 8));
     int plane, tr, tc;
-    tile_of(p.full + t, p.tiles_r, p.tiles_c, plane, tr, tc);
+    tile_of(q.full + t, q.tiles_r, q.tiles_c, plane, tr, tc);
+    const int tile = q.tile(), per_row = tile / 8;
     const int r = tr * tile + in / per_row, c = tc * tile + in % per_row * 8;
-    if (r >= rows || c >= p.D) continue;
-    const float *src = p.part + t * size + (int64_t)in * 8;
+    if (r >= (is_w ? p.F : p.M) || c >= p.D) continue;
+    const float *src = q.part + t * size + (int64_t)in * 8;
     float v[8] = {};
-    for (int s = 0; s < p.slices; ++s) {
+    for (int s = 0; s < q.slices; ++s) {
       const Vec a = load_stream(src), b = load_stream(src + 4);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += elem<float>(e < 4 ? a : b, e % 4);
-      src += p.rem * size;
+      src += q.rem * size;
     }
-    store8(p.out[plane] + (int64_t)r * p.D + c, v);
+    store8((is_w ? p.dw[plane] : p.dx) + (int64_t)r * p.D + c, v);
   }
 }
 
@@ -847,16 +896,28 @@ __global__ __launch_bounds__(kBlock) void zero_kernel(char *a, char *b,
 
 // ----------------------------------------------------------------- planning
 
-struct GluPlan {
-  int tiling = kSmall;
-  int32_t tiles_r = 0, tiles_c = 0;
-  int32_t steps = 0;
-  int32_t full = 0, rem = 0, slices = 1, per_slice = 0;
+struct GluPlan : Tiles {
   int64_t blocks = 0;
-  int tile() const { return tiling == kBig ? 256 : 128; }
+  double us = 0;  // what the model below says
   size_t part_bytes() const {
     return slices > 1 ? (size_t)slices * rem * tile() * tile() * sizeof(float)
                       : 0;
+  }
+};
+
+// The sizes of one product.
+struct Shape {
+  int64_t rows, cols, planes, steps;
+  int col_share;  // columns of a tile, of its side: 1, or 2 for half of it
+  Shape(int form, int dtype, int64_t M, int64_t D, int64_t F) {
+    const int S = dtype == ADALN_F32 ? kStep<float> : kStep<bf16>;
+    const bool pair = form == kHidden || form == kGrads;
+    rows = form == kDw ? F : M;
+    cols = pair ? F : D;
+    planes = form == kDw ? 2 : 1;
+    steps = pair ? (D + S - 1) / S
+            : form == kDx ? 2 * ((F + S - 1) / S) : (M + S - 1) / S;
+    col_share = pair ? 2 : 1;
   }
 };
 
@@ -865,53 +926,69 @@ struct GluPlan {
 // ones run one to a CU, 1.65 per step and 5 for filling the pipeline and
 // storing; the small ones two to a CU, 1.0 and 4; the deep ones one to a CU,
 // 0.5 and 4 (MI355X, D = 1536, F = 4096, forward: 256 tokens 15.7 us deep
-// against 20.5 small, 1024 tokens 31.6 against 27.7).  Whole rounds of tiles (as many as run at a time) are computed
-// unsplit; the tiles left over, less than a round, are split into slices of
-// the sum where that pays: s slices take ceil(rem * s / slots) / s of a round,
-// and 4 + 2 x 4 bytes per partial sum at 5 TB/s for adding them up.  Measured
-// on MI355X for the weights' gradients of 24960 x 1536 x 4096 (192 big tiles,
-// 4 slices) 654 -> 570 us, dx (588, the last 76 in 3 slices) 717 -> 589 us.
+// against 20.5 small, 1024 tokens 31.6 against 27.7).  Adding slices up takes
+// 4 and, per partial sum, 2 x 4 bytes at 5 TB/s.
+struct Costs {
+  int64_t tile, slots;
+  double step, fill;
+  Costs(int tiling, int dtype) {
+    tile = tiling == kBig ? 256 : 128;
+    slots = tiling == kSmall ? 2 * kCUs : kCUs;
+    fill = tiling == kBig ? 5 : 4;
+    step = dtype == ADALN_F32
+               ? (tiling == kBig ? 9 : tiling == kSmall ? 4.5 : 2.3)
+               : (tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.5);
+  }
+  double adding(int64_t blocks) const {
+    return 4 + 8e-6 / 5 * blocks * tile * tile;
+  }
+};
+
+// Tiles of a shape, the last `rem` of them in s slices of `per` steps.
+GluPlan cut(const Shape &h, int tiling, int64_t tile, int64_t rem, int64_t s,
+            int64_t per) {
+  GluPlan g;
+  const int64_t r = (h.rows + tile - 1) / tile;
+  const int64_t side = tile / h.col_share;
+  const int64_t c = (h.cols + side - 1) / side;
+  const int64_t n = r * c * h.planes;
+  g.tiling = tiling;
+  g.tiles_r = (int32_t)r;
+  g.tiles_c = (int32_t)c;
+  g.steps = (int32_t)h.steps;
+  g.rem = (int32_t)(s > 1 ? rem : 0);
+  g.full = (int32_t)(n - g.rem);
+  g.slices = (int32_t)s;
+  g.per_slice = (int32_t)per;
+  g.blocks = g.full + g.rem * s;
+  return g;
+}
+
+// One product in a launch of its own.  Whole rounds of tiles (as many as run
+// at a time) are computed unsplit; the tiles left over, less than a round,
+// are split into slices of the sum where that pays: s slices take
+// ceil(rem * s / slots) / s of a round.  Measured on MI355X for the weights'
+// gradients of 24960 x 1536 x 4096 (192 big tiles, 4 slices) 654 -> 570 us,
+// dx (588, the last 76 in 3 slices) 717 -> 589 us.
 GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F) {
-  const bool f32 = dtype == ADALN_F32;
-  const int S = f32 ? kStep<float> : kStep<bf16>;
+  const Shape h(form, dtype, M, D, F);
   const bool pair = form == kHidden || form == kGrads;
-  const int64_t rows = form == kDw ? F : M, cols = pair ? F : D;
-  const int64_t planes = form == kDw ? 2 : 1;
-  const int64_t steps = pair ? (D + S - 1) / S
-                        : form == kDx ? 2 * ((F + S - 1) / S)
-                                      : (M + S - 1) / S;
   GluPlan best;
-  double best_us = 0;
   for (int tiling = 0; tiling < 3; ++tiling) {
-    const int64_t t = tiling == kBig ? 256 : 128;
-    const int64_t slots = tiling == kSmall ? 2 * kCUs : kCUs;
-    const double step_us =
-        f32 ? (tiling == kBig ? 9 : tiling == kSmall ? 4.5 : 2.3)
-            : (tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.5);
-    const double tile_us = tiling == kBig ? 5 : 4;
-    const int64_t r = (rows + t - 1) / t;
-    const int64_t c = (cols + (pair ? t / 2 : t) - 1) / (pair ? t / 2 : t);
-    const int64_t n = r * c * planes;
-    const int64_t full = n / slots * slots, rem = n - full;
+    const Costs k(tiling, dtype);
+    const int64_t n = cut(h, tiling, k.tile, 0, 1, h.steps).blocks;
+    const int64_t full = n / k.slots * k.slots, rem = n - full;
     for (int64_t s = 1; s <= 16; ++s) {
-      if (s > 1 && (pair || rem == 0 || steps < 4 * s)) break;
-      const int64_t per = (steps + s - 1) / s;
-      if ((steps + per - 1) / per != s) continue;  // an empty slice
-      double us = full / slots * (steps * step_us + tile_us);
+      if (s > 1 && (pair || rem == 0 || h.steps < 4 * s)) break;
+      const int64_t per = (h.steps + s - 1) / s;
+      if ((h.steps + per - 1) / per != s) continue;  // an empty slice
+      double us = full / k.slots * (h.steps * k.step + k.fill);
       if (rem > 0)
-        us += (rem * s + slots - 1) / slots * (per * step_us + tile_us);
-      if (s > 1) us += 4 + 8e-6 / 5 * rem * s * t * t;
-      if (best.blocks > 0 && us >= best_us) continue;
-      best_us = us;
-      best.tiling = tiling;
-      best.tiles_r = (int32_t)r;
-      best.tiles_c = (int32_t)c;
-      best.steps = (int32_t)steps;
-      best.full = (int32_t)(s > 1 ? full : n);
-      best.rem = (int32_t)(s > 1 ? rem : 0);
-      best.slices = (int32_t)s;
-      best.per_slice = (int32_t)per;
-      best.blocks = s > 1 ? full + rem * s : n;
+        us += (rem * s + k.slots - 1) / k.slots * (per * k.step + k.fill);
+      if (s > 1) us += k.adding(rem * s);
+      if (best.blocks > 0 && us >= best.us) continue;
+      best = cut(h, tiling, k.tile, rem, s, per);
+      best.us = us;
     }
   }
   return best;
@@ -919,15 +996,64 @@ GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Workspace of the backward: dG and dU, then the partial products of dx or
-// of the weights (whichever needs more; they run one after the other).
-size_t glu_bwd_bytes(int dtype, int64_t M, int64_t D, int64_t F,
-                     size_t *part_at) {
-  const size_t dgu =
+// The backward's two products and its workspace: dG and dU, then the partial
+// sums.
+struct GluBackward {
+  GluPlan x, w;
+  bool joint = false;
+  size_t bytes = 0;
+  size_t x_part = 0, w_part = 0;  // offsets
+};
+
+// In one launch where the model finds that shorter: all tiles of both
+// products, in slices or not, taken by free CUs in turn (the average load and
+// half the longest block, or the longest block where all run at once).  Two
+// launches cost 3 more.  Measured on MI355X, whole backward, two launches
+// against one: 777 x 1000 x 1480 40.5 -> 33.6 us, 4096 x 256 x 1024 47.5 ->
+// 37.4, 64 x 512 x 1024 24.4 -> 21.5.
+GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
+  GluBackward b;
+  b.x = glu_plan(kDx, dtype, M, D, F);
+  b.w = glu_plan(kDw, dtype, M, D, F);
+  if (b.x.tiling != kBig || b.w.tiling != kBig) {
+    const Shape hx(kDx, dtype, M, D, F), hw(kDw, dtype, M, D, F);
+    double best = b.x.us + b.w.us + 3;
+    constexpr int64_t kTry[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    for (int tiling : {(int)kSmall, (int)kDeep}) {
+      const Costs k(tiling, dtype);
+      const int64_t nx = cut(hx, tiling, k.tile, 0, 1, hx.steps).blocks;
+      const int64_t nw = cut(hw, tiling, k.tile, 0, 1, hw.steps).blocks;
+      for (int64_t sx : kTry) {
+        const int64_t px = (hx.steps + sx - 1) / sx;
+        if (sx > 1 && (hx.steps < 4 * sx || (hx.steps + px - 1) / px != sx))
+          continue;
+        for (int64_t sw : kTry) {
+          const int64_t pw = (hw.steps + sw - 1) / sw;
+          if (sw > 1 && (hw.steps < 4 * sw || (hw.steps + pw - 1) / pw != sw))
+            continue;
+          const double tx = px * k.step + k.fill, tw = pw * k.step + k.fill;
+          const int64_t blocks = nx * sx + nw * sw;
+          const double longest = std::max(tx, tw);
+          double us = blocks <= k.slots
+                          ? longest
+                          : (nx * sx * tx + nw * sw * tw) / k.slots +
+                                longest / 2;
+          if (sx > 1 || sw > 1)
+            us += k.adding((sx > 1 ? nx * sx : 0) + (sw > 1 ? nw * sw : 0));
+          if (us >= best || blocks > kMaxGrid) continue;
+          best = us;
+          b.joint = true;
+          b.x = cut(hx, tiling, k.tile, nx, sx, px);
+          b.w = cut(hw, tiling, k.tile, nw, sw, pw);
+        }
+      }
+    }
+  }
+  b.x_part = b.w_part =
       align256((size_t)2 * M * F * (dtype == ADALN_F32 ? 4 : 2));
-  if (part_at != nullptr) *part_at = dgu;
-  return dgu + std::max(glu_plan(kDx, dtype, M, D, F).part_bytes(),
-                        glu_plan(kDw, dtype, M, D, F).part_bytes());
+  if (b.joint) b.w_part += align256(b.x.part_bytes());
+  b.bytes = std::max(b.x_part + b.x.part_bytes(), b.w_part + b.w.part_bytes());
+  return b;
 }
 
 // Few tokens: few_kernel.  Past 4 tokens only where the tiles of 64 hidden
@@ -956,35 +1082,68 @@ hipError_t launch_few(Product<T> p, hipStream_t s) {
 }
 
 template <typename T, int FORM, int ACT>
-hipError_t launch_product(Product<T> p, hipStream_t s) {
-  if constexpr (FORM == kHidden || FORM == kGrads)
-    if (few_tokens(p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
-  const GluPlan g = glu_plan(FORM, kDtype<T>, p.M, p.D, p.F);
-  p.tiles_r = g.tiles_r;
-  p.tiles_c = g.tiles_c;
-  p.steps = g.steps;
-  p.full = g.full;
-  p.rem = g.rem;
-  p.slices = g.slices;
-  p.per_slice = g.per_slice;
+hipError_t launch_tiles(const Product<T> &p, const GluPlan &g,
+                        hipStream_t s) {
+  Tiles q = g;
   hipError_t e = hipSuccess;
   for (int64_t at = 0; at < g.blocks && e == hipSuccess; at += kMaxGrid) {
-    p.block0 = (int32_t)at;
+    q.block0 = (int32_t)at;
     const int64_t n = std::min<int64_t>(kMaxGrid, g.blocks - at);
+    const int threads = tiling_threads(g.tiling);
     e = g.tiling == kBig
-            ? launch_kernel_threads(product_kernel<T, FORM, kBig, ACT>, n, 512,
-                                    s, p)
+            ? launch_kernel_threads(product_kernel<T, FORM, kBig, ACT>, n,
+                                    threads, s, p, q)
         : g.tiling == kSmall
             ? launch_kernel_threads(product_kernel<T, FORM, kSmall, ACT>, n,
-                                    256, s, p)
+                                    threads, s, p, q)
             : launch_kernel_threads(product_kernel<T, FORM, kDeep, ACT>, n,
-                                    256, s, p);
+                                    threads, s, p, q);
   }
-  if constexpr (FORM == kDx || FORM == kDw)
-    if (e == hipSuccess && g.slices > 1)
-      e = launch_kernel(slices_kernel<T, FORM>,
-                        (int64_t)g.rem * g.tile() * g.tile() / 8 / kBlock, s,
-                        p, (int32_t)g.tile());
+  return e;
+}
+
+// kHidden or kGrads.
+template <typename T, int FORM, int ACT>
+hipError_t launch_pair(const Product<T> &p, hipStream_t s) {
+  if (few_tokens(p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
+  return launch_tiles<T, FORM, ACT>(
+      p, glu_plan(FORM, kDtype<T>, p.M, p.D, p.F), s);
+}
+
+template <typename T>
+hipError_t launch_slices(const Product<T> &p, const Tiles &x, const Tiles &w,
+                         hipStream_t s) {
+  const int64_t n = (int64_t)x.rem * x.tile() * x.tile() +
+                    (int64_t)w.rem * w.tile() * w.tile();
+  return launch_kernel(slices_kernel<T>, n / 8 / kBlock, s, p, x, w);
+}
+
+template <typename T>
+hipError_t launch_grads(const Product<T> &p, const GluBackward &b, char *ws,
+                        hipStream_t s) {
+  GluPlan x = b.x, w = b.w;
+  x.part = (float *)(ws + b.x_part);
+  w.part = (float *)(ws + b.w_part);
+  hipError_t e;
+  if (b.joint) {
+    const bool w_first = w.per_slice > x.per_slice;
+    const int32_t first = (int32_t)(w_first ? w.blocks : x.blocks);
+    const int64_t n = x.blocks + w.blocks;
+    e = x.tiling == kSmall
+            ? launch_kernel_threads(grads_kernel<T, kSmall>, n, 256, s, p,
+                                    (Tiles)x, (Tiles)w, first,
+                                    (int32_t)w_first)
+            : launch_kernel_threads(grads_kernel<T, kDeep>, n, 256, s, p,
+                                    (Tiles)x, (Tiles)w, first,
+                                    (int32_t)w_first);
+    if (e != hipSuccess) return e;
+    return launch_slices<T>(p, x, w, s);
+  }
+  Tiles none;
+  e = launch_tiles<T, kDx, 0>(p, x, s);
+  if (e == hipSuccess) e = launch_slices<T>(p, x, none, s);
+  if (e == hipSuccess) e = launch_tiles<T, kDw, 0>(p, w, s);
+  if (e == hipSuccess) e = launch_slices<T>(p, none, w, s);
   return e;
 }
 
@@ -1039,41 +1198,36 @@ hipError_t run_fwd(const void *x, const void *wg, const void *wu, void *h,
   Product<T> p = product_of<T>(x, wg, wu, M, D, F);
   p.h = (T *)h;
   p.gu = saved;
-  return act == ADALN_ACT_SILU ? launch_product<T, kHidden, kSilu>(p, s)
-                               : launch_product<T, kHidden, kGeluTanh>(p, s);
+  return act == ADALN_ACT_SILU ? launch_pair<T, kHidden, kSilu>(p, s)
+                               : launch_pair<T, kHidden, kGeluTanh>(p, s);
 }
 
 template <typename T, int ACT>
-hipError_t run_bwd(Product<T> p, void *dx, void *dwg, void *dwu,
-                   hipStream_t s) {
+hipError_t launch_gate_grads(const Product<T> &p, hipStream_t s) {
+  if (p.gu == nullptr) return launch_pair<T, kGrads, ACT>(p, s);
   const int64_t n = (int64_t)p.M * p.F;
-  hipError_t e =
-      p.gu != nullptr
-          ? launch_kernel(gate_grads_kernel<T, ACT>,
-                          (n / 8 + kBlock - 1) / kBlock, s,
-                          (const float *)p.gu, p.dh, p.dgu, n)
-          : launch_product<T, kGrads, ACT>(p, s);
-  if (e != hipSuccess) return e;
-  p.out[0] = (T *)dx;
-  e = launch_product<T, kDx, 0>(p, s);
-  if (e != hipSuccess) return e;
-  p.out[0] = (T *)dwg;
-  p.out[1] = (T *)dwu;
-  return launch_product<T, kDw, 0>(p, s);
+  return launch_kernel(gate_grads_kernel<T, ACT>,
+                       (n / 8 + kBlock - 1) / kBlock, s, (const float *)p.gu,
+                       p.dh, p.dgu, n);
 }
 
 template <typename T>
 hipError_t run_bwd(const void *dh, const void *x, const void *wg,
                    const void *wu, const float *saved, void *dx, void *dwg,
-                   void *dwu, void *workspace, size_t part_at, int64_t M,
-                   int64_t D, int64_t F, int act, hipStream_t s) {
+                   void *dwu, void *workspace, const GluBackward &b,
+                   int64_t M, int64_t D, int64_t F, int act, hipStream_t s) {
   Product<T> p = product_of<T>(x, wg, wu, M, D, F);
   p.gu = const_cast<float *>(saved);
   p.dh = (const T *)dh;
   p.dgu = (T *)workspace;
-  p.part = (float *)((char *)workspace + part_at);
-  return act == ADALN_ACT_SILU ? run_bwd<T, kSilu>(p, dx, dwg, dwu, s)
-                               : run_bwd<T, kGeluTanh>(p, dx, dwg, dwu, s);
+  p.dx = (T *)dx;
+  p.dw[0] = (T *)dwg;
+  p.dw[1] = (T *)dwu;
+  const hipError_t e = act == ADALN_ACT_SILU
+                           ? launch_gate_grads<T, kSilu>(p, s)
+                           : launch_gate_grads<T, kGeluTanh>(p, s);
+  if (e != hipSuccess) return e;
+  return launch_grads<T>(p, b, (char *)workspace, s);
 }
 
 }  // namespace
@@ -1104,7 +1258,7 @@ ADALN_API int adaln_glu_fwd(const void *x, const void *wg, const void *wu,
 ADALN_API size_t adaln_glu_bwd_workspace_bytes(int64_t M, int64_t D, int64_t F,
                                                int dtype) {
   if (check_glu(M, D, F, ADALN_ACT_SILU, dtype) != ADALN_OK || M == 0) return 0;
-  return glu_bwd_bytes(dtype, M, D, F, nullptr);
+  return glu_backward(dtype, M, D, F).bytes;
 }
 
 ADALN_API int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
@@ -1132,18 +1286,18 @@ ADALN_API int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
     if (e != hipSuccess) return hip_fail(e, "adaln_glu_bwd launch");
     return ok();
   }
-  size_t part_at = 0;
-  const size_t need = glu_bwd_bytes(dtype, M, D, F, &part_at);
+  const GluBackward b = glu_backward(dtype, M, D, F);
+  const size_t need = b.bytes;
   if (workspace == nullptr || workspace_bytes < need)
     return fail(ADALN_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s",
                 need, workspace_bytes, workspace == nullptr ? " (NULL)" : "");
   ADALN_TRY(check_ptr(workspace, true, "workspace"));
   const hipError_t e =
       dtype == ADALN_BF16
-          ? run_bwd<bf16>(dh, x, wg, wu, saved, dx, dwg, dwu, workspace,
-                          part_at, M, D, F, act, s)
-          : run_bwd<float>(dh, x, wg, wu, saved, dx, dwg, dwu, workspace,
-                           part_at, M, D, F, act, s);
+          ? run_bwd<bf16>(dh, x, wg, wu, saved, dx, dwg, dwu, workspace, b, M,
+                          D, F, act, s)
+          : run_bwd<float>(dh, x, wg, wu, saved, dx, dwg, dwu, workspace, b,
+                           M, D, F, act, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_glu_bwd launch");
   return ok();
 }

@@ -587,10 +587,14 @@ struct HeadsPlan {
 HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
                      int dtype, bool bwd) {
   HeadsPlan p;
-  const int rows = kBlock / lanes_per_head((int)(d / elems_per_vec(dtype)));
+  const int lanes = lanes_per_head((int)(d / elems_per_vec(dtype)));
+  const int rows = kBlock / lanes;
+  // both halves of the table of sines within 32 KiB of LDS
+  const int fits = 32768 / (2 * lanes * elems_per_vec(dtype) * 8);
   const int tensors = (Hq > 0) + (Hk > 0);
   p.tb = kMaxTokens;
-  while (p.tb > 1 && (p.tb * std::max(Hq, Hk) > kBlockRows * rows ||
+  while (p.tb > 1 && (p.tb > fits ||
+                      p.tb * std::max(Hq, Hk) > kBlockRows * rows ||
                       tensors * B * ((N + p.tb - 1) / p.tb) <
                           kFillBlocks * kCUs))
     p.tb /= 2;
@@ -642,15 +646,24 @@ void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
   job.pairs = rot->pairs;
 }
 
-// Radians per unit position -> turns, modulo 1, in 64 bits (long double keeps
-// the 64 bits of the product).
+// Radians per unit position -> turns, modulo 1, in 64 bits.  The double's 53
+// bits times 1 / (2 pi) to 128 bits, in integers: the fraction of a turn is
+// within a unit of its last place (and a call turns up to 384 of these).
 uint64_t turns_of(double radians) {
-  const long double t =
-      (long double)radians * 0.159154943091895335768883763372514362L;
-  // the whole turns go: |t| < 2^18, so truncation to an integer is exact
-  const long double f = t - (long double)(int64_t)t;  // in (-1, 1)
-  const long double g = (f < 0 ? f + 1 : f) * 18446744073709551616.0L;
-  return g >= 18446744073709551615.0L ? 0 : (uint64_t)(g + 0.5L);
+  // floor(2^128 / (2 pi))
+  constexpr uint64_t kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;
+  const uint64_t bits = __builtin_bit_cast(uint64_t, radians);
+  const int e = (int)(bits >> 52 & 0x7ff) - 1022;
+  if (e < -70) return 0;  // (subnormal ones among them)
+  // |radians| = m 2^(e - 53)
+  const uint64_t m = (bits & ((uint64_t(1) << 52) - 1)) | uint64_t(1) << 52;
+  // turns * 2^64 = m (kHi:kLo) 2^(e - 53 - 64), so the upper 128 bits of the
+  // product, to the right by 53 - e: at least 33, as |radians| <= 1e6
+  typedef unsigned __int128 u128;
+  const u128 t = (u128)m * kHi + (uint64_t)(((u128)m * kLo) >> 64);
+  const int shift = 53 - e;
+  const uint64_t f = (uint64_t)((t >> shift) + ((t >> (shift - 1)) & 1));
+  return radians < 0 ? ~f + 1 : f;
 }
 
 // The small form, where it holds the rotation.
@@ -850,9 +863,9 @@ ADALN_API int adaln_qk_norm_rope_bwd(
   ADALN_TRY(check_heads(dk, B, N, Hk, d, dtype, true, "dk"));
   ADALN_TRY(check_weight(wq, rows && Hq > 0, "wq"));
   ADALN_TRY(check_weight(wk, rows && Hk > 0, "wk"));
-  ADALN_TRY(check_weight(dwq, Hq > 0, "dwq"));
-  ADALN_TRY(check_weight(dwk, Hk > 0, "dwk"));
-  if (Hq + Hk == 0) return ok();
+  ADALN_TRY(check_weight(dwq, Hq > 0 || dwq != nullptr, "dwq"));
+  ADALN_TRY(check_weight(dwk, Hk > 0 || dwk != nullptr, "dwk"));
+  if (dwq == nullptr && dwk == nullptr) return ok();  // no heads at all
   HeadsPlan p = {};
   if (rows) p = heads_plan(B, N, Hq, Hk, d, dtype, true);
   const size_t need =
@@ -885,10 +898,10 @@ ADALN_API int adaln_qk_norm_rope_bwd(
                                 (hipStream_t)stream,
                                 "adaln_qk_norm_rope_bwd launch"));
   }
-  Sums sums = {{part[0], part[1]},
-               {Hq > 0 ? dwq : nullptr, Hk > 0 ? dwk : nullptr},
-               {(int32_t)p.grid[0], (int32_t)p.grid[1]},
-               (int32_t)d};
+  const Sums sums = {{part[0], part[1]},
+                     {dwq, dwk},
+                     {(int32_t)p.grid[0], (int32_t)p.grid[1]},
+                     (int32_t)d};
   const hipError_t e = launch_kernel_threads(
       sum_kernel, 2 * ((d + kSumCols - 1) / kSumCols), kSumSlices * kSumCols,
       (hipStream_t)stream, sums);

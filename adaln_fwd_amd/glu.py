@@ -34,6 +34,14 @@ def _shapes(x, wg, wu, act):
     return lead, M, D, F, code
 
 
+def _out(t, like, name):
+    """An output: as given, or a new one."""
+    if t is None:
+        return torch.empty_like(like)
+    _check(t, name, like.shape, like.dtype, like.device)
+    return t
+
+
 def glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, *,
             act: str = "silu", save: bool = False,
             h: Optional[torch.Tensor] = None,
@@ -46,14 +54,15 @@ def glu_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, *,
     lib = _lib.load()
     with _on(dev, stream):
         if h is None:
-            h = torch.empty(lead + (F,), dtype=x.dtype, device=dev)
-        _check(h, "h", lead + (F,), x.dtype, dev)
-        if not save and saved is not None:
-            raise ValueError("saved was given without save=True")
-        if save and saved is None:
-            saved = torch.empty(2, M, F, dtype=torch.float32, device=dev)
-        if save:
+            h = x.new_empty(lead + (F,))
+        else:
+            _check(h, "h", lead + (F,), x.dtype, dev)
+        if saved is not None:
+            if not save:
+                raise ValueError("saved was given without save=True")
             _check(saved, "saved", (2, M, F), torch.float32, dev)
+        elif save:
+            saved = x.new_empty((2, M, F), dtype=torch.float32)
         rc = lib.adaln_glu_fwd(_ptr(x), _ptr(wg), _ptr(wu), _ptr(h),
                                _ptr(saved), M, D, F, _ACTS[act], code,
                                _stream(dev, stream))
@@ -84,26 +93,20 @@ def glu_bwd(dh: torch.Tensor, x: torch.Tensor, wg: torch.Tensor,
     lib = _lib.load()
     need = int(lib.adaln_glu_bwd_workspace_bytes(M, D, F, code))
     with _on(dev, stream):
-        if dx is None:
-            dx = torch.empty_like(x)
-        if dwg is None:
-            dwg = torch.empty_like(wg)
-        if dwu is None:
-            dwu = torch.empty_like(wu)
-        _check(dx, "dx", lead + (D,), dt, dev)
-        _check(dwg, "dwg", (F, D), dt, dev)
-        _check(dwu, "dwu", (F, D), dt, dev)
+        dx = _out(dx, x, "dx")
+        dwg = _out(dwg, wg, "dwg")
+        dwu = _out(dwu, wu, "dwu")
         if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8,
-                                    device=dev)
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on "
-                             f"{dev}")
+            wbytes = max(need, 1)
+            workspace = x.new_empty(wbytes, dtype=torch.uint8)
+        else:
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on "
+                                 f"{dev}")
+            wbytes = workspace.numel() * workspace.element_size()
         rc = lib.adaln_glu_bwd(_ptr(dh), _ptr(x), _ptr(wg), _ptr(wu),
                                _ptr(saved), _ptr(dx), _ptr(dwg), _ptr(dwu),
-                               _ptr(workspace),
-                               workspace.numel() * workspace.element_size(),
-                               M, D, F, _ACTS[act], code,
+                               _ptr(workspace), wbytes, M, D, F, _ACTS[act], code,
                                _stream(dev, stream))
     _lib.check(rc, "adaln_glu_bwd")
     return dx, dwg, dwu

@@ -370,7 +370,8 @@ size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq,
  *     dx = r * (g - xh * mean_d(g * xh))     dw = sum over tokens, heads of t * xh
  *   q, k       the forward's inputs;  dq_out, dk_out: gradients of its outputs
  *   dq, dk     [B, N, H, d] dtype out
- *   dwq, dwk   [d] f32 out (overwritten; zero if there are no tokens)
+ *   dwq, dwk   [d] f32 out (overwritten; zero if there are no tokens or no
+ *              heads; NULL only for a tensor without heads)
  * One launch and a fixed-order sum of the workgroups' partial rows: results
  * are bitwise reproducible.
  */

@@ -86,6 +86,10 @@ CASES = [
     (4, 4100, 1, 1, 32, 16, 2, "interleaved", "f32"),   # blocks of 16 tokens
     (1, 20, 64, 16, 32, 16, 2, "half", "bf16"),
     (1, 16391, 2, 1, 64, 32, 3, "interleaved", "bf16"),  # many per workgroup
+    # the widest heads in blocks as long as the LDS admits
+    (1, 20001, 2, 1, 512, 192, 2, "interleaved", "bf16"),
+    (1, 20001, 1, 1, 512, 96, 4, "half", "f32"),
+    (500, 1, 3, 1, 32, 16, 1, "half", "bf16"),           # a batch of tokens
 ]
 
 
@@ -274,6 +278,23 @@ def test_non_finite_rows_stay_in_their_heads():
     # a head of zeros: r = 1 / sqrt(eps), dx = r * g
     np.testing.assert_allclose(got[6][0, 7, 0].cpu(), dx[0, 7, 0], rtol=1e-5,
                                atol=1e-5 * float(dx[0, 7, 0].abs().max()))
+
+
+def test_no_heads():
+    """A tensor without heads next to one with: its weight's gradient is 0."""
+    h = _inputs(1, 20, 2, 1, 64, "f32")
+    x = {n: v.cuda() for n, v in h.items()}
+    pos = torch.arange(20, dtype=torch.int32).reshape(-1, 1).cuda()
+    f = _freqs(32, 1)
+    none = x["q"][:, :, :0]
+    dq, dk, dwq, dwk = A.qk_norm_rope_bwd(none, x["dk"], none, x["k"],
+                                          x["wq"], x["wk"], pos, f)
+    assert dq.shape == none.shape and not dwq.any()
+    want = A.qk_norm_rope_bwd(None, x["dk"], None, x["k"], None, x["wk"], pos,
+                              f)
+    assert torch.equal(dk, want[1]) and torch.equal(dwk, want[3])
+    q, k = A.rope_fwd(none, none, pos, f)
+    assert q.shape == none.shape
 
 
 def test_empty():
