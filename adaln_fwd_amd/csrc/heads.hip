@@ -95,7 +95,6 @@ struct Job {
   int32_t blocks_n;       // blocks per sample
   int64_t blocks;
   int32_t cached;         // plain loads (else the streaming hint)
-  int32_t kept;           // plain stores
   float eps;
   float inv_d;
   float dir;              // +1: by the angle, -1: by the negative angle
@@ -384,14 +383,8 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
         rotate<E, HALF>(fa, fb, cs);
       }
       char *dst = const_cast<char *>(out.data) + k.at(out, r.tok, r.head);
-      const Vec oa = pack<T>(fa), ob = pack<T>(fb);
-      if (job.kept) {
-        if (r.live && ok_a) store_vec(dst + va * 16, oa);
-        if (r.live && ok_b) store_vec(dst + vb * 16, ob);
-      } else {
-        if (r.live && ok_a) store_stream(dst + va * 16, oa);
-        if (r.live && ok_b) store_stream(dst + vb * 16, ob);
-      }
+      if (r.live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
+      if (r.live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
     }
     k = after;
   }
@@ -617,19 +610,13 @@ HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
   return p;
 }
 
-// Which accesses carry the streaming hint, which keeps them from displacing
-// others in the 256 MB Infinity Cache.  While everything a call reads and
-// writes fits it with room to spare, inputs that another kernel has just
-// written may still lie there: plain loads, streaming stores.  Past that the
-// inputs stream; outputs that fit the cache are stored plainly (it takes the
-// writes and lets the memory read), larger ones stream too.  Measured on
-// MI355X (bf16, 24 heads of 128, three sets of tensors in turn; q + k bytes;
-// plain loads / plain stores / neither): rotation of 61 MB 21.7 / 24.5 / 25.4
-// us, 160 MB 59.6 / 52.8 / 57.7, 246 MB 88.2 / 76.6 / 85.8, 307 MB 108.8 /
-// 110.8 / 106.0; backward of the norm 61 MB 42.7 / 47.4 / 45.4, 160 MB 91.6 /
-// 87.7 / 92.5, 246 MB 140.4 / 127.0 / 135.4, 307 MB 173.4 / 176.0 / 167.3.
-constexpr int64_t kCachedBytes = int64_t(192) << 20;
-constexpr int64_t kKeptBytes = int64_t(256) << 20;
+// Inputs that another kernel has just written may still lie in the 256 MB
+// Infinity Cache; the streaming hint reads past it.  Up to twice its size of
+// bytes read and written, plain loads win (MI355X: backward of 24960 tokens x
+// 24 heads of 128 bf16, 460 MB, 86 -> 80 us; of 3554 tokens x 15 heads of 72
+// f32 17 -> 13 us); past it the hint does (75600 tokens x 80 heads, 4.6 GB:
+// 837 -> 806 us).
+constexpr int64_t kCachedBytes = int64_t(512) << 20;
 
 void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
               bool inverse, int tensors, int64_t B, int64_t N, int64_t Hq,
@@ -653,9 +640,7 @@ void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
   job.grid_q = (int32_t)p.grid[0];
   job.blocks_n = (int32_t)p.blocks_n;
   job.blocks = p.blocks;
-  const int64_t bytes = B * N * (Hq + Hk) * d * (16 / E);
-  job.cached = bytes * tensors <= kCachedBytes;
-  job.kept = !job.cached && bytes <= kKeptBytes;
+  job.cached = B * N * (Hq + Hk) * d * (16 / E) * tensors <= kCachedBytes;
   job.dir = inverse ? -1.f : 1.f;
   job.axes = rot->axes;
   job.pairs = rot->pairs;
