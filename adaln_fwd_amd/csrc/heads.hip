@@ -44,7 +44,7 @@ constexpr int kBwdPerCu = 6;    // workgroups per CU of the norm's backward
 // Frequencies in turns per unit position, as 64-bit fractions of a turn:
 // pos * turns, wrapping modulo 2^64, is the phase modulo one turn with no
 // loss for any position.  They travel as kernel arguments, whose size a
-// launch pays for (MI355X: 11 us per call with 3.5 KiB of them, 4.7 with
+// launch pays for (MI355X: 11 us per call with 3.5 KiB of them, 3.8 with
 // the small form), so the usual case, up to 64 pairs turned by one axis
 // each, has a form of its own.
 struct OneAxis {
@@ -610,12 +610,16 @@ HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
   return p;
 }
 
-// Inputs that another kernel has just written may still lie in the 256 MB
-// Infinity Cache; the streaming hint reads past it.  Up to twice its size of
-// bytes read and written, plain loads win (MI355X: backward of 24960 tokens x
-// 24 heads of 128 bf16, 460 MB, 86 -> 80 us; of 3554 tokens x 15 heads of 72
-// f32 17 -> 13 us); past it the hint does (75600 tokens x 80 heads, 4.6 GB:
-// 837 -> 806 us).
+// Inputs that another kernel has just written or read may still lie in the
+// 256 MB Infinity Cache; the streaming hint reads past it.  Up to twice its
+// size of bytes read and written plain loads win or lose little, past it the
+// hint is the better one.  MI355X, bf16, 24 heads of 128, three sets of inputs
+// and outputs in turn, plain loads against the hint: rotation of 10000 tokens
+// (122 MB) 21.8 against 25.4 us, 32760 (402 MB) 73.6 against 71.8, 90000 (1.1
+// GB) 196 against 187; backward of the norm of 24960 tokens (460 MB) right
+// behind its forward 80 against 86; of 75600 tokens x 80 heads (4.6 GB) 837
+// against 806.  (Plain stores of the outputs were slower from 100 MB on, but
+// for outputs written over again while the cache still held them.)
 constexpr int64_t kCachedBytes = int64_t(512) << 20;
 
 void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
