@@ -40,6 +40,7 @@ constexpr int kMaxTokens = 16;  // tokens per block
 constexpr int kBlockRows = 4;   // rows of a block per lane group, about
 constexpr int kFillBlocks = 4;  // blocks per CU before blocks get longer
 constexpr int kBwdPerCu = 6;    // workgroups per CU of the norm's backward
+constexpr int kSingleRows = 4;  // rows per lane group of a lone workgroup
 
 // Frequencies in turns per unit position, as 64-bit fractions of a turn:
 // pos * turns, wrapping modulo 2^64, is the phase modulo one turn with no
@@ -571,6 +572,11 @@ struct HeadsPlan {
   int64_t blocks_n;  // blocks per sample
   int64_t blocks;
   int64_t grid[2];   // workgroups of q and of k
+  // backward of so few rows that a workgroup per tensor takes them all, whose
+  // partial row is dw itself: no workspace and no second launch (MI355X, 24
+  // heads of 128, in a graph: 1 token 5.0 us, 8 tokens 7.1, 16 tokens 10.2;
+  // with the second launch 7.3 from 22 tokens on)
+  bool single;
 };
 
 // A block has up to kBlockRows rows for each lane group of a workgroup, and
@@ -586,7 +592,7 @@ struct HeadsPlan {
 // of heads.
 HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
                      int dtype, bool bwd) {
-  HeadsPlan p;
+  HeadsPlan p = {};
   const int lanes = lanes_per_head((int)(d / elems_per_vec(dtype)));
   const int rows = kBlock / lanes;
   // both halves of the table of sines within 32 KiB of LDS
@@ -598,8 +604,15 @@ HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
                       tensors * B * ((N + p.tb - 1) / p.tb) <
                           kFillBlocks * kCUs))
     p.tb /= 2;
+  p.single = bwd && B * N * std::max(Hq, Hk) <= kSingleRows * rows;
+  if (p.single) p.tb = std::min(kMaxTokens, fits);
   p.blocks_n = (N + p.tb - 1) / p.tb;
   p.blocks = B * p.blocks_n;
+  if (p.single) {
+    p.grid[0] = Hq > 0;
+    p.grid[1] = Hk > 0;
+    return p;
+  }
   const int64_t most = bwd ? kBwdPerCu * kCUs : kMaxGrid;
   const int64_t all = std::min(most, tensors * p.blocks);
   p.grid[0] = Hq == 0 ? 0 : Hk == 0 ? all : all * Hq / (Hq + Hk);
@@ -844,6 +857,7 @@ ADALN_API size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N,
   if (check_sizes(B, N, Hq, Hk, d, dtype) != ADALN_OK) return 0;
   if (B * N == 0 || Hq + Hk == 0) return 0;
   const HeadsPlan p = heads_plan(B, N, Hq, Hk, d, dtype, true);
+  if (p.single) return 0;
   return (size_t)(p.grid[0] + p.grid[1]) * (size_t)d * sizeof(float);
 }
 
@@ -873,7 +887,8 @@ ADALN_API int adaln_qk_norm_rope_bwd(
   HeadsPlan p = {};
   if (rows) p = heads_plan(B, N, Hq, Hk, d, dtype, true);
   const size_t need =
-      (size_t)(p.grid[0] + p.grid[1]) * (size_t)d * sizeof(float);
+      p.single ? 0
+               : (size_t)(p.grid[0] + p.grid[1]) * (size_t)d * sizeof(float);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
       return fail(ADALN_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu%s",
@@ -881,8 +896,11 @@ ADALN_API int adaln_qk_norm_rope_bwd(
                   workspace == nullptr ? " (NULL)" : "");
     ADALN_TRY(check_weight(workspace, true, "workspace"));
   }
-  float *part[2] = {static_cast<float *>(workspace),
-                    static_cast<float *>(workspace) + p.grid[0] * d};
+  float *part[2] = {dwq, dwk};
+  if (!p.single) {
+    part[0] = static_cast<float *>(workspace);
+    part[1] = part[0] + p.grid[0] * d;
+  }
   if (rows) {
     Job job = {};
     fill_job(job, p, rot, true, 3, B, N, Hq, Hk, d, dtype);
@@ -902,6 +920,8 @@ ADALN_API int adaln_qk_norm_rope_bwd(
                                 (hipStream_t)stream,
                                 "adaln_qk_norm_rope_bwd launch"));
   }
+  if (p.single && p.grid[0] + p.grid[1] == (dwq != nullptr) + (dwk != nullptr))
+    return ok();
   const Sums sums = {{part[0], part[1]},
                      {dwq, dwk},
                      {(int32_t)p.grid[0], (int32_t)p.grid[1]},

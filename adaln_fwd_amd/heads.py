@@ -37,33 +37,27 @@ def rope_freqs(pairs: Sequence[int], theta: float = 10000.0) -> np.ndarray:
     return out
 
 
-def _heads(t, name, lead, d, dtype, device) -> Optional[_lib.Heads]:
-    """Descriptor of one tensor of heads, or None for None."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    shape, st = t.shape, t.stride()
-    # (one condition for calls that are right; which one failed comes after)
-    if not (t.dtype is dtype and t.device == device and t.is_cuda
-            and len(shape) == len(lead) + 2 and shape[:-2] == lead
-            and shape[-1] == d and (st[-1] == 1 or d == 1)):
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor, got {device}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if len(shape) != len(lead) + 2 or shape[:-2] != lead or shape[-1] != d:
-            raise ValueError(f"{name} has shape {tuple(shape)}, expected "
-                             f"{tuple(lead) + ('H', d)}")
-        raise ValueError(f"{name}: the features of a head must be contiguous")
-    return _lib.Heads(_ptr(t), st[0] if len(lead) == 2 else 0, st[-3], st[-2])
+def _wrong(t, name, shape, dtype, device):
+    """Raises for what _heads found wrong with a tensor."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor, got {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != len(shape) or t.shape[:-2] != shape[:-2] \
+            or t.shape[-1] != shape[-1]:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{tuple(shape[:-2]) + ('H', shape[-1])}")
+    raise ValueError(f"{name}: the features of a head must be contiguous")
 
 
 class _Call:
     """What the four entry points share: shapes, device, the rotation and the
     descriptors of the inputs."""
+
+    __slots__ = ("dev", "index", "dt", "code", "shape", "four", "B", "N", "d",
+                 "q", "k", "Hq", "Hk", "freqs", "rot")
 
     def __init__(self, q, k, pos, freqs, layout):
         ref = q if q is not None else k
@@ -71,19 +65,24 @@ class _Call:
             raise ValueError("q and k are both None")
         if not isinstance(ref, torch.Tensor):
             raise TypeError("q and k must be torch.Tensors")
-        if ref.dim() not in (3, 4):
-            raise ValueError("q and k must be [B, N, H, d] or [T, H, d], got "
-                             f"shape {tuple(ref.shape)}")
         shape = ref.shape
+        if len(shape) not in (3, 4):
+            raise ValueError("q and k must be [B, N, H, d] or [T, H, d], got "
+                             f"shape {tuple(shape)}")
         self.dev, self.dt = ref.device, ref.dtype
+        self.index = ref.get_device()
         self.code = _code(ref)
-        self.lead, self.d = shape[:-2], shape[-1]
-        self.B = shape[0] if len(shape) == 4 else 1
+        self.shape = shape
+        self.four = len(shape) == 4
+        self.B = shape[0] if self.four else 1
         self.N = N = shape[-3]
-        self.q = _heads(q, "q", self.lead, self.d, self.dt, self.dev)
-        self.k = _heads(k, "k", self.lead, self.d, self.dt, self.dev)
-        self.Hq = q.shape[-2] if q is not None else 0
-        self.Hk = k.shape[-2] if k is not None else 0
+        self.d = shape[-1]
+        self.Hq = self.Hk = 0
+        self.q = self.k = None
+        if q is not None:
+            self.q, self.Hq = self.heads(q, "q"), q.shape[-2]
+        if k is not None:
+            self.k, self.Hk = self.heads(k, "k"), k.shape[-2]
         if layout not in _LAYOUTS:
             raise ValueError("layout must be 'interleaved' or 'half', got "
                              f"{layout!r}")
@@ -93,25 +92,37 @@ class _Call:
                                  "tensor or an array")
             freqs = freqs.numpy()
         # contiguous float64; the caller's own array when it already is
-        self.freqs = np.ascontiguousarray(freqs, dtype=np.float64)
-        if self.freqs.ndim != 2:
+        self.freqs = freqs = np.ascontiguousarray(freqs, dtype=np.float64)
+        if freqs.ndim != 2:
             raise ValueError("freqs must be [axes, pairs], got shape "
-                             f"{self.freqs.shape}")
-        axes, pairs = self.freqs.shape
+                             f"{freqs.shape}")
+        axes, pairs = freqs.shape
         if not isinstance(pos, torch.Tensor):
             raise TypeError("pos must be a torch.Tensor")
-        shared = pos.dim() == 2 or len(shape) == 3
+        shared = pos.dim() == 2 or not self.four
         _check(pos, "pos", (N, axes) if shared else (self.B, N, axes),
                torch.int32, self.dev)
         self.rot = _lib.Rotation(_ptr(pos), 0 if shared else N * axes,
-                                 self.freqs.__array_interface__["data"][0],
-                                 axes, pairs, _LAYOUTS[layout])
+                                 freqs.__array_interface__["data"][0], axes,
+                                 pairs, _LAYOUTS[layout])
 
-    def heads(self, t, name, like=None):
-        if like is not None and t is not None and t.shape != like.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+    def heads(self, t, name, like=None) -> Optional[_lib.Heads]:
+        """Descriptor of one tensor of heads, or None for None."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        shape, st = t.shape, t.stride()
+        if like is not None and shape != like.shape:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                              f"{tuple(like.shape)}")
-        return _heads(t, name, self.lead, self.d, self.dt, self.dev)
+        # one condition for calls that are right; which one failed comes after
+        if not (t.is_cuda and t.get_device() == self.index
+                and t.dtype is self.dt and len(shape) == len(self.shape)
+                and shape[-1] == self.d and shape[-3] == self.N
+                and shape[0] == self.shape[0] and (st[-1] == 1 or self.d == 1)):
+            _wrong(t, name, self.shape, self.dt, self.dev)
+        return _lib.Heads(_ptr(t), st[0] if self.four else 0, st[-3], st[-2])
 
     def out(self, t, like, name):
         """An output and its descriptor: as given, or a contiguous one."""

@@ -361,7 +361,8 @@ int adaln_qk_norm_rope_fwd(const adaln_heads_t *q, const adaln_heads_t *k,
                            void *stream);
 
 /* Bytes of device workspace of adaln_qk_norm_rope_bwd (partial sums of the
- * weights' gradients).  A pure function of its arguments; 0 for invalid ones. */
+ * weights' gradients).  A pure function of its arguments; 0 for invalid ones
+ * and for so few tokens that none is needed (NULL will do then). */
 size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq,
                                               int64_t Hk, int64_t d, int dtype);
 
@@ -372,8 +373,8 @@ size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq,
  *   dq, dk     [B, N, H, d] dtype out
  *   dwq, dwk   [d] f32 out (overwritten; zero if there are no tokens or no
  *              heads; NULL only for a tensor without heads)
- * One launch and a fixed-order sum of the workgroups' partial rows: results
- * are bitwise reproducible.
+ * One launch and a fixed-order sum of the workgroups' partial rows (no second
+ * launch for few tokens): results are bitwise reproducible.
  */
 int adaln_qk_norm_rope_bwd(
     const adaln_heads_t *dq_out, const adaln_heads_t *dk_out,

@@ -153,20 +153,26 @@ def test_refusals_of_the_norm(lib):
                               (P, P, float("nan"), _lib.ERR_INVALID),
                               (P, P, float("inf"), _lib.ERR_INVALID)]:
         assert f(_h(), _h(), wq, wk, eps, _rot(), _h(), _h(), *size) == code
+    # so few tokens need no workspace; 500 per sample do
+    assert lib.adaln_qk_norm_rope_bwd_workspace_bytes(*size[:-1]) == 0
+    size = (2, 500) + size[2:]
     need = lib.adaln_qk_norm_rope_bwd_workspace_bytes(*size[:-1])
     assert need > 0 and need % (2 * 64 * 4) == 0
 
+    def _far(data=P, b=64 * 2 * 500):
+        return ctypes.byref(_lib.Heads(data, b, 128, 64))
+
     def g(dwq=P, dwk=P, ws=P, n=need, dy=None):
         return lib.adaln_qk_norm_rope_bwd(
-            dy or _h(), _h(), _h(), _h(), P, P, 1e-6, _rot(), _h(), _h(), dwq,
-            dwk, ws, n, *size)
+            dy or _far(), _far(), _far(), _far(), P, P, 1e-6, _rot(), _far(),
+            _far(), dwq, dwk, ws, n, *size)
 
     assert g(ws=None) == _lib.ERR_WORKSPACE
     assert g(n=need - 1) == _lib.ERR_WORKSPACE
     assert b"workspace" in lib.adaln_last_error()
     assert g(ws=P + 4) == _lib.ERR_ALIGN
     assert g(dwq=None) == _lib.ERR_INVALID
-    assert g(dy=_h(data=None)) == _lib.ERR_INVALID
+    assert g(dy=_far(data=None)) == _lib.ERR_INVALID
 
 
 def test_empty_calls_need_nothing(lib):
