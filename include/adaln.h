@@ -374,7 +374,7 @@ size_t adaln_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq,
  *   dwq, dwk   [d] f32 out (overwritten; zero if there are no tokens or no
  *              heads; NULL only for a tensor without heads)
  * One launch and a fixed-order sum of the workgroups' partial rows (no second
- * launch for few tokens): results are bitwise reproducible.
+ * launch for few tokens): the same call repeats bit for bit.
  */
 int adaln_qk_norm_rope_bwd(
     const adaln_heads_t *dq_out, const adaln_heads_t *dk_out,
