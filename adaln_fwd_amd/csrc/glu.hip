@@ -701,7 +701,7 @@ product_kernel(Product<T> p, Tiles q) {
   product<T, FORM, TILING, ACT>(p, q, blockIdx.x + q.block0, lds);
 }
 
-// dx and dW in one launch, for calls whose tiles of either alone leave CUs
+// dx and dW in one launch, where the tiles of either alone would leave CUs
 // idle; the product with the longer blocks comes first.
 template <typename T, int TILING>
 __global__ __launch_bounds__(tiling_threads(TILING),
@@ -925,7 +925,7 @@ struct Shape {
 // of f32 a step has half the elements at a sixteenth of the rate): the big
 // ones run one to a CU, 1.65 per step and 5 for filling the pipeline and
 // storing; the small ones two to a CU, 1.0 and 4; the deep ones one to a CU,
-// 0.5 and 4 (MI355X, D = 1536, F = 4096, forward: 256 tokens 15.7 us deep
+// 0.55 and 4 (MI355X, D = 1536, F = 4096, forward: 256 tokens 15.7 us deep
 // against 20.5 small, 1024 tokens 31.6 against 27.7).  Adding slices up takes
 // 4 and, per partial sum, 2 x 4 bytes at 5 TB/s.
 struct Costs {
@@ -937,7 +937,7 @@ struct Costs {
     fill = tiling == kBig ? 5 : 4;
     step = dtype == ADALN_F32
                ? (tiling == kBig ? 9 : tiling == kSmall ? 4.5 : 2.3)
-               : (tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.5);
+               : (tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.55);
   }
   double adding(int64_t blocks) const {
     return 4 + 8e-6 / 5 * blocks * tile * tile;
@@ -1005,47 +1005,77 @@ struct GluBackward {
   size_t x_part = 0, w_part = 0;  // offsets
 };
 
+// When the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, on `slots`
+// that each take the next block when they are free.
+double makespan(int64_t slots, int64_t n1, double t1, int64_t n2, double t2) {
+  if (n1 + n2 <= slots) return n1 > 0 ? t1 : t2;
+  const int64_t rounds = n1 / slots, late = n1 - rounds * slots;
+  // `late` slots start on the second kind at s1, the others at s0
+  const double s0 = rounds * t1, s1 = late > 0 ? s0 + t1 : s0;
+  if (n2 == 0) return s1;
+  auto done = [&](double t) {
+    auto of = [&](double s) {
+      return t >= s ? (int64_t)((t - s) / t2 + 1e-9) : 0;
+    };
+    return late * of(s1) + (slots - late) * of(s0) >= n2;
+  };
+  // it ends a whole number of blocks after s0 or s1, no sooner than the
+  // average load
+  const double average = (n1 * t1 + n2 * t2) / slots;
+  double best = 0;
+  for (double s : {s0, s1}) {
+    double t = s + std::max<double>(1, (int64_t)((average - s) / t2)) * t2;
+    while (!done(t)) t += t2;
+    if (best == 0 || t < best) best = t;
+  }
+  return std::max(best, s1);
+}
+
 // In one launch where the model finds that shorter: all tiles of both
-// products, in slices or not, taken by free CUs in turn (the average load and
-// half the longest block, or the longest block where all run at once).  Two
-// launches cost 3 more.  Measured on MI355X, whole backward, two launches
-// against one: 777 x 1000 x 1480 40.5 -> 33.6 us, 4096 x 256 x 1024 47.5 ->
-// 37.4, 64 x 512 x 1024 24.4 -> 21.5.
+// products, in slices or not, taken by free CUs in turn, the longer ones
+// first.  Two launches cost 3 more.  Measured on MI355X, whole backward, two
+// launches against one: 777 x 1000 x 1480 40.5 -> 33.6 us, 4096 x 256 x 1024
+// 47.5 -> 37.4, 64 x 512 x 1024 24.4 -> 21.5; big tiles, which fill the
+// rounds that the other product leaves open: 8190 x 1536 x 4096 536 -> 424,
+// 12000 x 1000 x 3000 444 -> 351, 24960 x 1536 x 4096 1341 -> 1313.  (Where
+// it is wrong it costs less: 3000 x 640 x 5000 142 -> 157.)
 GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
   GluBackward b;
   b.x = glu_plan(kDx, dtype, M, D, F);
   b.w = glu_plan(kDw, dtype, M, D, F);
-  if (b.x.tiling != kBig || b.w.tiling != kBig) {
-    const Shape hx(kDx, dtype, M, D, F), hw(kDw, dtype, M, D, F);
-    double best = b.x.us + b.w.us + 3;
-    constexpr int64_t kTry[] = {1, 2, 3, 4, 6, 8, 12, 16};
-    for (int tiling : {(int)kSmall, (int)kDeep}) {
-      const Costs k(tiling, dtype);
-      const int64_t nx = cut(hx, tiling, k.tile, 0, 1, hx.steps).blocks;
-      const int64_t nw = cut(hw, tiling, k.tile, 0, 1, hw.steps).blocks;
-      for (int64_t sx : kTry) {
-        const int64_t px = (hx.steps + sx - 1) / sx;
-        if (sx > 1 && (hx.steps < 4 * sx || (hx.steps + px - 1) / px != sx))
+  const Shape hx(kDx, dtype, M, D, F), hw(kDw, dtype, M, D, F);
+  double best = b.x.us + b.w.us + 3;
+  for (int tiling : {(int)kSmall, (int)kBig, (int)kDeep}) {
+    // (f32's small tiles are as fast as its big ones and end more evenly)
+    if (tiling == kBig && dtype == ADALN_F32) continue;
+    const Costs k(tiling, dtype);
+    const int64_t nx = cut(hx, tiling, k.tile, 0, 1, hx.steps).blocks;
+    const int64_t nw = cut(hw, tiling, k.tile, 0, 1, hw.steps).blocks;
+    // (many tiles: the slices' sums would cost more than they even out)
+    const int64_t most = nx + nw > 4 * k.slots ? 1 : 16;
+    for (int64_t sx : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      const int64_t px = (hx.steps + sx - 1) / sx;
+      if (sx > most) break;
+      if (sx > 1 && (hx.steps < 4 * sx || (hx.steps + px - 1) / px != sx))
+        continue;
+      for (int64_t sw : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        const int64_t pw = (hw.steps + sw - 1) / sw;
+        if (sw > most) break;
+        if (sw > 1 && (hw.steps < 4 * sw || (hw.steps + pw - 1) / pw != sw))
           continue;
-        for (int64_t sw : kTry) {
-          const int64_t pw = (hw.steps + sw - 1) / sw;
-          if (sw > 1 && (hw.steps < 4 * sw || (hw.steps + pw - 1) / pw != sw))
-            continue;
-          const double tx = px * k.step + k.fill, tw = pw * k.step + k.fill;
-          const int64_t blocks = nx * sx + nw * sw;
-          const double longest = std::max(tx, tw);
-          double us = blocks <= k.slots
-                          ? longest
-                          : (nx * sx * tx + nw * sw * tw) / k.slots +
-                                longest / 2;
-          if (sx > 1 || sw > 1)
-            us += k.adding((sx > 1 ? nx * sx : 0) + (sw > 1 ? nw * sw : 0));
-          if (us >= best || blocks > kMaxGrid) continue;
-          best = us;
-          b.joint = true;
-          b.x = cut(hx, tiling, k.tile, nx, sx, px);
-          b.w = cut(hw, tiling, k.tile, nw, sw, pw);
-        }
+        const double tx = px * k.step + k.fill, tw = pw * k.step + k.fill;
+        if (nx * sx + nw * sw > kMaxGrid ||
+            (nx * sx * tx + nw * sw * tw) / k.slots >= best)
+          continue;
+        double us = tw > tx ? makespan(k.slots, nw * sw, tw, nx * sx, tx)
+                            : makespan(k.slots, nx * sx, tx, nw * sw, tw);
+        if (sx > 1 || sw > 1)
+          us += k.adding((sx > 1 ? nx * sx : 0) + (sw > 1 ? nw * sw : 0));
+        if (us >= best) continue;
+        best = us;
+        b.joint = true;
+        b.x = cut(hx, tiling, k.tile, nx, sx, px);
+        b.w = cut(hw, tiling, k.tile, nw, sw, pw);
       }
     }
   }
@@ -1124,18 +1154,21 @@ hipError_t launch_grads(const Product<T> &p, const GluBackward &b, char *ws,
   GluPlan x = b.x, w = b.w;
   x.part = (float *)(ws + b.x_part);
   w.part = (float *)(ws + b.w_part);
-  hipError_t e;
+  hipError_t e = hipSuccess;
   if (b.joint) {
     const bool w_first = w.per_slice > x.per_slice;
     const int32_t first = (int32_t)(w_first ? w.blocks : x.blocks);
     const int64_t n = x.blocks + w.blocks;
-    e = x.tiling == kSmall
-            ? launch_kernel_threads(grads_kernel<T, kSmall>, n, 256, s, p,
-                                    (Tiles)x, (Tiles)w, first,
-                                    (int32_t)w_first)
-            : launch_kernel_threads(grads_kernel<T, kDeep>, n, 256, s, p,
-                                    (Tiles)x, (Tiles)w, first,
-                                    (int32_t)w_first);
+    auto go = [&](auto kernel) {
+      return launch_kernel_threads(kernel, n, tiling_threads(x.tiling), s, p,
+                                   (Tiles)x, (Tiles)w, first,
+                                   (int32_t)w_first);
+    };
+    if constexpr (kDtype<T> == ADALN_BF16) {
+      if (x.tiling == kBig) e = go(grads_kernel<T, kBig>);
+    }
+    if (x.tiling == kSmall) e = go(grads_kernel<T, kSmall>);
+    if (x.tiling == kDeep) e = go(grads_kernel<T, kDeep>);
     if (e != hipSuccess) return e;
     return launch_slices<T>(p, x, w, s);
   }

@@ -48,7 +48,8 @@ SIZES = [
     (129, 136, 264), (200, 1000, 1480), (255, 64, 64), (257, 72, 2056),
     (777, 1000, 1480), (1024, 512, 512), (1030, 264, 4104), (3001, 8, 16),
     (2500, 1536, 2048), (4097, 520, 1288), (300, 5120, 640),
-    (2048, 2048, 4096),
+    (2048, 2048, 4096), (4100, 512, 2064), (4097, 1032, 2056),
+    (1000, 2048, 2048),
 ]
 
 
