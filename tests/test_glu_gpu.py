@@ -289,8 +289,12 @@ def test_offsets_past_32_bits():
     _say(f"M*F = {M * F}")
     _, x, wg, wu = [t.cuda() for t in _whole(1000, D, F, 5)]
     x = x.repeat(M // 1000, 1)
-    dh = torch.randint(-1, 2, (1000, F), device="cuda",
-                       dtype=torch.int8).to(torch.bfloat16)
+    # one in four is not zero: the largest sums, of dh * 64 * 8 over 1000
+    # tokens 270 times, have a deviation of 2.2e6, an eighth of 2^24
+    g = torch.Generator().manual_seed(6)
+    dh = torch.randint(-1, 2, (1000, F), generator=g)
+    dh = (dh * (torch.rand(1000, F, generator=g) < 0.375)).cuda()
+    dh = dh.to(torch.bfloat16)
     dh = dh.repeat(M // 1000, 1)
     h = A.glu_fwd(x, wg, wu)
     dx, dwg, dwu = A.glu_bwd(dh, x, wg, wu)
