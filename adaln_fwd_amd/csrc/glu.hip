@@ -7,9 +7,10 @@
 //
 // Four products of one shape of loop, all on the matrix cores (bf16 or f32
 // operands, float32 sums): a workgroup computes a tile of rows x columns,
-// walking the summed dimension in steps of 128 bytes.  Each step's two operand tiles go from
-// memory straight to LDS (16 bytes per lane, no registers), double-buffered:
-// the loads of step s + 1 are in flight while step s is multiplied.
+// walking the summed dimension in steps of 128 bytes.  Each step's two operand
+// tiles go from memory straight to LDS (16 bytes per lane, no registers),
+// double-buffered: the loads of step s + 1 are in flight while step s is
+// multiplied.
 //
 // An operand is stored with the summed dimension contiguous (x and W in the
 // forward) or across it (W in dx; both in dW).  Its LDS tile keeps the
@@ -51,9 +52,9 @@ constexpr int kStep = 128 / sizeof(T);
 
 // 16 bytes per lane from memory to LDS at `lds` + 16 * lane: a wave-uniform
 // base and a 32-bit offset per lane.  Outstanding loads are waited for by
-// arrive() below, by hand: the compiler does not see these loads.  (m0 takes the LDS address; nothing
-// else in these kernels uses it.  The s_nop is the wait state that the ISA
-// asks for between writing m0 and a load to LDS.)
+// arrive() below, by hand: the compiler does not see these loads.  (m0 takes
+// the LDS address; nothing else in these kernels uses it.  The s_nop is the
+// wait state that the ISA asks for between writing m0 and a load to LDS.)
 __device__ __forceinline__ void dma(uint32_t lds, const void *base,
                                     uint32_t offset) {
   asm volatile(
@@ -292,6 +293,13 @@ __device__ __forceinline__ void load4(const float *p, float (&f)[4]) {
   for (int e = 0; e < 4; ++e) f[e] = elem<float>(v, e);
 }
 
+__device__ __forceinline__ void store4(bf16 *p, const float (&f)[4]) {
+  *reinterpret_cast<uint2 *>(p) = pack4(f);
+}
+__device__ __forceinline__ void store4(float *p, const float (&f)[4]) {
+  store_vec(p, pack<float>(f));
+}
+
 // Eight neighbouring elements, 16-byte aligned.
 __device__ __forceinline__ void store8(bf16 *p, const float (&f)[8]) {
   store_vec(p, pack<bf16>(f));
@@ -369,6 +377,7 @@ struct Product {
   T *dx;                  // [M, D]
   T *dw[2];               // dWg, dWu [F, D]
   int32_t M, D, F;
+  int32_t fold;           // not 0: dx's row m is the sum of rows m, m + fold
 };
 
 // How a product is cut: tiles of a plane (dW has two), `full` of them
@@ -457,7 +466,7 @@ __device__ __forceinline__ void product(const Product<T> &p, const Tiles &q,
     split = (id - q.full) / q.rem;
     n = q.full + xcd_run(id - q.full - split * q.rem, q.rem);
   }
-  const bool partial = id >= q.full && q.slices > 1;
+  const bool partial = id >= q.full;
   int plane, tr, tc;
   tile_of(n, q.tiles_r, q.tiles_c, plane, tr, tc);
   const int row0 = tr * kTile, col0 = tc * kCols;
@@ -716,6 +725,29 @@ grads_kernel(Product<T> p, Tiles x, Tiles w, int32_t first, int32_t w_first) {
     product<T, kDw, TILING, 0>(p, w, id, lds);
 }
 
+// dG, dU of 8 elements from G, U [2, n].
+template <typename T, int ACT>
+__device__ __forceinline__ void gate_grads(const float *gu, const T *dh,
+                                           int64_t n, int64_t at,
+                                           float (&dg)[8], float (&du)[8]) {
+  Vec d[8 / Elems<T>::value];
+#pragma unroll
+  for (int i = 0; i < 8 / Elems<T>::value; ++i)
+    d[i] = load_stream(dh + at + i * Elems<T>::value);
+  const Vec g0 = load_stream(gu + at), g1 = load_stream(gu + at + 4);
+  const Vec u0 = load_stream(gu + n + at), u1 = load_stream(gu + n + at + 4);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float g = elem<float>(e < 4 ? g0 : g1, e % 4);
+    const float u = elem<float>(e < 4 ? u0 : u1, e % 4);
+    const float t = elem<T>(d[e / Elems<T>::value], e % Elems<T>::value);
+    float a, da;
+    activate<ACT>(g, a, da);
+    dg[e] = t * u * da;
+    du[e] = t * a;
+  }
+}
+
 // dG, dU from the saved G, U: one pass, 8 elements per thread.
 template <typename T, int ACT>
 __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
@@ -724,25 +756,45 @@ __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
   const int64_t stride = (int64_t)gridDim.x * kBlock * 8;
   for (int64_t at = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8; at < n;
        at += stride) {
-    Vec d[8 / Elems<T>::value];
-#pragma unroll
-    for (int i = 0; i < 8 / Elems<T>::value; ++i)
-      d[i] = load_stream(dh + at + i * Elems<T>::value);
-    const Vec g0 = load_stream(gu + at), g1 = load_stream(gu + at + 4);
-    const Vec u0 = load_stream(gu + n + at), u1 = load_stream(gu + n + at + 4);
     float dg[8], du[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float g = elem<float>(e < 4 ? g0 : g1, e % 4);
-      const float u = elem<float>(e < 4 ? u0 : u1, e % 4);
-      const float t = elem<T>(d[e / Elems<T>::value], e % Elems<T>::value);
-      float a, da;
-      activate<ACT>(g, a, da);
-      dg[e] = t * u * da;
-      du[e] = t * a;
-    }
+    gate_grads<T, ACT>(gu, dh, n, at, dg, du);
     store8(dgu + at, dg);
     store8(dgu + n + at, du);
+  }
+}
+
+// The same for few tokens, without the rounding to bf16: each of dG, dU is the
+// sum of two bf16 (exact to 2^-16), the second in the rows of as many tokens
+// more, and x stands there twice.  The products of 2 M tokens then give dW,
+// and dx in the sums of rows m and M + m.
+template <int ACT>
+__global__ __launch_bounds__(kBlock) void split_grads_kernel(
+    const float *__restrict__ gu, const bf16 *__restrict__ dh,
+    const bf16 *__restrict__ x, bf16 *__restrict__ dgu, bf16 *__restrict__ x2,
+    int64_t n, int64_t n_x) {
+  const int64_t stride = (int64_t)gridDim.x * kBlock * 8;
+  for (int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8;
+       i < n + n_x; i += stride) {
+    if (i >= n) {
+      const Vec v = load_vec(x + i - n);
+      store_vec(x2 + i - n, v);
+      store_vec(x2 + n_x + i - n, v);
+      continue;
+    }
+    float d[2][8];
+    gate_grads<bf16, ACT>(gu, dh, n, i, d[0], d[1]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const Vec hi = pack<bf16>(d[q]);
+      float lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = elem<bf16>(hi, e);
+        lo[e] = fabsf(f) < INFINITY ? d[q][e] - f : 0.f;
+      }
+      store_vec(dgu + 2 * q * n + i, hi);
+      store8(dgu + (2 * q + 1) * n + i, lo);
+    }
   }
 }
 
@@ -751,8 +803,8 @@ __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
 // kHidden and kGrads of up to 16 * TB tokens: bound by the weights' bytes, so
 // they go from memory to registers as matrix fragments, each read once, and
 // the tokens' fragments come from the caches.  A workgroup owns 16 hidden
-// features; its 8 wavefronts take the steps of 64 bytes of the sum in turn (so that
-// together they read 512 contiguous bytes of every row), four steps'
+// features; its 8 wavefronts take the steps of 64 bytes of the sum in turn (so
+// that together they read 512 contiguous bytes of every row), four steps'
 // loads in flight each, and their sums meet in LDS, added in order.  (Plain
 // loads: with the streaming hint one token took 8.4 us, not 7.4, D = 1536, F =
 // 4096; 32 features per workgroup, 11.6.)
@@ -851,38 +903,58 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product<T> p) {
   }
 }
 
-// The tiles of dx and of dW that were computed in slices: the sum of these,
-// in slice order.
+// The tiles of dx (`blocks_x` workgroups) and of dW that were computed in
+// slices: the sum of these, in slice order (of folded rows, both in turn).
+// Four elements per thread, in a tile of the workgroup's own, so that the
+// tile's place is scalar arithmetic, and several loads in flight: over few
+// tokens it is a chain of instructions with nothing beside it (MI355X, 12
+// slices of 1 x 1536: 6.9 -> 4.0 us, of 64 x 1536 8.0 -> 4.9, against 8
+// elements per thread of any tile).
+constexpr int kSumElems = 4 * kBlock;  // of a workgroup
+
 template <typename T>
 __global__ __launch_bounds__(kBlock) void slices_kernel(Product<T> p, Tiles x,
-                                                        Tiles w) {
-  const int64_t size_x = (int64_t)x.tile() * x.tile();
-  const int64_t size_w = (int64_t)w.tile() * w.tile();
-  const int64_t all_x = x.rem * size_x / 8;
-  const int64_t total = all_x + w.rem * size_w / 8;
-  for (int64_t at = (int64_t)blockIdx.x * kBlock + threadIdx.x; at < total;
-       at += (int64_t)gridDim.x * kBlock) {
-    const bool is_w = at >= all_x;
-    const Tiles &q = is_w ? w : x;
-    const int64_t size = is_w ? size_w : size_x;
-    const int64_t i = is_w ? at - all_x : at;
-    const int t = (int)(i / (size / 8));
-    const int in = (int)(i - t * (size / 8));
-    int plane, tr, tc;
-    tile_of(q.full + t, q.tiles_r, q.tiles_c, plane, tr, tc);
-    const int tile = q.tile(), per_row = tile / 8;
-    const int r = tr * tile + in / per_row, c = tc * tile + in % per_row * 8;
-    if (r >= (is_w ? p.F : p.M) || c >= p.D) continue;
-    const float *src = q.part + t * size + (int64_t)in * 8;
-    float v[8] = {};
-    for (int s = 0; s < q.slices; ++s) {
-      const Vec a = load_stream(src), b = load_stream(src + 4);
+                                                        Tiles w,
+                                                        int32_t blocks_x) {
+  constexpr int kBatch = 8;
+  const bool is_w = (int)blockIdx.x >= blocks_x;
+  const Tiles q = is_w ? w : x;
+  const int id = blockIdx.x - (is_w ? blocks_x : 0);
+  const int bits = q.tiling == kBig ? 8 : 7;  // of a tile's side
+  const int tile = 1 << bits, size = tile << bits;
+  const int t = id / (size / kSumElems);
+  const int in = (id * kBlock + (int)threadIdx.x) * 4 - t * size;
+  int plane, tr, tc;
+  tile_of(q.full + t, q.tiles_r, q.tiles_c, plane, tr, tc);
+  const int fold = is_w ? 0 : p.fold;
+  const int rows = is_w ? p.F : fold > 0 ? fold : p.M;
+  const int r = tr * tile + (in >> bits), c = tc * tile + (in & (tile - 1));
+  if (r >= rows || c >= p.D) return;
+  const float *src = q.part + (int64_t)t * size + in;
+  const int64_t next = (int64_t)q.rem * size;
+  float v[4] = {};
+  auto add = [&](auto two) {
+    const int terms = q.slices << two;
+    for (int s = 0; s < terms; s += kBatch) {
+      Vec a[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += elem<float>(e < 4 ? a : b, e % 4);
-      src += q.rem * size;
+      for (int i = 0; i < kBatch; ++i) {
+        const int n = min(s + i, terms - 1);
+        a[i] = load_stream(src + (n >> two) * next + (n & two) * fold * tile);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] += s + i < terms ? elem<float>(a[i], e) : 0.f;
     }
-    store8((is_w ? p.dw[plane] : p.dx) + (int64_t)r * p.D + c, v);
-  }
+  };
+  if (fold > 0)
+    add(std::integral_constant<int, 1>());
+  else
+    add(std::integral_constant<int, 0>());
+  T *out = is_w ? p.dw[plane] : p.dx;
+  store4(out + (int64_t)r * p.D + c, v);
 }
 
 __global__ __launch_bounds__(kBlock) void zero_kernel(char *a, char *b,
@@ -900,8 +972,7 @@ struct GluPlan : Tiles {
   int64_t blocks = 0;
   double us = 0;  // what the model below says
   size_t part_bytes() const {
-    return slices > 1 ? (size_t)slices * rem * tile() * tile() * sizeof(float)
-                      : 0;
+    return (size_t)slices * rem * tile() * tile() * sizeof(float);
   }
 };
 
@@ -909,7 +980,10 @@ struct GluPlan : Tiles {
 struct Shape {
   int64_t rows, cols, planes, steps;
   int col_share;  // columns of a tile, of its side: 1, or 2 for half of it
-  Shape(int form, int dtype, int64_t M, int64_t D, int64_t F) {
+  bool fold;      // all tiles go through the slices' sums, which add its rows
+  Shape(int form, int dtype, int64_t M, int64_t D, int64_t F,
+        bool fold = false)
+      : fold(fold) {
     const int S = dtype == ADALN_F32 ? kStep<float> : kStep<bf16>;
     const bool pair = form == kHidden || form == kGrads;
     rows = form == kDw ? F : M;
@@ -956,7 +1030,7 @@ GluPlan cut(const Shape &h, int tiling, int64_t tile, int64_t rem, int64_t s,
   g.tiles_r = (int32_t)r;
   g.tiles_c = (int32_t)c;
   g.steps = (int32_t)h.steps;
-  g.rem = (int32_t)(s > 1 ? rem : 0);
+  g.rem = (int32_t)(s > 1 || h.fold ? rem : 0);
   g.full = (int32_t)(n - g.rem);
   g.slices = (int32_t)s;
   g.per_slice = (int32_t)per;
@@ -970,14 +1044,15 @@ GluPlan cut(const Shape &h, int tiling, int64_t tile, int64_t rem, int64_t s,
 // ceil(rem * s / slots) / s of a round.  Measured on MI355X for the weights'
 // gradients of 24960 x 1536 x 4096 (192 big tiles, 4 slices) 654 -> 570 us,
 // dx (588, the last 76 in 3 slices) 717 -> 589 us.
-GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F) {
-  const Shape h(form, dtype, M, D, F);
+GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F,
+                 bool fold = false) {
+  const Shape h(form, dtype, M, D, F, fold);
   const bool pair = form == kHidden || form == kGrads;
   GluPlan best;
   for (int tiling = 0; tiling < 3; ++tiling) {
     const Costs k(tiling, dtype);
-    const int64_t n = cut(h, tiling, k.tile, 0, 1, h.steps).blocks;
-    const int64_t full = n / k.slots * k.slots, rem = n - full;
+    const int64_t n = cut(h, tiling, k.tile, 0, 1, h.steps).full;
+    const int64_t full = fold ? 0 : n / k.slots * k.slots, rem = n - full;
     for (int64_t s = 1; s <= 16; ++s) {
       if (s > 1 && (pair || rem == 0 || h.steps < 4 * s)) break;
       const int64_t per = (h.steps + s - 1) / s;
@@ -985,7 +1060,7 @@ GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F) {
       double us = full / k.slots * (h.steps * k.step + k.fill);
       if (rem > 0)
         us += (rem * s + k.slots - 1) / k.slots * (per * k.step + k.fill);
-      if (s > 1) us += k.adding(rem * s);
+      if (s > 1 || fold) us += k.adding(rem * s);
       if (best.blocks > 0 && us >= best.us) continue;
       best = cut(h, tiling, k.tile, rem, s, per);
       best.us = us;
@@ -996,14 +1071,25 @@ GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The backward's two products and its workspace: dG and dU, then the partial
-// sums.
+// The backward's two products and its workspace: dG and dU, what a split call
+// has besides, then the partial sums.
 struct GluBackward {
   GluPlan x, w;
   bool joint = false;
+  // dG, dU in two parts (split_grads_kernel).  Rounded to bf16 they add as
+  // much to the error of dx and dW as these' own rounding does, 1.41 times it
+  // together, and over few tokens, where it does not average out, up to 1.7.
+  // Up to 64 tokens both parts' rows fit into one row of tiles and the
+  // weights' bytes bound the products, so the parts cost little (MI355X, D =
+  // 1536, F = 4096: 1 token 22.1 -> 23.1 us, 16 22.6 -> 24.2, 64 23.4 -> 28.5;
+  // D = 5120, F = 13824: 1 token 161 -> 162, 64 165 -> 182; at most 2.5 us
+  // where dx alone was one slice).  Past that they would double the work.
+  bool split = false;
   size_t bytes = 0;
-  size_t x_part = 0, w_part = 0;  // offsets
+  size_t x2 = 0, gu = 0, h = 0;   // offsets: x twice; G, U computed again; h
+  size_t x_part = 0, w_part = 0;
 };
+constexpr int64_t kSplitTokens = 64;
 
 // When the last of n1 blocks of t1 and then n2 of t2 <= t1 ends, on `slots`
 // that each take the next block when they are free.
@@ -1041,16 +1127,19 @@ double makespan(int64_t slots, int64_t n1, double t1, int64_t n2, double t2) {
 // it is wrong it costs less: 3000 x 640 x 5000 142 -> 157.)
 GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
   GluBackward b;
-  b.x = glu_plan(kDx, dtype, M, D, F);
-  b.w = glu_plan(kDw, dtype, M, D, F);
-  const Shape hx(kDx, dtype, M, D, F), hw(kDw, dtype, M, D, F);
+  b.split = dtype == ADALN_BF16 && M <= kSplitTokens;
+  const int64_t rows = b.split ? 2 * M : M;
+  b.x = glu_plan(kDx, dtype, rows, D, F, b.split);
+  b.w = glu_plan(kDw, dtype, rows, D, F);
+  const Shape hx(kDx, dtype, rows, D, F, b.split);
+  const Shape hw(kDw, dtype, rows, D, F);
   double best = b.x.us + b.w.us + 3;
   for (int tiling : {(int)kSmall, (int)kBig, (int)kDeep}) {
     // (f32's small tiles are as fast as its big ones and end more evenly)
     if (tiling == kBig && dtype == ADALN_F32) continue;
     const Costs k(tiling, dtype);
-    const int64_t nx = cut(hx, tiling, k.tile, 0, 1, hx.steps).blocks;
-    const int64_t nw = cut(hw, tiling, k.tile, 0, 1, hw.steps).blocks;
+    const int64_t nx = cut(hx, tiling, k.tile, 0, 1, hx.steps).full;
+    const int64_t nw = cut(hw, tiling, k.tile, 0, 1, hw.steps).full;
     // (many tiles: the slices' sums would cost more than they even out)
     const int64_t most = nx + nw > 4 * k.slots ? 1 : 16;
     for (int64_t sx : {1, 2, 3, 4, 6, 8, 12, 16}) {
@@ -1069,8 +1158,9 @@ GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
           continue;
         double us = tw > tx ? makespan(k.slots, nw * sw, tw, nx * sx, tx)
                             : makespan(k.slots, nx * sx, tx, nw * sw, tw);
-        if (sx > 1 || sw > 1)
-          us += k.adding((sx > 1 ? nx * sx : 0) + (sw > 1 ? nw * sw : 0));
+        const bool add_x = sx > 1 || b.split;
+        if (add_x || sw > 1)
+          us += k.adding((add_x ? nx * sx : 0) + (sw > 1 ? nw * sw : 0));
         if (us >= best) continue;
         best = us;
         b.joint = true;
@@ -1079,8 +1169,10 @@ GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
       }
     }
   }
-  b.x_part = b.w_part =
-      align256((size_t)2 * M * F * (dtype == ADALN_F32 ? 4 : 2));
+  b.x2 = align256((size_t)2 * rows * F * (dtype == ADALN_F32 ? 4 : 2));
+  b.gu = b.x2 + (b.split ? align256((size_t)rows * D * 2) : 0);
+  b.h = b.gu + (b.split ? align256((size_t)2 * M * F * 4) : 0);
+  b.x_part = b.w_part = b.h + (b.split ? align256((size_t)M * F * 2) : 0);
   if (b.joint) b.w_part += align256(b.x.part_bytes());
   b.bytes = std::max(b.x_part + b.x.part_bytes(), b.w_part + b.w.part_bytes());
   return b;
@@ -1135,7 +1227,9 @@ hipError_t launch_tiles(const Product<T> &p, const GluPlan &g,
 // kHidden or kGrads.
 template <typename T, int FORM, int ACT>
 hipError_t launch_pair(const Product<T> &p, hipStream_t s) {
-  if (few_tokens(p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
+  // (few tokens' gradients in bf16 come from split_grads_kernel)
+  if constexpr (FORM == kHidden || kDtype<T> == ADALN_F32)
+    if (few_tokens(p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
   return launch_tiles<T, FORM, ACT>(
       p, glu_plan(FORM, kDtype<T>, p.M, p.D, p.F), s);
 }
@@ -1143,9 +1237,12 @@ hipError_t launch_pair(const Product<T> &p, hipStream_t s) {
 template <typename T>
 hipError_t launch_slices(const Product<T> &p, const Tiles &x, const Tiles &w,
                          hipStream_t s) {
-  const int64_t n = (int64_t)x.rem * x.tile() * x.tile() +
-                    (int64_t)w.rem * w.tile() * w.tile();
-  return launch_kernel(slices_kernel<T>, n / 8 / kBlock, s, p, x, w);
+  // (at most 4 * 512 tiles are cut in slices: below 2^17 workgroups)
+  auto blocks = [](const Tiles &q) {
+    return q.rem * (q.tile() * q.tile() / kSumElems);
+  };
+  return launch_kernel(slices_kernel<T>, (int64_t)blocks(x) + blocks(w), s, p,
+                       x, w, (int32_t)blocks(x));
 }
 
 template <typename T>
@@ -1244,6 +1341,29 @@ hipError_t launch_gate_grads(const Product<T> &p, hipStream_t s) {
                        p.dh, p.dgu, n);
 }
 
+// Of a split call: G, U computed again if they were not saved (the h that
+// comes with them is not used), then the parts.  The products are then those
+// of 2 M tokens.
+template <int ACT>
+hipError_t launch_split_grads(Product<bf16> &p, const GluBackward &b, char *ws,
+                              hipStream_t s) {
+  if (p.gu == nullptr) {
+    p.gu = (float *)(ws + b.gu);
+    p.h = (bf16 *)(ws + b.h);
+    const hipError_t e = launch_pair<bf16, kHidden, ACT>(p, s);
+    if (e != hipSuccess) return e;
+  }
+  bf16 *x2 = (bf16 *)(ws + b.x2);
+  const int64_t n = (int64_t)p.M * p.F, n_x = (int64_t)p.M * p.D;
+  const hipError_t e = launch_kernel(
+      split_grads_kernel<ACT>, ((n + n_x) / 8 + kBlock - 1) / kBlock, s,
+      (const float *)p.gu, p.dh, p.x, p.dgu, x2, n, n_x);
+  p.x = x2;
+  p.fold = p.M;
+  p.M *= 2;
+  return e;
+}
+
 template <typename T>
 hipError_t run_bwd(const void *dh, const void *x, const void *wg,
                    const void *wu, const float *saved, void *dx, void *dwg,
@@ -1256,9 +1376,16 @@ hipError_t run_bwd(const void *dh, const void *x, const void *wg,
   p.dx = (T *)dx;
   p.dw[0] = (T *)dwg;
   p.dw[1] = (T *)dwu;
-  const hipError_t e = act == ADALN_ACT_SILU
-                           ? launch_gate_grads<T, kSilu>(p, s)
-                           : launch_gate_grads<T, kGeluTanh>(p, s);
+  const bool silu = act == ADALN_ACT_SILU;
+  hipError_t e = hipSuccess;
+  if constexpr (kDtype<T> == ADALN_BF16) {
+    if (b.split)
+      e = silu ? launch_split_grads<kSilu>(p, b, (char *)workspace, s)
+               : launch_split_grads<kGeluTanh>(p, b, (char *)workspace, s);
+  }
+  if (!b.split)
+    e = silu ? launch_gate_grads<T, kSilu>(p, s)
+             : launch_gate_grads<T, kGeluTanh>(p, s);
   if (e != hipSuccess) return e;
   return launch_grads<T>(p, b, (char *)workspace, s);
 }

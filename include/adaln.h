@@ -407,7 +407,8 @@ size_t adaln_glu_bwd_workspace_bytes(int64_t M, int64_t D, int64_t F,
 
 /*
  * Its gradient:
- *     dU = dh * act(G), dG = dh * U * act'(G)     (rounded to dtype)
+ *     dU = dh * act(G), dG = dh * U * act'(G)     (rounded to dtype;
+ *         of at most 64 bf16 tokens to the sum of two bf16 each)
  *     dx = dG Wg + dU Wu    dWg = dG^T x    dWu = dU^T x
  *   dh       [M, F] dtype in;  x, wg, wu: the forward's inputs
  *   saved    the forward's [2, M, F], or NULL to compute G and U again (half

@@ -9,7 +9,8 @@ an output is rounded once (eps/2 = 2^-8 of the value); a float32 sum of K
 terms is within K * 2^-24 of the sum of their magnitudes; dG and dU are
 rounded to bfloat16 inside (at most 2^-8 of each, independent: 8 standard
 deviations of their sum are at most 8 * 2^-8 times the root of the sum of the
-squared terms)."""
+squared terms), or, up to 64 tokens, split into two bfloat16 (the second one
+rounds at most 2^-8 of each, within 2^-8 of itself)."""
 
 import pytest
 import torch
@@ -104,6 +105,21 @@ def _within(got, ref, tol, what):
 @pytest.mark.parametrize("size", [(1, 256, 520), (7, 1536, 1024),
                                   (130, 200, 392), (513, 768, 1096)])
 def test_real_numbers(size, act, dt):
+    _check_real(size, act, dt, split=False)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("size", [(1, 64, 64), (1, 256, 520), (2, 72, 2056),
+                                  (4, 1536, 1024), (5, 264, 8200),
+                                  (16, 512, 520), (17, 1000, 264),
+                                  (33, 136, 1032), (63, 328, 16),
+                                  (64, 768, 4104)])
+def test_gradients_of_few_tokens_are_rounded_once(size, act):
+    """Up to 64 tokens dG and dU have two parts: within 2^-16 of each."""
+    _check_real(size, act, torch.bfloat16, split=True)
+
+
+def _check_real(size, act, dt, split):
     M, D, F = size
     _say(f"real {size} {act} {dt}")
     dh, x, wg, wu = _real(M, D, F, M, dt)
@@ -134,6 +150,10 @@ def test_real_numbers(size, act, dt):
             t = e8 * ref.abs() + 1e-37
             for l, le, w in zip(L, Lerr, W):
                 t = t + le @ w.abs() + (K + 2) * e24 * (l.abs() @ w.abs())
+                if split:  # each part adds K terms
+                    t = t + (2.0 ** -16 + K * e24) * (l.abs() @ w.abs())
+            if split:
+                return t
             sq = sum((l ** 2) @ (w ** 2) for l, w in zip(L, W))
             return t + 8 * e8 * sq.sqrt()
 
