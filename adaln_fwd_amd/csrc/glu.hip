@@ -414,24 +414,31 @@ __device__ __forceinline__ void tile_of(int n, int tiles_r, int tiles_c,
   tc = in / rows;
 }
 
-// Three tilings.  kBig: 256 x 256 tiles by 8 wavefronts (2 x 4, each 128 x
+// Four tilings.  kBig: 256 x 256 tiles by 8 wavefronts (2 x 4, each 128 x
 // 64), two steps in LDS (128 KiB); kSmall: 128 x 128 by 4 (2 x 2, each 64 x
 // 64), two steps (64 KiB, so two workgroups to a CU); kDeep: the same with
 // four steps (128 KiB), for calls of so few tiles that a CU has one at most
-// and a step's arithmetic is far shorter than its loads take to arrive.
+// and a step's arithmetic is far shorter than its loads take to arrive; kFine:
+// 64 x 64 by 2, four steps (64 KiB), of pairs whose deep tiles would leave CUs
+// idle.
 // Columns of kHidden and kGrads: half of them of G, half the same ones of U,
 // so that a lane holds both of an element.
-enum { kSmall = 0, kBig = 1, kDeep = 2 };
+enum { kSmall = 0, kBig = 1, kDeep = 2, kFine = 3 };
 
 __host__ __device__ inline int Tiles::tile() const {
-  return tiling == kBig ? 256 : 128;
+  return tiling == kBig ? 256 : tiling == kFine ? 64 : 128;
 }
 
-constexpr int tiling_threads(int tiling) { return tiling == kBig ? 512 : 256; }
-constexpr int tiling_waves(int tiling) { return tiling == kDeep ? 1 : 2; }
+constexpr int tiling_threads(int tiling) {
+  return tiling == kBig ? 512 : tiling == kFine ? 128 : 256;
+}
+constexpr int tiling_waves(int tiling) {
+  return tiling == kDeep || tiling == kFine ? 1 : 2;
+}
 // LDS: two steps' operand tiles, or four.
 constexpr int tiling_lds(int tiling) {
-  return (tiling == kDeep ? 4 : 2) * 2 * (tiling == kBig ? 256 : 128) * 128;
+  return (tiling == kDeep || tiling == kFine ? 4 : 2) * 2 *
+         (tiling == kBig ? 256 : tiling == kFine ? 64 : 128) * 128;
 }
 
 // Block `id` of a product.
@@ -439,9 +446,10 @@ template <typename T, int FORM, int TILING, int ACT>
 __device__ __forceinline__ void product(const Product<T> &p, const Tiles &q,
                                         int id, char *lds) {
   constexpr bool BIG = TILING == kBig;
-  constexpr int kWaves = BIG ? 8 : 4;
-  constexpr int kTile = BIG ? 256 : 128;
-  constexpr int kBufs = TILING == kDeep ? 4 : 2;
+  constexpr bool FINE = TILING == kFine;
+  constexpr int kWaves = BIG ? 8 : FINE ? 2 : 4;
+  constexpr int kTile = BIG ? 256 : FINE ? 64 : 128;
+  constexpr int kBufs = TILING == kDeep || FINE ? 4 : 2;
   constexpr int kWn = kWaves / 2;          // wavefronts across the columns
   constexpr int MI = kTile / 2 / 32;        // 32-row blocks of a wavefront
   constexpr int NI = kTile / kWn / 32;      // 32-column blocks
@@ -999,19 +1007,21 @@ struct Shape {
 // of f32 a step has half the elements at a sixteenth of the rate): the big
 // ones run one to a CU, 1.65 per step and 5 for filling the pipeline and
 // storing; the small ones two to a CU, 1.0 and 4; the deep ones one to a CU,
-// 0.55 and 4 (MI355X, D = 1536, F = 4096, forward: 256 tokens 15.7 us deep
-// against 20.5 small, 1024 tokens 31.6 against 27.7).  Adding slices up takes
-// 4 and, per partial sum, 2 x 4 bytes at 5 TB/s.
+// 0.55 and 4; the fine ones two to a CU, 0.5 and 3 (MI355X, D = 1536, F =
+// 4096, forward, by fine, deep and small tiles: 128 tokens 12.3 us, 18.7, -;
+// 256 tokens 15.8, 18.1, 20.5; 1024 tokens -, 31.6, 27.7; f32, 128 tokens 61.2
+// and 99.9).  Adding slices up takes 4 and, per partial sum, 2 x 4 bytes at 5
+// TB/s.
 struct Costs {
   int64_t tile, slots;
   double step, fill;
   Costs(int tiling, int dtype) {
-    tile = tiling == kBig ? 256 : 128;
-    slots = tiling == kSmall ? 2 * kCUs : kCUs;
-    fill = tiling == kBig ? 5 : 4;
-    step = dtype == ADALN_F32
-               ? (tiling == kBig ? 9 : tiling == kSmall ? 4.5 : 2.3)
-               : (tiling == kBig ? 1.65 : tiling == kSmall ? 1.0 : 0.55);
+    tile = tiling == kBig ? 256 : tiling == kFine ? 64 : 128;
+    slots = tiling == kSmall || tiling == kFine ? 2 * kCUs : kCUs;
+    fill = tiling == kBig ? 5 : tiling == kFine ? 3 : 4;
+    constexpr double kF32[] = {4.5, 9, 2.3, 1.2};
+    constexpr double kBf16[] = {1.0, 1.65, 0.55, 0.5};
+    step = dtype == ADALN_F32 ? kF32[tiling] : kBf16[tiling];
   }
   double adding(int64_t blocks) const {
     return 4 + 8e-6 / 5 * blocks * tile * tile;
@@ -1049,7 +1059,7 @@ GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F,
   const Shape h(form, dtype, M, D, F, fold);
   const bool pair = form == kHidden || form == kGrads;
   GluPlan best;
-  for (int tiling = 0; tiling < 3; ++tiling) {
+  for (int tiling = 0; tiling <= (pair ? kFine : kDeep); ++tiling) {
     const Costs k(tiling, dtype);
     const int64_t n = cut(h, tiling, k.tile, 0, 1, h.steps).full;
     const int64_t full = fold ? 0 : n / k.slots * k.slots, rem = n - full;
@@ -1178,14 +1188,19 @@ GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
   return b;
 }
 
-// Few tokens: few_kernel.  Past 4 tokens only where the tiles of 64 hidden
-// features leave half the CUs idle (MI355X, D = 1536, F = 4096: 1 token 7.4
-// us, 32 tokens 10.5, 64 tokens 14.9, against 15.0 by tiles for all of
-// these).  Elsewhere the tiles stream the weights as fast and its repeated
-// reads of the tokens cost more (D = 5120, F = 13824: 1 token 61 us, 16
-// tokens 80, 64 tokens 137, against 63).
-bool few_tokens(int64_t M, int64_t F) {
-  return M <= 4 || (M <= 64 && (F + 63) / 64 < kCUs / 2);
+// Few tokens: few_kernel.  Past 4 tokens only where deep tiles, of 64 hidden
+// features, leave half the CUs idle.  Elsewhere the tiles stream the weights
+// as fast and its repeated reads of the tokens cost more (MI355X, D = 5120, F =
+// 13824: 1 token 61 us, 16 tokens 80, 64 tokens 137, against 43-52).  Past 48
+// tokens of bf16 the fine tiles are faster once they fill half the CUs (D =
+// 1536, F = 4096: 1 token 7.4 us, 32 tokens 10.6, 48 13.5, 64 15.3, against
+// 12.3 for 17-64; D = F = 2048: 64 tokens 13.7 against 14.8; f32, D = 1536, F =
+// 4096: 64 tokens 35 against 61).
+bool few_tokens(int dtype, int64_t M, int64_t F) {
+  const int64_t tiles = (F + 63) / 64;
+  if (M <= 4) return true;
+  return tiles < kCUs / 2 &&
+         M <= (dtype == ADALN_F32 || tiles < kCUs / 4 ? 64 : 48);
 }
 
 template <typename T>
@@ -1211,15 +1226,16 @@ hipError_t launch_tiles(const Product<T> &p, const GluPlan &g,
   for (int64_t at = 0; at < g.blocks && e == hipSuccess; at += kMaxGrid) {
     q.block0 = (int32_t)at;
     const int64_t n = std::min<int64_t>(kMaxGrid, g.blocks - at);
-    const int threads = tiling_threads(g.tiling);
-    e = g.tiling == kBig
-            ? launch_kernel_threads(product_kernel<T, FORM, kBig, ACT>, n,
-                                    threads, s, p, q)
-        : g.tiling == kSmall
-            ? launch_kernel_threads(product_kernel<T, FORM, kSmall, ACT>, n,
-                                    threads, s, p, q)
-            : launch_kernel_threads(product_kernel<T, FORM, kDeep, ACT>, n,
-                                    threads, s, p, q);
+    auto go = [&](auto kernel) {
+      return launch_kernel_threads(kernel, n, tiling_threads(g.tiling), s, p,
+                                   q);
+    };
+    if constexpr (FORM == kHidden || FORM == kGrads) {
+      if (g.tiling == kFine) e = go(product_kernel<T, FORM, kFine, ACT>);
+    }
+    if (g.tiling == kSmall) e = go(product_kernel<T, FORM, kSmall, ACT>);
+    if (g.tiling == kBig) e = go(product_kernel<T, FORM, kBig, ACT>);
+    if (g.tiling == kDeep) e = go(product_kernel<T, FORM, kDeep, ACT>);
   }
   return e;
 }
@@ -1229,7 +1245,7 @@ template <typename T, int FORM, int ACT>
 hipError_t launch_pair(const Product<T> &p, hipStream_t s) {
   // (few tokens' gradients in bf16 come from split_grads_kernel)
   if constexpr (FORM == kHidden || kDtype<T> == ADALN_F32)
-    if (few_tokens(p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
+    if (few_tokens(kDtype<T>, p.M, p.F)) return launch_few<T, FORM, ACT>(p, s);
   return launch_tiles<T, FORM, ACT>(
       p, glu_plan(FORM, kDtype<T>, p.M, p.D, p.F), s);
 }
