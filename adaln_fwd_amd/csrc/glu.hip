@@ -1001,6 +1001,10 @@ struct Shape {
             : form == kDx ? 2 * ((F + S - 1) / S) : (M + S - 1) / S;
     col_share = pair ? 2 : 1;
   }
+  int64_t tiles(int64_t tile) const {
+    const int64_t side = tile / col_share;
+    return (rows + tile - 1) / tile * ((cols + side - 1) / side) * planes;
+  }
 };
 
 // A plan's time, in microseconds, is modelled from what a tile takes (bf16;
@@ -1035,13 +1039,12 @@ GluPlan cut(const Shape &h, int tiling, int64_t tile, int64_t rem, int64_t s,
   const int64_t r = (h.rows + tile - 1) / tile;
   const int64_t side = tile / h.col_share;
   const int64_t c = (h.cols + side - 1) / side;
-  const int64_t n = r * c * h.planes;
   g.tiling = tiling;
   g.tiles_r = (int32_t)r;
   g.tiles_c = (int32_t)c;
   g.steps = (int32_t)h.steps;
   g.rem = (int32_t)(s > 1 || h.fold ? rem : 0);
-  g.full = (int32_t)(n - g.rem);
+  g.full = (int32_t)(h.tiles(tile) - g.rem);
   g.slices = (int32_t)s;
   g.per_slice = (int32_t)per;
   g.blocks = g.full + g.rem * s;
@@ -1061,7 +1064,8 @@ GluPlan glu_plan(int form, int dtype, int64_t M, int64_t D, int64_t F,
   GluPlan best;
   for (int tiling = 0; tiling <= (pair ? kFine : kDeep); ++tiling) {
     const Costs k(tiling, dtype);
-    const int64_t n = cut(h, tiling, k.tile, 0, 1, h.steps).full;
+    const int64_t n = h.tiles(k.tile);
+    if (n > INT32_MAX) continue;  // (the finest only)
     const int64_t full = fold ? 0 : n / k.slots * k.slots, rem = n - full;
     for (int64_t s = 1; s <= 16; ++s) {
       if (s > 1 && (pair || rem == 0 || h.steps < 4 * s)) break;
@@ -1148,8 +1152,7 @@ GluBackward glu_backward(int dtype, int64_t M, int64_t D, int64_t F) {
     // (f32's small tiles are as fast as its big ones and end more evenly)
     if (tiling == kBig && dtype == ADALN_F32) continue;
     const Costs k(tiling, dtype);
-    const int64_t nx = cut(hx, tiling, k.tile, 0, 1, hx.steps).full;
-    const int64_t nw = cut(hw, tiling, k.tile, 0, 1, hw.steps).full;
+    const int64_t nx = hx.tiles(k.tile), nw = hw.tiles(k.tile);
     // (many tiles: the slices' sums would cost more than they even out)
     const int64_t most = nx + nw > 4 * k.slots ? 1 : 16;
     for (int64_t sx : {1, 2, 3, 4, 6, 8, 12, 16}) {
