@@ -165,8 +165,8 @@ __device__ __forceinline__ void slot_vectors(const Job &job, int slot, int &a,
 
 // Rotates the lane's 2 * E values; cs: its E (cos, sin) entries.
 template <int E, bool HALF>
-__device__ __forceinline__ void rotate(float (&xa)[E], float (&xb)[E],
-                                       const float2 (&cs)[E]) {
+__device__ __forceinline__ void rotate_all(float (&xa)[E], float (&xb)[E],
+                                           const float2 (&cs)[E]) {
   if constexpr (HALF) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -185,6 +185,49 @@ __device__ __forceinline__ void rotate(float (&xa)[E], float (&xb)[E],
       xb[2 * i + 1] = u * cs[E / 2 + i].y + v * cs[E / 2 + i].x;
     }
   }
+}
+
+// How many pairs of the lane's vectors are rotated (half layout: those of
+// both vectors together), and whether any feature of the head is not.
+struct Part {
+  bool some;
+  int a, b;
+  template <int E, bool HALF>
+  __device__ __forceinline__ bool rotated(bool second, int i) const {
+    return HALF ? a > 0 : i / 2 < (second ? b : a);
+  }
+};
+
+// Rotates those of the values that are.  The others keep theirs: a rotation
+// by no angle is u * 1 - v * 0, which takes an infinite or undefined v, and
+// the sign of a zero, to u.
+template <int E, bool HALF>
+__device__ __forceinline__ void rotate(float (&xa)[E], float (&xb)[E],
+                                       const float2 (&cs)[E],
+                                       const Part &part) {
+  if (!part.some) {
+    rotate_all<E, HALF>(xa, xb, cs);
+    return;
+  }
+  float ra[E], rb[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) ra[i] = xa[i], rb[i] = xb[i];
+  rotate_all<E, HALF>(ra, rb, cs);
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if (part.rotated<E, HALF>(false, i)) xa[i] = ra[i];
+    if (part.rotated<E, HALF>(true, i)) xb[i] = rb[i];
+  }
+}
+
+// The vector y of a rotation of x with the bits of x where it is not rotated
+// (a conversion to float and back would make a signalling NaN a quiet one).
+template <int E, bool HALF>
+__device__ __forceinline__ void keep_bits(Vec &y, const Vec &x,
+                                          const Part &part, bool second) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!part.rotated<E, HALF>(second, i * (E / 4))) y.w[i] = x.w[i];
 }
 
 enum { kRope = 0, kNormFwd = 1, kNormBwd = 2 };
@@ -231,6 +274,11 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
   // entries of the lane's pairs in the table's row of a token
   const int ta = HALF ? slot * E : (ok_a ? va : 0) * (E / 2);
   const int tbl = HALF ? slot * E + E / 2 : (ok_b ? vb : 0) * (E / 2);
+
+  // half layout: slots of rotated pairs, and the others
+  const Part part = {2 * job.pairs < job.d,
+                     HALF ? slot < job.rot_vecs : job.pairs - ta,
+                     HALF ? 0 : job.pairs - tbl};
 
   // the workgroups of q, then those of k
   const int t = blockIdx.x >= job.grid_q;
@@ -279,7 +327,8 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
     }
     return r;
   };
-  // the sines of a block's tokens; pairs past the rotated ones turn by 0
+  // the sines of a block's tokens; the entries past the rotated pairs' are
+  // read, but not used
   auto sines = [&](const Block &k, float2 *table) {
     const int32_t *pos =
         job.pos + k.b * job.pos_batch + (int64_t)k.n0 * job.axes;
@@ -345,7 +394,7 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
             fa[i] = fa[i] * s * w[i];
             fb[i] = fb[i] * s * w[E + i];
           }
-          rotate<E, HALF>(fa, fb, cs);
+          rotate<E, HALF>(fa, fb, cs, part);
         } else {
           float ga[E], gb[E];
 #pragma unroll
@@ -353,7 +402,7 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
             ga[i] = elem<T>(r.ya, i);
             gb[i] = elem<T>(r.yb, i);
           }
-          rotate<E, HALF>(ga, gb, cs);
+          rotate<E, HALF>(ga, gb, cs, part);
           // t * x is what both sums need
           float pa[E], pb[E], sg = 0.f;
 #pragma unroll
@@ -381,11 +430,18 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
           }
         }
       } else {
-        rotate<E, HALF>(fa, fb, cs);
+        rotate_all<E, HALF>(fa, fb, cs);
       }
       char *dst = const_cast<char *>(out.data) + k.at(out, r.tok, r.head);
-      if (r.live && ok_a) store_stream(dst + va * 16, pack<T>(fa));
-      if (r.live && ok_b) store_stream(dst + vb * 16, pack<T>(fb));
+      Vec oa = pack<T>(fa), ob = pack<T>(fb);
+      if constexpr (OP == kRope) {
+        if (part.some) {
+          keep_bits<E, HALF>(oa, r.xa, part, false);
+          keep_bits<E, HALF>(ob, r.xb, part, true);
+        }
+      }
+      if (r.live && ok_a) store_stream(dst + va * 16, oa);
+      if (r.live && ok_b) store_stream(dst + vb * 16, ob);
     }
     k = after;
   }
