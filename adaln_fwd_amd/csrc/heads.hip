@@ -103,16 +103,22 @@ struct Job {
   int32_t pairs;
 };
 
-// cos and sin of a phase given as a 64-bit fraction of a turn.  The top 32
-// bits (rounded) are taken to the nearest quarter turn; what remains, at most
-// pi/4, goes through the Taylor polynomials of degree 9 and 10 (truncation
-// below 2e-9 and 2e-10), so both are within an ulp or so of float32 at any
-// position.
+// cos and sin of a phase given as a 64-bit fraction of a turn, which is taken
+// to the nearest quarter turn.  What remains, at most pi/4, is converted as a
+// signed whole number, so that small angles keep all their digits, and goes
+// through the Taylor polynomials of degree 9 and 10 (truncation below 2e-9 and
+// 2e-10): both results are within 4 * 2^-24 of themselves.  (Of the phase
+// itself the frequencies' last place is uncertain, half of 2^-64 turns per
+// unit position.  Once per pair and token of a block: the conversion from 64
+// bits costs nothing that can be measured.)
 __device__ __forceinline__ void cos_sin(uint64_t phase, float &c, float &s) {
-  const uint32_t p = (uint32_t)((phase + (uint64_t(1) << 31)) >> 32);
-  const uint32_t quarter = (p + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(p - (quarter << 30)) *
-                  (6.283185307179586f / 4294967296.0f);
+  const uint32_t quarter = (uint32_t)((phase + (uint64_t(1) << 61)) >> 62);
+  const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));
+  // 2 pi / 2^64, and what float32 leaves of it
+  constexpr double kTurn = 6.283185307179586 / 18446744073709551616.0;
+  constexpr float kHi = (float)kTurn, kLo = (float)(kTurn - (double)kHi);
+  const float f = (float)rest;
+  const float x = fmaf(f, kHi, f * kLo);
   const float x2 = x * x;
   float a = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);
   a = fmaf(x2, a, 8.3333333e-3f);

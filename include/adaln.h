@@ -315,7 +315,9 @@ typedef struct adaln_heads {
  * so an axis that does not move a pair has a zero there (time, height and
  * width with a run of pairs each: a block matrix).  Pair j is the features
  * (2j, 2j + 1) of the head, or (j, j + pairs); the features from 2 * pairs on
- * pass through.  The angle is reduced exactly for every 32-bit position.
+ * pass through.  Frequencies are taken to 2^-64 turns per unit position, and
+ * the angle is reduced exactly for every 32-bit position: cos and sin are
+ * within 4 * 2^-24 of themselves, those of small angles too.
  */
 #define ADALN_ROPE_INTERLEAVED 0 /* pairs (2j, 2j + 1) */
 #define ADALN_ROPE_HALF 1        /* pairs (j, j + pairs); pairs a multiple of
