@@ -231,30 +231,41 @@ struct Across {
 
 enum { kSilu = 0, kGeluTanh = 1 };
 
-// 4 / (1 + exp(-v)).  The hardware's reciprocal (one unit in the last place
-// of float32, before results are rounded to bfloat16; a correctly rounded
-// quotient takes ten instructions more per element) gives zero for quotients
-// below 2^-126: a quarter of 1 + exp(-v) has none.
-__device__ __forceinline__ float logistic4(float v) {
-  return __builtin_amdgcn_rcpf(fmaf(__expf(-v), 0.25f, 0.25f));
+// exp(-v).  float32 results keep its digits; for those rounded to bfloat16 (or
+// to two of them, 2^-16) the hardware's exp2 of a rounded product will do,
+// |v| * 2^-24 of itself.  (MI355X, f32 forward, the full exponential against
+// the other: 24960 x 1536 -> 4096 4465 us against 4434, 16380 x 64 -> 8192,
+// where little else is computed, 380 against 344.)
+template <typename T>
+__device__ __forceinline__ float exp_minus(float v) {
+  return sizeof(T) == 2 ? __expf(-v) : expf(-v);
 }
 
-// act(g) and act'(g).  Both are g times a logistic function s, of g or of
-// twice the tanh form's polynomial v: (1 + tanh(v)) / 2 = 1 / (1 + exp(-2v))
-// keeps its digits where 1 + tanh(v) cancels, and both ends saturate.
-template <int ACT>
+// act(g) and act'(g).  Both are g times a logistic function s = 1 / (1 + e),
+// e = exp(-v), of v = g or twice the tanh form's polynomial: (1 + tanh(w)) / 2
+// = 1 / (1 + exp(-2w)) keeps its digits where 1 + tanh(w) cancels.  act' needs
+// 1 - s too, which is e s: a difference would leave few digits of it where s is
+// near 1, and g times as much of the error.  So float32 derivatives are within
+// a few 2^-24 of themselves for positive g (a difference: up to 24 of them for
+// SiLU, 800 for GELU).  Both ends saturate: where e is infinite, s is 0 and 1 -
+// s is 1.
+// The hardware's reciprocal (one unit in the last place; a correctly rounded
+// quotient takes ten instructions more per element) gives zero for quotients
+// below 2^-126: a quarter of 1 + e has none.
+template <typename T, int ACT>
 __device__ __forceinline__ void activate(float g, float &a, float &da) {
-  if constexpr (ACT == kSilu) {
-    const float s4 = logistic4(g), s = 0.25f * s4;
-    a = 0.25f * g * s4;
-    da = s * (1.f + g * (1.f - s));
-  } else {
-    constexpr float c = 0.7978845608028654f, e = 0.044715f;
-    const float g2 = g * g;
-    const float s4 = logistic4(2.f * c * g * (1.f + e * g2)), s = 0.25f * s4;
-    a = 0.25f * g * s4;
-    da = s + 2.f * g * s * (1.f - s) * c * (1.f + 3.f * e * g2);
-  }
+  constexpr float c = 0.7978845608028654f, p = 0.044715f;
+  const float g2 = g * g;
+  const float e =
+      exp_minus<T>(ACT == kSilu ? g : 2.f * c * g * (1.f + p * g2));
+  const float s4 = __builtin_amdgcn_rcpf(fmaf(e, 0.25f, 0.25f));
+  const float s = 0.25f * s4;
+  const float rest = e < INFINITY ? 0.25f * e * s4 : 1.f;
+  a = 0.25f * g * s4;
+  if constexpr (ACT == kSilu)
+    da = s * (1.f + g * rest);
+  else
+    da = s + s * rest * g * (2.f * c * (1.f + 3.f * p * g2));
 }
 
 __device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
@@ -671,7 +682,7 @@ __device__ __forceinline__ void product(const Product<T> &p, const Tiles &q,
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float a, da;
-            activate<ACT>(g[e], a, da);
+            activate<T, ACT>(g[e], a, da);
             v0[e] = a * u[e];
           }
           store_block(stage, v0, p.h + at, cols, n_r, n_c);
@@ -689,7 +700,7 @@ __device__ __forceinline__ void product(const Product<T> &p, const Tiles &q,
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float a, da;
-              activate<ACT>(g[4 * q + e], a, da);
+              activate<T, ACT>(g[4 * q + e], a, da);
               v0[4 * q + e] = dh[e] * u[4 * q + e] * da;
               v1[4 * q + e] = dh[e] * a;
             }
@@ -750,7 +761,7 @@ __device__ __forceinline__ void gate_grads(const float *gu, const T *dh,
     const float u = elem<float>(e < 4 ? u0 : u1, e % 4);
     const float t = elem<T>(d[e / Elems<T>::value], e % Elems<T>::value);
     float a, da;
-    activate<ACT>(g, a, da);
+    activate<T, ACT>(g, a, da);
     dg[e] = t * u * da;
     du[e] = t * a;
   }
@@ -896,7 +907,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(Product<T> p) {
     const int64_t at = (int64_t)m * F + f0 + ff;
     const int64_t plane_size = (int64_t)M * F;
     float a, da;
-    activate<ACT>(gu[0], a, da);
+    activate<T, ACT>(gu[0], a, da);
     if constexpr (FORM == kHidden) {
       store_one(p.h + at, a * gu[1]);
       if (p.gu != nullptr) {
