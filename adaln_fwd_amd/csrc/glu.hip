@@ -248,14 +248,15 @@ __device__ __forceinline__ float exp_minus(float v) {
 // near 1, and g times as much of the error.  So float32 derivatives are within
 // a few 2^-24 of themselves for positive g (a difference: up to 24 of them for
 // SiLU, 800 for GELU).  Both ends saturate: where e is infinite, s is 0 and 1 -
-// s is 1.
+// s is 1; g^2, which passes float32 at |g| = 1.8e19, stops at 1e30, where s or
+// 1 - s is 0 long since and must not meet an infinity.
 // The hardware's reciprocal (one unit in the last place; a correctly rounded
 // quotient takes ten instructions more per element) gives zero for quotients
 // below 2^-126: a quarter of 1 + e has none.
 template <typename T, int ACT>
 __device__ __forceinline__ void activate(float g, float &a, float &da) {
   constexpr float c = 0.7978845608028654f, p = 0.044715f;
-  const float g2 = g * g;
+  const float g2 = fminf(g * g, 1e30f);
   const float e =
       exp_minus<T>(ACT == kSilu ? g : 2.f * c * g * (1.f + p * g2));
   const float s4 = __builtin_amdgcn_rcpf(fmaf(e, 0.25f, 0.25f));

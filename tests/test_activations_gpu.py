@@ -82,3 +82,26 @@ def test_activations_of_float32(act, M):
         bad = ~(err <= tol)
         assert not bad.any(), (n, int(bad.sum()), float(g[(err / tol).argmax()]),
                                float((err / tol).max()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_derivatives_of_the_largest_numbers(act, dtype):
+    """act' is 1 or 0 there, where g^2 and exp(-g) are infinite."""
+    _say(f"largest numbers {act} {dtype}")
+    g = torch.tensor([1e4, 1e12, 1e18, 2e19, 1e30, 3e38])
+    g = torch.cat([g, -g]).to(dtype)
+    for M in (12, 240):
+        x = torch.zeros(M, 8, dtype=dtype)
+        x[:, 0] = g.repeat(M // 12)
+        x[:, 1] = 1
+        wg, wu, dh = torch.zeros(8, 8), torch.zeros(8, 8), torch.zeros(M, 8)
+        wg[0, 0], wu[0, 1], dh[:, 0] = 1, 1, 1
+        x, wg, wu, dh = [t.to(dtype).cuda() for t in (x, wg, wu, dh)]
+        h, saved = A.glu_fwd(x, wg, wu, act=act, save=True)
+        want = x[:, 0].clamp_min(0)
+        assert torch.equal(h[:, 0], want)
+        for s in (saved, None):
+            dx = A.glu_bwd(dh, x, wg, wu, s, act=act)[0]
+            assert torch.equal(dx[:, 0], (want > 0).to(dtype))
+            assert torch.equal(dx[:, 1], want)
