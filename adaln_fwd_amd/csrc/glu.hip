@@ -53,8 +53,8 @@ constexpr int kStep = 128 / sizeof(T);
 // 16 bytes per lane from memory to LDS at `lds` + 16 * lane: a wave-uniform
 // base and a 32-bit offset per lane.  Outstanding loads are waited for by
 // arrive() below, by hand: the compiler does not see these loads.  (m0 takes
-// the LDS address; nothing else in these kernels uses it.  The s_nop is the
-// wait state that the ISA asks for between writing m0 and a load to LDS.)
+// the LDS address.  The s_nop is the wait state that the ISA asks for between
+// writing m0 and a load to LDS.)
 __device__ __forceinline__ void dma(uint32_t lds, const void *base,
                                     uint32_t offset) {
   asm volatile(
@@ -63,7 +63,7 @@ __device__ __forceinline__ void dma(uint32_t lds, const void *base,
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(offset), "s"(base)
-      : "memory");
+      : "memory", "m0");
 }
 
 // All loads of this wavefront but the last LATER have landed, then those of
