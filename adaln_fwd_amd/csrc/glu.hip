@@ -324,6 +324,14 @@ __device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
 
 // ------------------------------------------------------- storing a block
 
+// What lanes of a wavefront wrote to LDS before it, the others read after it.
+// The hardware keeps a wavefront's accesses to LDS in order; this keeps the
+// compiler from moving them.
+__device__ __forceinline__ void lanes_agree() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // A 32 x 32 block as the matrix cores leave it (lane l: row l % 32, columns
 // 8 q + 4 (l / 32) + e in register 4 q + e) to memory, in row order: through
 // LDS of the wavefront's own, so that 8 lanes write a whole 128-byte line
@@ -343,12 +351,14 @@ __device__ __forceinline__ void store_block(char *stage, const f32x16 &v,
     *reinterpret_cast<f32x4 *>(stage + (lane % 32) * 144 +
                                (8 * q + 4 * (lane / 32)) * 4) = f;
   }
+  lanes_agree();
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int r = t * 8 + lane / 8, c = lane % 8 * 4;
     const Vec f = load_vec(stage + r * 144 + c * 4);
     if (r < n_r && c < n_c) store_stream(out + r * pitch + c, f);
   }
+  lanes_agree();
 }
 
 __device__ __forceinline__ void store_block(char *stage, const f32x16 &v,
@@ -361,12 +371,14 @@ __device__ __forceinline__ void store_block(char *stage, const f32x16 &v,
     *reinterpret_cast<uint2 *>(stage + (lane % 32) * 80 +
                                (8 * q + 4 * (lane / 32)) * 2) = pack4(f);
   }
+  lanes_agree();
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int r = t * 16 + lane / 4, c = lane % 4 * 8;
     const Vec f = load_vec(stage + r * 80 + c * 2);
     if (r < n_r && c < n_c) store_vec(out + r * pitch + c, f);
   }
+  lanes_agree();
 }
 
 // ------------------------------------------------------------- the products
