@@ -206,12 +206,15 @@ struct Part {
 
 // Rotates those of the values that are.  The others keep theirs: a rotation
 // by no angle is u * 1 - v * 0, which takes an infinite or undefined v, and
-// the sign of a zero, to u.
-template <int E, bool HALF>
+// the sign of a zero, to u.  BRANCH: whole heads rotated go past the selection;
+// it pays in the norm's backward, which issues more than it loads (MI355X,
+// 75600 x 80 heads of 128 bf16, 801 us against 820), and not in its forward
+// (3554 x 15 heads of 72 f32, 64 of them rotated, 9.9 us against 9.1).
+template <int E, bool HALF, bool BRANCH>
 __device__ __forceinline__ void rotate(float (&xa)[E], float (&xb)[E],
                                        const float2 (&cs)[E],
                                        const Part &part) {
-  if (!part.some) {
+  if (BRANCH && !part.some) {
     rotate_all<E, HALF>(xa, xb, cs);
     return;
   }
@@ -400,7 +403,7 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
             fa[i] = fa[i] * s * w[i];
             fb[i] = fb[i] * s * w[E + i];
           }
-          rotate<E, HALF>(fa, fb, cs, part);
+          rotate<E, HALF, false>(fa, fb, cs, part);
         } else {
           float ga[E], gb[E];
 #pragma unroll
@@ -408,7 +411,7 @@ __global__ __launch_bounds__(kBlock) void heads_kernel(Job job, ROT rot) {
             ga[i] = elem<T>(r.ya, i);
             gb[i] = elem<T>(r.yb, i);
           }
-          rotate<E, HALF>(ga, gb, cs, part);
+          rotate<E, HALF, true>(ga, gb, cs, part);
           // t * x is what both sums need
           float pa[E], pb[E], sg = 0.f;
 #pragma unroll
@@ -644,14 +647,14 @@ struct HeadsPlan {
 // A block has up to kBlockRows rows for each lane group of a workgroup, and
 // fewer where the GPU would not be filled: short blocks keep the window of
 // memory that is read and written at a time small.  Measured on MI355X (bf16,
-// 128 features): 32760 tokens x 24 heads rotated, 16 tokens per block 74.6
-// us, 8 (96 rows of 32 lane groups) 69.0; norm and rotation of 75600 x 80
-// heads, 16 tokens 583 us, 4 (160 rows) 536, 2 (80 rows) 534.
+// 128 features): 32760 tokens x 24 heads rotated, 16 tokens per block 78.4
+// us, 8 (96 rows of 32 lane groups) 72.2; norm and rotation of 75600 x 80
+// heads, 16 tokens 590 us, 4 (160 rows) 546, 2 (80 rows) 508.
 // The backward of the norm runs a persistent grid, so that each workgroup
 // adds up dw over many blocks before it writes its partial row: 6 per CU,
-// twice what its registers admit at a time, evens out the end (75600 x 80
-// heads: 3 per CU 817 us, 6 per CU 807).  q and k share it by their numbers
-// of heads.
+// twice what its registers admit at a time in bf16, evens out the end (75600 x
+// 80 heads: 3 per CU 815 us, 6 per CU 800; f32, 24960 x 24 heads, where a CU
+// holds 4: 160 and 170).  q and k share it by their numbers of heads.
 HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
                      int dtype, bool bwd) {
   HeadsPlan p = {};
@@ -687,14 +690,17 @@ HeadsPlan heads_plan(int64_t B, int64_t N, int64_t Hq, int64_t Hk, int64_t d,
 
 // Inputs that another kernel has just written or read may still lie in the
 // 256 MB Infinity Cache; the streaming hint reads past it.  Up to twice its
-// size of bytes read and written plain loads win or lose little, past it the
-// hint is the better one.  MI355X, bf16, 24 heads of 128, three sets of inputs
-// and outputs in turn, plain loads against the hint: rotation of 10000 tokens
-// (122 MB) 21.8 against 25.4 us, 32760 (402 MB) 73.6 against 71.8, 90000 (1.1
-// GB) 196 against 187; backward of the norm of 24960 tokens (460 MB) right
-// behind its forward 80 against 86; of 75600 tokens x 80 heads (4.6 GB) 837
-// against 806.  (Plain stores of the outputs were slower from 100 MB on, but
-// for outputs written over again while the cache still held them.)
+// size of bytes read and written a call takes plain loads, past it the hint.
+// MI355X, bf16, heads of 128, three sets of inputs and outputs in turn, plain
+// loads against the hint: rotation of 10000 x 24 (122 MB) 20.7 against 25.2 us,
+// 24960 x 24 (307 MB) 56.4 and 55.2, 32760 x 24 (402 MB) 72.2 and 71.1, 90000 x
+// 24 (1.1 GB) 192 and 184.  Alone the hint would win from 300 MB on, by 2%; but
+// the backward of the norm of 24960 x 24 heads (460 MB) comes right behind its
+// forward, and the two take 139 us with plain loads, 143 with the hint (by
+// itself 92 and 89; 75600 x 80 heads, 4.6 GB, 856 and 812).  One bound for all
+// of them costs the rotations those 2%.  (Plain stores of the outputs were
+// slower from 100 MB on, but for outputs written over again while the cache
+// still held them.)
 constexpr int64_t kCachedBytes = int64_t(512) << 20;
 
 void fill_job(Job &job, const HeadsPlan &p, const adaln_rotation_t *rot,
