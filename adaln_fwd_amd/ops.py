@@ -26,6 +26,16 @@ _DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
 _HERE = contextlib.nullcontext()
 
 
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of a device's current stream.  torch.cuda.current_stream() makes a
+# Stream object for it, 1.8 us of a call of some 12, so the handle alone is
+# asked for where this torch has that (it is not part of its public interface).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _code(t: torch.Tensor) -> int:
     try:
         return _DTYPES[t.dtype]
@@ -60,9 +70,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device: torch.device, stream) -> int:
     if stream is None:
-        # the handle alone: torch.cuda.current_stream() makes a Stream object
-        # for it, 1.8 us of a call of some 12
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _current(device.index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
