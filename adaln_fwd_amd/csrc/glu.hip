@@ -338,7 +338,8 @@ __device__ __forceinline__ void lanes_agree() {
 // (float32) or 4 lanes half of one (bf16) at a time instead of 32 lanes 32
 // pieces of lines.  The rows' pitch keeps both sides free of bank conflicts.
 // n_r, n_c: rows and columns of the block that exist.  Forward of 24960 x
-// 1536 -> 4096 with G and U saved, on MI355X: 952 -> 673 us.
+// 1536 -> 4096 with G and U saved, on MI355X: 952 -> 673 us (with later steps
+// 605-650).
 constexpr int kStageBytes = 32 * (32 * 4 + 16);
 
 __device__ __forceinline__ void store_block(char *stage, const f32x16 &v,
@@ -780,7 +781,10 @@ __device__ __forceinline__ void gate_grads(const float *gu, const T *dh,
   }
 }
 
-// dG, dU from the saved G, U: one pass, 8 elements per thread.
+// dG, dU from the saved G, U: one pass, 8 elements per thread.  In bf16 they
+// are rounded to it, as kGrads rounds them: the matrix cores' operands of dx
+// and dW.  Kept in two parts, as for few tokens (GluBackward::split), they
+// would double those products, for 1.41 times less error of dx and dW.
 template <typename T, int ACT>
 __global__ __launch_bounds__(kBlock) void gate_grads_kernel(
     const float *__restrict__ gu, const T *__restrict__ dh,

@@ -1,6 +1,7 @@
 """Binding of the gated feed-forward (adaln_glu_*) for torch tensors: token
 rows [M, D] or [B, N, D], weights [F, D] as a linear layer keeps them.
-Checks, streams and allocation are those of :mod:`adaln_fwd_amd.ops`."""
+Checks, streams and allocation are those of :mod:`adaln_fwd_amd.ops`; outputs
+and the workspace must not overlap inputs or each other."""
 
 from __future__ import annotations
 
