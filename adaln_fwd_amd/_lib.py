@@ -42,6 +42,7 @@ class Rotation(ctypes.Structure):
 # Every function the header declares, with its ctypes signature.
 _VP, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _HP, _RP, _F = ctypes.POINTER(Heads), ctypes.POINTER(Rotation), ctypes.c_float
+_D = ctypes.c_double
 SIGNATURES = {
     "adaln_fwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT,
                          _VP]),
@@ -85,6 +86,29 @@ SIGNATURES = {
     "adaln_glu_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
     "adaln_glu_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
                              _I64, _I64, _I64, _INT, _INT, _VP]),
+    "adaln_residual_fwd": (_INT, [_VP, _VP, _VP, _D, _VP, _VP, _I64, _I64,
+                                  _I64, _INT, _VP]),
+    "adaln_residual_bwd_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
+    "adaln_residual_bwd": (_INT, [_VP, _VP, _VP, _D, _VP, _VP, _VP, _VP, _SZ,
+                                  _I64, _I64, _I64, _INT, _VP]),
+    "adaln_residual_fwd_segments": (_INT, [_VP, _VP, _VP, _D, _VP, _VP, _VP,
+                                           _VP, _I64, _I64, _I64, _INT, _VP]),
+    "adaln_residual_bwd_segments_workspace_bytes": (_SZ, [_VP, _I64, _I64,
+                                                          _INT]),
+    "adaln_residual_bwd_segments": (_INT, [_VP, _VP, _VP, _D, _VP, _VP, _VP,
+                                           _VP, _SZ, _VP, _VP, _I64, _I64,
+                                           _I64, _INT, _VP]),
+    "adaln_experts_plan_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "adaln_experts_plan": (_INT, [_VP, _INT, _VP, _VP, _VP, _SZ, _I64, _I64,
+                                  _I64, _VP]),
+    "adaln_experts_sort_fwd": (_INT, [_VP, _VP, _VP, _I64, _I64, _I64, _INT,
+                                      _VP]),
+    "adaln_experts_sort_bwd": (_INT, [_VP, _VP, _VP, _I64, _I64, _I64, _INT,
+                                      _VP]),
+    "adaln_experts_join_fwd": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64,
+                                      _INT, _VP]),
+    "adaln_experts_join_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _I64,
+                                      _I64, _I64, _INT, _VP]),
     "adaln_bshape": (_I64, [_I64, _I64, _I64, ctypes.c_int32]),
     "adaln_bshape_real": (_I64, [_I64, _I64, ctypes.c_double,
                                  ctypes.c_double]),

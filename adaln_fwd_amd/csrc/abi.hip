@@ -9,9 +9,8 @@
 #include <stdint.h>
 
 #include "adaln.h"
+#include "checks.hpp"
 #include "launch.hpp"
-
-#define ADALN_API extern "C" __attribute__((visibility("default")))
 
 namespace adaln {
 namespace {
@@ -41,6 +40,8 @@ int elems_per_vec(int dtype) { return dtype == ADALN_BF16 ? 8 : 4; }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxB = int64_t(1) << 20;
+
+}  // namespace
 
 // Checks shared by every operator entry point.
 int check_shape(int64_t B, int64_t N, int64_t D, int dtype) {
@@ -79,11 +80,7 @@ int check_ptr(const void *p, bool needed, const char *name) {
   return ADALN_OK;
 }
 
-#define ADALN_TRY(expr)          \
-  do {                           \
-    const int rc_ = (expr);      \
-    if (rc_ != ADALN_OK) return rc_; \
-  } while (0)
+namespace {
 
 size_t partial_bytes(int64_t n_tiles, int64_t B, int64_t D) {
   return (size_t)2 * (size_t)B * (size_t)n_tiles * (size_t)D * sizeof(float);
@@ -632,10 +629,8 @@ ADALN_API int adaln_bwd(const void *dy, const void *x, const void *scale,
 
 // ------------------------------------------------------ packed segments
 
-namespace {
-
 // Validates the segment table (host arrays) and the shape.
-int check_segments(const int64_t *off, const int32_t *mod, int64_t nseg,
+int adaln::check_segments(const int64_t *off, const int32_t *mod, int64_t nseg,
                    int64_t nmod, int64_t D, int dtype) {
   ADALN_TRY(check_shape(1, 0, D, dtype));
   if (nseg < 0 || nseg > kMaxSegments)
@@ -661,8 +656,6 @@ int check_segments(const int64_t *off, const int32_t *mod, int64_t nseg,
   if (nmod > kMaxRows / D) return fail(ADALN_ERR_INVALID, "nmod*D too large");
   return ADALN_OK;
 }
-
-}  // namespace
 
 ADALN_API size_t adaln_bwd_segments_workspace_bytes(const int64_t *seg_offsets,
                                                     int64_t nseg, int64_t D,

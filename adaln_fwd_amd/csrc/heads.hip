@@ -19,16 +19,9 @@
 #include <math.h>
 
 #include "adaln.h"
+#include "checks.hpp"
 #include "common.hpp"
 #include "launch.hpp"
-
-#define ADALN_API extern "C" __attribute__((visibility("default")))
-
-#define ADALN_TRY(expr)          \
-  do {                           \
-    const int rc_ = (expr);      \
-    if (rc_ != ADALN_OK) return rc_; \
-  } while (0)
 
 namespace adaln {
 namespace {
@@ -575,6 +568,8 @@ int check_rotation(const adaln_rotation_t *rot, int64_t d, int dtype,
   return ADALN_OK;
 }
 
+}  // namespace
+
 // One tensor: pointer, alignment, strides; an output's rows must not overlap.
 int check_heads(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
                 int64_t d, int dtype, bool output, const char *name) {
@@ -611,6 +606,8 @@ int check_heads(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
   }
   return ADALN_OK;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- launching
 

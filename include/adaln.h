@@ -426,6 +426,127 @@ int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
                   void *stream);
 
 /*
+ * The join of a branch with the residual stream: the gate that a block's
+ * conditioning gives beside scale and shift, and dropout whose mask is never
+ * stored.
+ *     y = x + gate[b] * drop(h)     drop(h) = h * s where kept, else 0
+ *   x      [B,N,D] dtype in, or NULL: nothing is added (dropout by itself)
+ *   h      [B,N,D] dtype in   the branch's output
+ *   gate   [B,D]   dtype in, or NULL: no gate
+ *   p      the rate of dropping, 0 to 1 - 2^-16, taken to a multiple of 2^-16
+ *          (s = 65536 / T, T = floor((1 - p) * 65536 + 1/2), is exact for that)
+ *   rng    device int64 [2]: the seed, and the number of the call, which the
+ *          caller raises from call to call (a captured graph can do so
+ *          itself); read by the kernels only, and not at all if p is 0
+ *   y      [B,N,D] dtype out; may be x or h
+ * An element that is dropped leaves x as it is, whatever h and gate hold.
+ * Feature d of token row r = b*N + n is kept if its 16 bits are below T: those
+ * of halfword d % 8 (word d % 8 / 2, low half first) of the Philox 4x32-10
+ * block with the counter (r * ceil(D / 8) + d / 8, rng[1]) and the key rng[0],
+ * low words first.  So the mask depends on sizes, seed and number alone, not
+ * on the type or the machine.
+ */
+int adaln_residual_fwd(const void *x, const void *h, const void *gate,
+                       double p, const int64_t *rng, void *y, int64_t B,
+                       int64_t N, int64_t D, int dtype, void *stream);
+
+/* Bytes of device workspace of adaln_residual_bwd with a gate (partial sums of
+ * dgate).  A pure function of its arguments; 0 for invalid ones and for so few
+ * tokens that none is needed (NULL will do then, as without a gate). */
+size_t adaln_residual_bwd_workspace_bytes(int64_t B, int64_t N, int64_t D,
+                                          int dtype);
+
+/*
+ * Its gradient (that of x is dy itself):
+ *     dh = dy * gate[b] * s where kept, else 0    dgate[b] = sum_n dy * drop(h)
+ *   dy, h, gate  as above; p and rng those of the forward.  Without a gate h
+ *                is not read and dgate is NULL.
+ *   dh           [B,N,D] dtype out; may be dy or h
+ *   dgate        [B,D] f32 out (overwritten; zero if there are no tokens)
+ * Results are bitwise reproducible.
+ */
+int adaln_residual_bwd(const void *dy, const void *h, const void *gate,
+                       double p, const int64_t *rng, void *dh, float *dgate,
+                       void *workspace, size_t workspace_bytes, int64_t B,
+                       int64_t N, int64_t D, int dtype, void *stream);
+
+/*
+ * The same for packed sequences: x, h, y, dy, dh [T, D], gate [nmod, D], dgate
+ * [nmod, D] f32, segments and their vectors as in adaln_fwd_segments; r is the
+ * packed row.  A gate is needed.
+ */
+int adaln_residual_fwd_segments(const void *x, const void *h, const void *gate,
+                                double p, const int64_t *rng, void *y,
+                                const int64_t *seg_offsets,
+                                const int32_t *seg_mod, int64_t nseg,
+                                int64_t nmod, int64_t D, int dtype,
+                                void *stream);
+
+size_t adaln_residual_bwd_segments_workspace_bytes(const int64_t *seg_offsets,
+                                                   int64_t nseg, int64_t D,
+                                                   int dtype);
+
+int adaln_residual_bwd_segments(const void *dy, const void *h,
+                                const void *gate, double p, const int64_t *rng,
+                                void *dh, float *dgate, void *workspace,
+                                size_t workspace_bytes,
+                                const int64_t *seg_offsets,
+                                const int32_t *seg_mod, int64_t nseg,
+                                int64_t nmod, int64_t D, int dtype,
+                                void *stream);
+
+/*
+ * Tokens to the experts of a mixture and back.  Each of T tokens has k choices
+ * of an expert; adaln_experts_plan sorts the choices by expert, those of one
+ * expert by token and then by choice.
+ *   expert   [T,k] int32 (wide = 0) or int64 (wide = 1) in; a choice of an
+ *            expert outside [0, E) is dropped
+ *   offsets  [E+1] int32 out: expert e has the sorted rows offsets[e] up to
+ *            offsets[e+1]; the rows from offsets[E] on are nobody's
+ *   slot     [T,k] int32 out: each choice's sorted row, -1 for a dropped one
+ *   workspace  adaln_experts_plan_workspace_bytes bytes (0 for so few choices
+ *            that none is needed, and for invalid arguments)
+ * k is 1 to 64, E 1 to 512, T*k < 2^31.
+ */
+size_t adaln_experts_plan_workspace_bytes(int64_t T, int64_t k, int64_t E);
+
+int adaln_experts_plan(const void *expert, int wide, int32_t *offsets,
+                       int32_t *slot, void *workspace, size_t workspace_bytes,
+                       int64_t T, int64_t k, int64_t E, void *stream);
+
+/*
+ * The token rows in sorted order, xs[slot[t,j]] = x[t], and the gradient,
+ * dx[t] = sum_j dxs[slot[t,j]].
+ *   x, dx    [T,D] dtype;  xs, dxs [T*k,D] dtype
+ * Sorted rows that no choice has are neither read nor written.  A slot outside
+ * [0, T*k) counts as dropped.  Sums are float32, in the order of the choices.
+ */
+int adaln_experts_sort_fwd(const void *x, const int32_t *slot, void *xs,
+                           int64_t T, int64_t k, int64_t D, int dtype,
+                           void *stream);
+
+int adaln_experts_sort_bwd(const void *dxs, const int32_t *slot, void *dx,
+                           int64_t T, int64_t k, int64_t D, int dtype,
+                           void *stream);
+
+/*
+ * The experts' outputs back at their tokens, weighted, and the gradients:
+ *     y[t] = sum_j w[t,j] ys[slot[t,j]]
+ *     dys[slot[t,j]] = w[t,j] dy[t]      dw[t,j] = dy[t] . ys[slot[t,j]]
+ *   w, dw    [T,k] f32 (dw of a dropped choice is zero)
+ *   y, dy    [T,D] dtype (y of a token without choices is zero)
+ *   ys, dys  [T*k,D] dtype; rows that no choice has are neither read nor
+ *            written.  dys may be ys.
+ */
+int adaln_experts_join_fwd(const void *ys, const int32_t *slot, const float *w,
+                           void *y, int64_t T, int64_t k, int64_t D, int dtype,
+                           void *stream);
+
+int adaln_experts_join_bwd(const void *dy, const void *ys, const int32_t *slot,
+                           const float *w, void *dys, float *dw, int64_t T,
+                           int64_t k, int64_t D, int dtype, void *stream);
+
+/*
  * Dual-constraint bucket batch size of section 2.A:
  *     max(1, min(floor(m_mem / S), floor(m_comp / S^p)))
  * in exact integer arithmetic.  When S^p exceeds the int64 range the compute
