@@ -109,6 +109,18 @@ SIGNATURES = {
                                       _INT, _VP]),
     "adaln_experts_join_bwd": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _I64,
                                       _I64, _I64, _INT, _VP]),
+    "adaln_lin_attn_states_bytes": (_SZ, [_VP, _I64, _I64, _I64, _I64, _I64,
+                                          _INT]),
+    "adaln_lin_attn_fwd": (_INT, [_HP, _HP, _HP, _VP, _F, _VP, _HP, _VP, _VP,
+                                  _SZ, _VP, _I64, _I64, _I64, _I64, _I64,
+                                  _INT, _VP]),
+    "adaln_lin_attn_bwd_workspace_bytes": (_SZ, [_INT, _VP, _I64, _I64, _I64,
+                                                 _I64, _I64, _INT]),
+    "adaln_lin_attn_bwd": (_INT, [_HP, _HP, _HP, _HP, _VP, _F, _VP, _VP, _VP,
+                                  _HP, _HP, _HP, _VP, _VP, _SZ, _VP, _I64,
+                                  _I64, _I64, _I64, _I64, _INT, _VP]),
+    "adaln_lin_attn_step": (_INT, [_HP, _HP, _HP, _VP, _F, _VP, _HP, _VP,
+                                   _I64, _I64, _I64, _INT, _VP]),
     "adaln_bshape": (_I64, [_I64, _I64, _I64, ctypes.c_int32]),
     "adaln_bshape_real": (_I64, [_I64, _I64, ctypes.c_double,
                                  ctypes.c_double]),

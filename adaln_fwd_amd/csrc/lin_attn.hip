@@ -1,0 +1,1092 @@
+// Linear attention with a decay for each head, forward, backward and one token
+// at a time, with their C entry points.
+//
+//     S_t = l S_{t-1} + k_t v_t^T      o_t = c S_t^T q_t      l = exp(log_decay)
+//
+// In chunks of 32 tokens, t and s counted from the chunk's first, S the state
+// before it and n its tokens:
+//
+//     o_t = c l^(t+1) S^T q_t + sum_{s <= t} c l^(t-s) (q_t . k_s) v_s
+//     S'  = l^n S + sum_s k_s (l^(n-1-s) v_s)^T
+//
+// The powers of l are never negative ones, so no decay, however strong,
+// overflows.  The gradients are the same operator with its parts exchanged,
+// dq = lin(do, v, k) with S^T, and, from the last token to the first, with G
+// the gradient of the state:
+//
+//     dv = lin(k, q, do) with G        dk = lin(v, do, q) with G^T
+//     G_{t-1} = l (G_t + c q_t do_t^T)
+//
+// A workgroup walks a stretch of tokens of one head, d / 32 wavefronts with 32
+// columns of the state each, which stay in the accumulators of the matrix
+// cores.  Their layout is the point of the design: a lane of an accumulator
+// holds, of one column, the rows (r / 4) * 8 + 4 * (lane / 32) + r % 4, and if
+// the summed dimension of a product is numbered in this order in both
+// operands, an accumulator's registers are an operand as they stand.  So
+// the scores q k^T, computed with k as the rows, and the state go into the
+// next product without crossing lanes.  Sequences are split into stretches to
+// fill the GPU: one pass computes what each adds to the state, a second one
+// adds these up along the sequence, the third walks the stretches from there.
+#include <algorithm>
+#include <math.h>
+
+#include "adaln.h"
+#include "checks.hpp"
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace adaln {
+namespace {
+
+constexpr int kMaxHead = 128;
+constexpr int kChunk = 32;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// Eight elements of a row or column: those numbered slot(i) of 16 summed ones.
+template <typename T>
+struct Frag;
+template <>
+struct Frag<bf16> {
+  bf16x8 v;
+};
+template <>
+struct Frag<float> {
+  f32x8 v;
+};
+
+__device__ __forceinline__ int half_of() { return lane_id() / 32; }
+__device__ __forceinline__ int slot(int i) {
+  return (i / 4) * 8 + 4 * half_of() + i % 4;
+}
+
+// acc[row of a][row of b] += a b^T over 16 summed elements.
+__device__ __forceinline__ void mma(f32x16 &acc, const Frag<bf16> &a,
+                                    const Frag<bf16> &b) {
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void mma(f32x16 &acc, const Frag<float> &a,
+                                    const Frag<float> &b) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[i], b.v[i], acc, 0, 0, 0);
+}
+
+// Eight float32 as a fragment.
+__device__ __forceinline__ void to_frag(Frag<bf16> &f, const float (&x)[8]) {
+  const Vec v = pack<bf16>(x);
+  f.v = __builtin_bit_cast(bf16x8, v);
+}
+__device__ __forceinline__ void to_frag(Frag<float> &f, const float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.v[i] = x[i];
+}
+__device__ __forceinline__ void from_frag(float (&x)[8], const Frag<bf16> &f) {
+  const Vec v = __builtin_bit_cast(Vec, f.v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = elem<bf16>(v, i);
+}
+__device__ __forceinline__ void from_frag(float (&x)[8],
+                                          const Frag<float> &f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = f.v[i];
+}
+
+// acc += x b^T (or b x^T) with x in float32: of bf16 as the sum of two, so
+// that what the matrix cores are given is within 2^-16 of x.
+template <bool X_FIRST, typename T>
+__device__ __forceinline__ void mma_f32(f32x16 &acc, const float (&x)[8],
+                                        const Frag<T> &b) {
+  Frag<T> hi;
+  to_frag(hi, x);
+  if (X_FIRST)
+    mma(acc, hi, b);
+  else
+    mma(acc, b, hi);
+  if constexpr (sizeof(T) == 2) {
+    float back[8], rest[8];
+    from_frag(back, hi);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = x[i] - back[i];
+    Frag<T> lo;
+    to_frag(lo, rest);
+    if (X_FIRST)
+      mma(acc, lo, b);
+    else
+      mma(acc, b, lo);
+  }
+}
+
+// ----------------------------------------------------------- tiles in LDS
+
+// A stage's tokens of one tensor, in units of four elements; unit u of token
+// r stands at u ^ turn(r), so that the units which 16 lanes read at a time (8
+// for f32), of as many rows or of four rows (two) beside each other, lie in
+// distinct banks.
+template <typename T, int DP>
+struct Tile {
+  static constexpr int E = Elems<T>::value;
+  static constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
+  static constexpr int kUnit = 4 * sizeof(T);
+  static constexpr int kUnits = sizeof(T) == 2 ? (DP <= 32   ? 8
+                                                  : DP <= 64 ? 16
+                                                             : 32)
+                                               : (DP <= 64 ? 16 : 32);
+  static constexpr int kBytes = kTokens * kUnits * kUnit;
+  static constexpr int kRowVecs = DP / E;
+  static constexpr int kVecs = kTokens * kRowVecs;
+
+  static __device__ __forceinline__ int turn(int r) {
+    if (sizeof(T) == 4) return ((r >> 2 & 1) << 3) | (r & 3);
+    if (kUnits == 32) return ((r & 3) << 2) | (r >> 2 & 3);
+    if (kUnits == 16) return ((r >> 1 & 3) << 2) | (r >> 3 & 1);
+    return r >> 2 & 3;
+  }
+  static __device__ __forceinline__ char *at(char *tile, int r, int u) {
+    return tile + (r * kUnits + (u ^ turn(r))) * kUnit;
+  }
+  static __device__ __forceinline__ const char *at(const char *tile, int r,
+                                                   int u) {
+    return tile + (r * kUnits + (u ^ turn(r))) * kUnit;
+  }
+  // vector j of token r
+  static __device__ __forceinline__ void put(char *tile, int r, int j,
+                                             const Vec &v) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint2 *>(at(tile, r, 2 * j)) =
+          make_uint2(v.w[0], v.w[1]);
+      *reinterpret_cast<uint2 *>(at(tile, r, 2 * j + 1)) =
+          make_uint2(v.w[2], v.w[3]);
+    } else {
+      store_vec(at(tile, r, j), v);
+    }
+  }
+  // Tokens r0 + lane % 32, features 16 b + slot(i).
+  static __device__ __forceinline__ Frag<T> rows(const char *tile, int r0,
+                                                 int b) {
+    const int r = r0 + lane_id() % 32, u = 4 * b + half_of();
+    Frag<T> f;
+    if constexpr (sizeof(T) == 2) {
+      const uint2 x = *reinterpret_cast<const uint2 *>(at(tile, r, u));
+      const uint2 y = *reinterpret_cast<const uint2 *>(at(tile, r, u + 2));
+      const u32x4 v = {x.x, x.y, y.x, y.y};
+      f.v = __builtin_bit_cast(bf16x8, v);
+    } else {
+      const Vec x = load_vec(at(tile, r, u)), y = load_vec(at(tile, r, u + 2));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f.v[i] = elem<float>(x, i);
+        f.v[4 + i] = elem<float>(y, i);
+      }
+    }
+    return f;
+  }
+  // Features c0 + lane % 32, tokens r0 + slot(i).
+  static __device__ __forceinline__ Frag<T> cols(const char *tile, int r0,
+                                                 int c0) {
+    const int l = lane_id();
+    Frag<T> f;
+    if constexpr (sizeof(T) == 2) {
+      // 16 lanes read four tokens of 16 features, and get a feature's four
+      // tokens each
+      const int r = r0 + 4 * half_of() + (l % 16) / 4;
+      const int u = c0 / 4 + (l >> 4 & 1) * 4 + (l & 3);
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const s16x4 lo =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at(tile, r, u));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4 *)at(tile, r + 8, u));
+      const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      f.v = __builtin_bit_cast(bf16x8, v);
+    } else {
+      const int c = c0 + l % 32;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        f.v[i] = *reinterpret_cast<const float *>(
+            at(tile, r0 + slot(i), c / 4) + c % 4 * 4);
+    }
+    return f;
+  }
+};
+
+// ------------------------------------------------------------------ the work
+
+// One tensor of heads, distances in vectors of 16 bytes.
+struct Part {
+  const char *data;
+  int64_t batch, token;
+  int32_t head;
+};
+
+// Stretches of up to `len` tokens: B sequences of N tokens, `splits` each, or
+// the segments of a table (a segment without tokens has one stretch too, which
+// hands its state on).
+struct Stretches {
+  int32_t nseg;    // 0: sequences of N tokens
+  int32_t splits;
+  int64_t N, len;
+  int32_t first[kMaxSegments + 1];  // stretches before a segment
+  int64_t row[kMaxSegments + 1];    // tokens before it
+};
+
+struct Stretch {
+  int seq;        // which state
+  int64_t batch;  // which sample of the tensors
+  int64_t start;  // first token
+  int n;          // tokens
+  bool head, tail;  // the sequence's first, last stretch
+};
+
+__device__ __forceinline__ Stretch find_stretch(const Stretches &m, int id) {
+  Stretch s;
+  if (m.nseg == 0) {
+    s.seq = id / m.splits;
+    const int j = id - s.seq * m.splits;
+    s.batch = s.seq;
+    s.start = j * m.len;
+    s.n = (int)min(m.len, m.N - s.start);
+    s.head = j == 0;
+    s.tail = j == m.splits - 1;
+    return s;
+  }
+  int lo = 0, hi = m.nseg - 1;  // last segment with first[] <= id
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (m.first[mid] <= id)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int j = id - m.first[lo];
+  s.seq = lo;
+  s.batch = 0;
+  s.start = m.row[lo] + j * m.len;
+  s.n = (int)min(m.len, m.row[lo + 1] - s.start);
+  s.head = j == 0;
+  s.tail = id == m.first[lo + 1] - 1;
+  return s;
+}
+
+struct Lin {
+  Part in[4];
+  Part out[2];
+  const float *log_decay;
+  const float *init;     // [sequences, H, d, d]: the state before, or NULL
+  float *states;         // [stretches, H, d, d], or NULL: one to a sequence
+  float *final;          // [sequences, H, d, d]: the state behind, or NULL
+  float scale;
+  int32_t H, d;
+  int32_t nvec;          // vectors of a head
+  int64_t first;         // workgroups in the launches before
+  int64_t jobs;          // stretches * H
+};
+
+// log2 of the decay; so strong that 0 tokens leave 1 and one leaves 0.
+__device__ __forceinline__ float decay_of(const Lin &p, int h) {
+  const float g = p.log_decay[h] * 1.44269504088896341f;
+  return g < -1e30f ? -1e30f : g;
+}
+
+// Registers for one stage of NT tensors, vectors of THREADS threads.
+template <typename T, int DP, int NT, int THREADS>
+struct Loads {
+  typedef Tile<T, DP> Tl;
+  static constexpr int kPer = Tl::kVecs / THREADS;
+  Vec v[NT][kPer];
+
+  // n >= 1 tokens from `start`; what lies past them or past the features is
+  // read from the last one that exists, and cleared on its way to LDS
+  __device__ __forceinline__ void load(const Part (&in)[NT], int64_t start,
+                                       int n, int nvec) {
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = threadIdx.x + i * THREADS;
+        const int r = min(x / Tl::kRowVecs, n - 1);
+        const int j = min(x % Tl::kRowVecs, nvec - 1);
+        v[a][i] = load_vec(in[a].data + ((start + r) * in[a].token + j) * 16);
+      }
+  }
+  __device__ __forceinline__ void put(char *tiles, int n, int nvec) const {
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = threadIdx.x + i * THREADS;
+        const int r = x / Tl::kRowVecs, j = x % Tl::kRowVecs;
+        Tl::put(tiles + a * Tl::kBytes, r, j,
+                r < n && j < nvec ? v[a][i] : vzero());
+      }
+  }
+};
+
+// A wavefront's 32 columns of a state, rows by blocks of 32.
+template <int DP>
+struct State {
+  f32x16 s[DP / 32];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[m][r] = 0.f;
+  }
+  // [d, d] in memory; `across`: its transpose.
+  __device__ __forceinline__ void load(const float *src, int d, int c0,
+                                       bool across) {
+    const int c = c0 + lane_id() % 32;
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = 32 * m + 16 * (r / 8) + slot(r % 8);
+        const bool in = row < d && c < d;
+        const int at = across ? c * d + row : row * d + c;
+        const float x = src[in ? at : 0];
+        s[m][r] = in ? x : 0.f;
+      }
+  }
+  __device__ __forceinline__ void store(float *dst, int d, int c0) const {
+    const int c = c0 + lane_id() % 32;
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = 32 * m + 16 * (r / 8) + slot(r % 8);
+        if (row < d && c < d) dst[row * d + c] = s[m][r];
+      }
+  }
+};
+
+// The powers of the decay that a chunk of n tokens needs, forward (REV: from
+// the last token to the first; then the state has c in it).
+template <bool REV>
+struct Powers {
+  float own;      // of the state, for the lane's token
+  float add[16];  // of token 16 j + slot(i) on its way into the state
+  float over;     // of the state over the chunk
+  int n = 0;
+
+  // (only a sequence's last chunk has less than 32: one of the two ends)
+  __device__ __forceinline__ void set(float g, float c, int tokens) {
+    if (n == tokens) return;
+    n = tokens;
+    const int t = lane_id() % 32;
+    own = REV ? exp2f(g * max(n - 1 - t, 0)) : c * exp2f(g * (t + 1));
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const int s = 16 * (x / 8) + slot(x % 8);
+      add[x] = REV ? c * exp2f(g * (s + 1)) : exp2f(g * max(n - 1 - s, 0));
+    }
+    over = exp2f(g * n);
+  }
+};
+
+// The state over one chunk of 32 tokens from token r0 of the stage.
+template <typename T, int DP, bool REV>
+__device__ __forceinline__ void advance(State<DP> &S, const char *K,
+                                        const Frag<T> (&v)[2], int r0,
+                                        const Powers<REV> &pw) {
+  float x[2][8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    from_frag(x[j], v[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[j][i] *= pw.add[8 * j + i];
+  }
+#pragma unroll
+  for (int m = 0; m < DP / 32; ++m) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S.s[m][r] *= pw.over;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      mma_f32<false>(S.s[m], x[j], Tile<T, DP>::cols(K, r0 + 16 * j, 32 * m));
+  }
+}
+
+// What each stretch adds to the state (from zero): S of its own tokens, at the
+// place of the state that the next one starts from.
+template <typename T, int DP, bool REV>
+__global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) {
+  typedef Tile<T, DP> Tl;
+  constexpr int kThreads = 2 * DP;
+  __shared__ __align__(1024) char tiles[2 * Tl::kBytes];
+  const int64_t job = p.first + blockIdx.x;
+  const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
+  const Stretch st = find_stretch(map, id);
+  if (REV ? st.head : st.tail) return;  // nobody starts from its end
+  const Part in[2] = {
+      {p.in[0].data + (st.batch * p.in[0].batch + (int64_t)h * p.in[0].head) * 16,
+       0, p.in[0].token, 0},
+      {p.in[1].data + (st.batch * p.in[1].batch + (int64_t)h * p.in[1].head) * 16,
+       0, p.in[1].token, 0}};
+  const float g = decay_of(p, h);
+  const int c0 = 32 * wave_id();
+  State<DP> S;
+  S.clear();
+  Powers<REV> pw;
+  Loads<T, DP, 2, kThreads> ld;
+  const int stages = (st.n + Tl::kTokens - 1) / Tl::kTokens;
+  auto from = [&](int i) { return (REV ? stages - 1 - i : i) * Tl::kTokens; };
+  if (stages > 0)
+    ld.load(in, st.start + from(0), min(Tl::kTokens, st.n - from(0)), p.nvec);
+  for (int i = 0; i < stages; ++i) {
+    const int n = min(Tl::kTokens, st.n - from(i));
+    __syncthreads();
+    ld.put(tiles, n, p.nvec);
+    __syncthreads();
+    if (i + 1 < stages)
+      ld.load(in, st.start + from(i + 1),
+              min(Tl::kTokens, st.n - from(i + 1)), p.nvec);
+#pragma unroll
+    for (int c = 0; c < Tl::kTokens / kChunk; ++c) {
+      const int r0 = REV ? Tl::kTokens - kChunk * (c + 1) : kChunk * c;
+      const int left = n - r0;
+      if (left <= 0) continue;
+      pw.set(g, p.scale, min(left, kChunk));
+      Frag<T> v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        v[j] = Tl::cols(tiles + Tl::kBytes, r0 + 16 * j, c0);
+      advance<T, DP, REV>(S, tiles, v, r0, pw);
+    }
+  }
+  S.store(p.states + job * p.d * p.d, p.d, c0);
+}
+
+// Along each sequence: states[j] = the state before stretch j.
+template <bool REV>
+__global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
+                                                      int32_t blocks) {
+  const int64_t row = blockIdx.x / blocks;  // sequence, head
+  const int seq = (int)(row / p.H), h = (int)(row - (int64_t)seq * p.H);
+  const int dd = p.d * p.d;
+  const int at = ((int)(blockIdx.x - row * blocks) * kBlock + threadIdx.x) * 4;
+  if (at >= dd) return;
+  const int first = map.nseg == 0 ? seq * map.splits : map.first[seq];
+  const int count = map.nseg == 0 ? map.splits : map.first[seq + 1] - first;
+  const float g = decay_of(p, h);
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.init != nullptr)
+    run = *reinterpret_cast<const float4 *>(p.init + row * dd + at);
+  const int64_t tokens =
+      map.nseg == 0 ? map.N : map.row[seq + 1] - map.row[seq];
+  for (int i = 0; i < count; ++i) {
+    const int j = REV ? count - 1 - i : i;
+    float4 *s = reinterpret_cast<float4 *>(
+        p.states + ((int64_t)(first + j) * p.H + h) * dd + at);
+    const float4 before = run;
+    if (i + 1 < count) {
+      const float4 own = *s;
+      const float over = exp2f(g * (float)min(map.len, tokens - j * map.len));
+      run.x = fmaf(run.x, over, own.x);
+      run.y = fmaf(run.y, over, own.y);
+      run.z = fmaf(run.z, over, own.z);
+      run.w = fmaf(run.w, over, own.w);
+    }
+    *s = before;
+  }
+}
+
+// The outputs of a stretch, from the state before it.  ROLES 1: in = q, k, v.
+// ROLES 2, the two gradients that run backwards: in = q, k, v, do, out = dv
+// (of k, q, do) and dk (of v, do, q), a set of wavefronts for each.  `across`
+// (bit by role): the states in memory are the transpose of this role's.
+template <typename T, int DP, bool REV, int ROLES>
+__global__ __launch_bounds__(2 * DP * ROLES,
+                             ROLES == 1 ? 2 : 1) void out_kernel(
+    Lin p, Stretches map, int32_t across) {
+  typedef Tile<T, DP> Tl;
+  constexpr int kThreads = 2 * DP * ROLES, NT = ROLES + 2;
+  constexpr int kWaves = kThreads / kWave;
+  constexpr int kPitch = 36 * sizeof(T);  // of a token's 32 outputs in LDS
+  constexpr int E = Elems<T>::value;
+  __shared__ __align__(1024) char tiles[NT * Tl::kBytes];
+  __shared__ __align__(16) char outs[kWaves][kChunk * kPitch];
+  const int64_t job = p.first + blockIdx.x;
+  const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
+  const Stretch st = find_stretch(map, id);
+  const int wave = wave_id(), lane = lane_id();
+  const int role = ROLES == 1 ? 0 : wave / (DP / 32);
+  const int c0 = 32 * (ROLES == 1 ? wave : wave % (DP / 32));
+  Part in[NT];
+#pragma unroll
+  for (int a = 0; a < NT; ++a) {
+    in[a] = p.in[a];
+    in[a].data += (st.batch * in[a].batch + (int64_t)h * in[a].head) * 16;
+  }
+  const Part out = p.out[role];
+  char *dst = const_cast<char *>(out.data) +
+              (st.batch * out.batch + (int64_t)h * out.head) * 16;
+  const char *Q = tiles + (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
+  const char *K = tiles + (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
+  const char *V = tiles + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
+  const float g = decay_of(p, h);
+  const int64_t dd = (int64_t)p.d * p.d;
+  State<DP> S;
+  const float *src = p.states != nullptr ? p.states + job * dd
+                     : p.init != nullptr
+                         ? p.init + ((int64_t)st.seq * p.H + h) * dd
+                         : nullptr;
+  if (src != nullptr)
+    S.load(src, p.d, c0, across >> role & 1);
+  else
+    S.clear();
+  // powers of the scores: rows are s, the lane's column t
+  float near[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int s = 16 * (r / 8) + slot(r % 8), t = lane % 32;
+    const int e = REV ? s - t : t - s;
+    near[r] = e >= 0 ? p.scale * exp2f(g * e) : 0.f;
+  }
+  Powers<REV> pw;
+  Loads<T, DP, NT, kThreads> ld;
+  const int stages = (st.n + Tl::kTokens - 1) / Tl::kTokens;
+  auto from = [&](int i) { return (REV ? stages - 1 - i : i) * Tl::kTokens; };
+  if (stages > 0)
+    ld.load(in, st.start + from(0), min(Tl::kTokens, st.n - from(0)), p.nvec);
+  for (int i = 0; i < stages; ++i) {
+    const int n = min(Tl::kTokens, st.n - from(i));
+    __syncthreads();
+    ld.put(tiles, n, p.nvec);
+    __syncthreads();
+    if (i + 1 < stages)
+      ld.load(in, st.start + from(i + 1),
+              min(Tl::kTokens, st.n - from(i + 1)), p.nvec);
+#pragma unroll
+    for (int c = 0; c < Tl::kTokens / kChunk; ++c) {
+      const int r0 = REV ? Tl::kTokens - kChunk * (c + 1) : kChunk * c;
+      const int left = n - r0;
+      if (left <= 0) continue;
+      pw.set(g, p.scale, min(left, kChunk));
+      // scores (rows s, columns t) and the state's part, in one pass over q
+      f32x16 a = {}, o = {};
+#pragma unroll
+      for (int b = 0; b < DP / 16; ++b) {
+        const Frag<T> q = Tl::rows(Q, r0, b);
+        mma(a, Tl::rows(K, r0, b), q);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = S.s[b / 2][8 * (b % 2) + e];
+        mma_f32<true>(o, x, q);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[r] *= pw.own;
+      Frag<T> v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j] = Tl::cols(V, r0 + 16 * j, c0);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = a[8 * j + e] * near[8 * j + e];
+        mma_f32<false>(o, x, v[j]);
+      }
+      advance<T, DP, REV>(S, K, v, r0, pw);
+      // o: rows are features, the lane's column its token; through LDS into
+      // rows of 32 features
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        char *at = outs[wave] + (lane % 32) * kPitch +
+                   (16 * (r / 8) + slot(r % 8)) * sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+          const float x[8] = {o[r], o[r + 1], o[r + 2], o[r + 3], 0, 0, 0, 0};
+          const Vec y = pack<bf16>(x);
+          *reinterpret_cast<uint2 *>(at) = make_uint2(y.w[0], y.w[1]);
+        } else {
+          *reinterpret_cast<float4 *>(at) =
+              make_float4(o[r], o[r + 1], o[r + 2], o[r + 3]);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+      constexpr int kRow = 32 / E;  // vectors of 32 features
+#pragma unroll
+      for (int x = lane; x < kChunk * kRow; x += kWave) {
+        const int t = x / kRow, j = x % kRow;
+        Vec y;
+        const uint2 *from_lds = reinterpret_cast<const uint2 *>(
+            outs[wave] + t * kPitch + j * 16);
+        const uint2 lo = from_lds[0], hi = from_lds[1];
+        y.w[0] = lo.x;
+        y.w[1] = lo.y;
+        y.w[2] = hi.x;
+        y.w[3] = hi.y;
+        if (t < left && c0 / E + j < p.nvec)
+          store_vec(dst + ((st.start + from(i) + r0 + t) * out.token + c0 / E +
+                           j) * 16,
+                    y);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  if (p.final != nullptr && role == 0 && (REV ? st.head : st.tail))
+    S.store(p.final + ((int64_t)st.seq * p.H + h) * dd, p.d, c0);
+}
+
+// One token of each sample: S' = l S + k v^T, o = c S'^T q.  A thread holds
+// four columns of every R-th row.
+struct Step {
+  Part q, k, v, o;
+  const float *log_decay, *state;
+  float *state_out;
+  float scale;
+  int32_t H, d;
+  int32_t cols;    // threads across a workgroup's columns
+  int32_t groups;  // workgroups across the state's
+  int64_t jobs;
+};
+
+template <typename T>
+__device__ __forceinline__ float scalar(const Part &p, int64_t b, int h,
+                                        int i) {
+  const char *at = p.data + (b * p.batch + (int64_t)h * p.head) * 16;
+  if constexpr (sizeof(T) == 2)
+    return __builtin_bit_cast(
+        float, (uint32_t)reinterpret_cast<const uint16_t *>(at)[i] << 16);
+  else
+    return reinterpret_cast<const float *>(at)[i];
+}
+
+template <typename T>
+__global__ __launch_bounds__(kBlock) void step_kernel(Step p) {
+  __shared__ float sums[kBlock][4];
+  __shared__ float qk[2][kMaxHead];
+  const int t = threadIdx.x;
+  const int c = t % p.cols, r0 = t / p.cols, R = kBlock / p.cols;
+  for (int64_t job = blockIdx.x; job < p.jobs; job += gridDim.x) {
+    const int64_t bh = job / p.groups;
+    const int64_t b = bh / p.H;
+    const int h = (int)(bh - b * p.H);
+    const int col = ((int)(job - bh * p.groups) * p.cols + c) * 4;
+    const bool active = r0 < R && col < p.d;
+    __syncthreads();
+    if (t < p.d) qk[0][t] = scalar<T>(p.q, b, h, t);
+    if (t >= kMaxHead && t - kMaxHead < p.d)
+      qk[1][t - kMaxHead] = scalar<T>(p.k, b, h, t - kMaxHead);
+    float v[4] = {}, sum[4] = {};
+    if (active)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = scalar<T>(p.v, b, h, col + i);
+    const float l = expf(p.log_decay[h]);
+    __syncthreads();
+    if (active) {
+      const float *src = p.state + bh * p.d * p.d + col;
+      float *dst = p.state_out + bh * p.d * p.d + col;
+#pragma unroll 4
+      for (int r = r0; r < p.d; r += R) {
+        const float4 s = *reinterpret_cast<const float4 *>(src + r * p.d);
+        const float k = qk[1][r], q = qk[0][r];
+        float4 n;
+        n.x = fmaf(l, s.x, k * v[0]);
+        n.y = fmaf(l, s.y, k * v[1]);
+        n.z = fmaf(l, s.z, k * v[2]);
+        n.w = fmaf(l, s.w, k * v[3]);
+        sum[0] = fmaf(q, n.x, sum[0]);
+        sum[1] = fmaf(q, n.y, sum[1]);
+        sum[2] = fmaf(q, n.z, sum[2]);
+        sum[3] = fmaf(q, n.w, sum[3]);
+        *reinterpret_cast<float4 *>(dst + r * p.d) = n;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[t][i] = sum[i];
+    __syncthreads();
+    if (active && r0 == 0) {
+      for (int r = 1; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += sums[t + r * p.cols][i];
+      char *at = const_cast<char *>(p.o.data) +
+                 (b * p.o.batch + (int64_t)h * p.o.head) * 16;
+      const float x[8] = {p.scale * sum[0], p.scale * sum[1],
+                          p.scale * sum[2], p.scale * sum[3], 0, 0, 0, 0};
+      if constexpr (sizeof(T) == 2) {
+        const Vec y = pack<bf16>(x);
+        *reinterpret_cast<uint2 *>(at + col * 2) = make_uint2(y.w[0], y.w[1]);
+      } else {
+        *reinterpret_cast<float4 *>(at + col * 4) =
+            make_float4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- planning
+
+int elems_per_vec(int dtype) { return dtype == ADALN_BF16 ? 8 : 4; }
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+// Stretches are long enough that the GPU is filled about twice, and not
+// shorter than 128 tokens: what a stretch adds, its state written and read
+// three times, is the traffic of some 200 tokens.
+constexpr int64_t kFill = 2 * kCUs;
+constexpr int64_t kShort = 128;
+constexpr int64_t kStage = 64;  // stretches are whole stages of either type
+
+// false: more stretches than can be numbered.
+bool make_stretches(Stretches &m, const int64_t *off, int64_t nseg, int64_t B,
+                    int64_t N, int64_t H, int64_t *count) {
+  m = Stretches{};
+  const int64_t tokens = off != nullptr ? (nseg > 0 ? off[nseg] : 0) : B * N;
+  int64_t len = std::max(kShort, tokens * H / kFill);
+  len = (len + kStage - 1) / kStage * kStage;
+  m.N = N;
+  m.len = len;
+  if (off == nullptr) {
+    m.splits = (int32_t)std::max<int64_t>(1, (N + len - 1) / len);
+    *count = B * m.splits;
+    return *count * H <= kMaxRows;
+  }
+  m.nseg = (int32_t)nseg;
+  int64_t n = 0;
+  bool more = false;
+  for (int64_t s = 0; s < nseg; ++s) {
+    m.first[s] = (int32_t)n;
+    m.row[s] = off[s];
+    const int64_t k =
+        std::max<int64_t>(1, (off[s + 1] - off[s] + len - 1) / len);
+    more |= k > 1;
+    n += k;
+  }
+  m.first[nseg] = (int32_t)n;
+  m.row[nseg] = tokens;
+  m.splits = more ? 2 : 1;
+  *count = n;
+  return n * H <= kMaxRows;
+}
+
+size_t states_bytes(const Stretches &m, int64_t count, int64_t H, int64_t d) {
+  return m.splits > 1 ? (size_t)count * H * d * d * sizeof(float) : 0;
+}
+
+int hip_fail(hipError_t e, const char *what) {
+  return fail(ADALN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+constexpr int64_t kLaunch = 1 << 20;  // workgroups of a launch
+
+template <typename K, typename... A>
+hipError_t launch_jobs(K k, int threads, Lin p, hipStream_t s, A... args) {
+  for (p.first = 0; p.first < p.jobs; p.first += kLaunch) {
+    void *argv[] = {(void *)&p, (void *)&args...};
+    const hipError_t e = hipLaunchKernel(
+        (const void *)k, dim3((unsigned)std::min(kLaunch, p.jobs - p.first)),
+        dim3(threads), argv, 0, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T, bool REV>
+hipError_t run_states(const Lin &p, const Stretches &m, hipStream_t s) {
+  if (p.d <= 32)
+    return launch_jobs(state_kernel<T, 32, REV>, 64, p, s, m);
+  if (p.d <= 64)
+    return launch_jobs(state_kernel<T, 64, REV>, 128, p, s, m);
+  if (p.d <= 96)
+    return launch_jobs(state_kernel<T, 96, REV>, 192, p, s, m);
+  return launch_jobs(state_kernel<T, 128, REV>, 256, p, s, m);
+}
+
+template <typename T, bool REV, int ROLES>
+hipError_t run_out(const Lin &p, const Stretches &m, int32_t across,
+                   hipStream_t s) {
+  if (p.d <= 32)
+    return launch_jobs(out_kernel<T, 32, REV, ROLES>, 64 * ROLES, p, s, m,
+                       across);
+  if (p.d <= 64)
+    return launch_jobs(out_kernel<T, 64, REV, ROLES>, 128 * ROLES, p, s, m,
+                       across);
+  if (p.d <= 96)
+    return launch_jobs(out_kernel<T, 96, REV, ROLES>, 192 * ROLES, p, s, m,
+                       across);
+  return launch_jobs(out_kernel<T, 128, REV, ROLES>, 256 * ROLES, p, s, m,
+                     across);
+}
+
+// The states that the stretches start from: p.in are the two parts that make
+// up the state.
+template <bool REV>
+hipError_t make_states(const Lin &p, const Stretches &m, int64_t sequences,
+                       int dtype, hipStream_t s) {
+  hipError_t e = dtype == ADALN_BF16 ? run_states<bf16, REV>(p, m, s)
+                                     : run_states<float, REV>(p, m, s);
+  if (e != hipSuccess) return e;
+  const int32_t blocks = (p.d * p.d / 4 + kBlock - 1) / kBlock;
+  void *argv[] = {(void *)&p, (void *)&m, (void *)&blocks};
+  return hipLaunchKernel((const void *)scan_kernel<REV>,
+                         dim3((unsigned)(sequences * p.H * blocks)),
+                         dim3(kBlock), argv, 0, s);
+}
+
+Part part_of(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
+             int dtype) {
+  Part h = {};
+  if (t == nullptr) return h;
+  const int E = elems_per_vec(dtype);
+  h.data = static_cast<const char *>(t->data);
+  h.batch = B > 1 ? t->batch_stride / E : 0;
+  h.token = N > 1 ? t->token_stride / E : 0;
+  h.head = H > 1 ? (int32_t)(t->head_stride / E) : 0;
+  return h;
+}
+
+int check_lin(const float *log_decay, float scale, const int64_t *off,
+              int64_t nseg, int64_t B, int64_t N, int64_t H, int64_t d,
+              int dtype) {
+  if (dtype != ADALN_F32 && dtype != ADALN_BF16)
+    return fail(ADALN_ERR_DTYPE, "unknown dtype code %d", dtype);
+  if (B < 0 || N < 0 || H < 0)
+    return fail(ADALN_ERR_INVALID, "negative size: B=%lld N=%lld H=%lld",
+                (long long)B, (long long)N, (long long)H);
+  if (d <= 0)
+    return fail(ADALN_ERR_INVALID, "d must be positive, got %lld",
+                (long long)d);
+  const int E = elems_per_vec(dtype);
+  if (d % E != 0)
+    return fail(ADALN_ERR_ALIGN, "d=%lld is not a multiple of %d",
+                (long long)d, E);
+  if (d > kMaxHead)
+    return fail(ADALN_ERR_UNSUPPORTED, "d=%lld exceeds the widest head (%d)",
+                (long long)d, kMaxHead);
+  if (H > 4096) return fail(ADALN_ERR_INVALID, "more than 4096 heads");
+  if (B > (int64_t(1) << 20))
+    return fail(ADALN_ERR_INVALID, "B=%lld exceeds 2^20", (long long)B);
+  if (N > kMaxRows || (N > 0 && B > kMaxRows / N))
+    return fail(ADALN_ERR_INVALID, "B*N exceeds 2^31-1 tokens");
+  if (off != nullptr) {
+    if (B != 1)
+      return fail(ADALN_ERR_INVALID, "packed sequences need B=1, got %lld",
+                  (long long)B);
+    if (nseg < 1)
+      return fail(ADALN_ERR_INVALID, "nseg=%lld outside [1, %d]",
+                  (long long)nseg, kMaxSegments);
+    ADALN_TRY(check_segments(off, nullptr, nseg, nseg, 8, ADALN_BF16));
+    if (off[nseg] != N)
+      return fail(ADALN_ERR_INVALID, "seg_offsets end at %lld, N is %lld",
+                  (long long)off[nseg], (long long)N);
+  }
+  if (!isfinite(scale))
+    return fail(ADALN_ERR_INVALID, "scale is not finite");
+  const bool work = H > 0 && B > 0;
+  if (work && log_decay == nullptr)
+    return fail(ADALN_ERR_INVALID, "log_decay is NULL");
+  if (work && reinterpret_cast<uintptr_t>(log_decay) % 4 != 0)
+    return fail(ADALN_ERR_ALIGN, "log_decay is not 4-byte aligned");
+  return ADALN_OK;
+}
+
+int check_workspace(const void *ws, size_t have, size_t need,
+                    const char *name) {
+  if (need == 0) return ADALN_OK;
+  if (ws == nullptr || have < need)
+    return fail(ADALN_ERR_WORKSPACE, "%s needs %zu bytes, got %zu%s", name,
+                need, have, ws == nullptr ? " (NULL)" : "");
+  return check_ptr(ws, true, name);
+}
+
+Lin lin_of(const float *log_decay, float scale, int64_t H, int64_t d,
+           int64_t count, int dtype) {
+  Lin p = {};
+  p.log_decay = log_decay;
+  p.scale = scale;
+  p.H = (int32_t)H;
+  p.d = (int32_t)d;
+  p.nvec = (int32_t)(d / elems_per_vec(dtype));
+  p.jobs = count * H;
+  return p;
+}
+
+const int kTooMany = ADALN_ERR_UNSUPPORTED;
+
+}  // namespace
+}  // namespace adaln
+
+using namespace adaln;
+
+ADALN_API size_t adaln_lin_attn_states_bytes(const int64_t *seg_offsets,
+                                             int64_t nseg, int64_t B,
+                                             int64_t N, int64_t H, int64_t d,
+                                             int dtype) {
+  static const float any = 0.f;
+  if (check_lin(&any, 1.f, seg_offsets, nseg, B, N, H, d, dtype) != ADALN_OK)
+    return 0;
+  Stretches m;
+  int64_t count;
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, &count)) return 0;
+  return states_bytes(m, count, H, d);
+}
+
+ADALN_API int adaln_lin_attn_fwd(
+    const adaln_heads_t *q, const adaln_heads_t *k, const adaln_heads_t *v,
+    const float *log_decay, float scale, const float *state,
+    const adaln_heads_t *o, float *state_out, float *states,
+    size_t states_size, const int64_t *seg_offsets, int64_t nseg, int64_t B,
+    int64_t N, int64_t H, int64_t d, int dtype, void *stream) {
+  ADALN_TRY(check_lin(log_decay, scale, seg_offsets, nseg, B, N, H, d, dtype));
+  ADALN_TRY(check_heads(q, B, N, H, d, dtype, false, "q"));
+  ADALN_TRY(check_heads(k, B, N, H, d, dtype, false, "k"));
+  ADALN_TRY(check_heads(v, B, N, H, d, dtype, false, "v"));
+  ADALN_TRY(check_heads(o, B, N, H, d, dtype, true, "o"));
+  ADALN_TRY(check_ptr(state, state != nullptr, "state"));
+  ADALN_TRY(check_ptr(state_out, state_out != nullptr, "state_out"));
+  if (B == 0 || H == 0) return ok();
+  Stretches m;
+  int64_t count;
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, &count))
+    return fail(kTooMany, "too many sequences and heads");
+  const size_t need = states_bytes(m, count, H, d);
+  ADALN_TRY(check_workspace(states, states_size, need, "states"));
+  const hipStream_t s = (hipStream_t)stream;
+  const int64_t sequences = seg_offsets != nullptr ? nseg : B;
+  Lin p = lin_of(log_decay, scale, H, d, count, dtype);
+  p.init = state;
+  p.states = need > 0 ? states : nullptr;
+  hipError_t e = hipSuccess;
+  if (need > 0) {
+    p.in[0] = part_of(k, B, N, H, dtype);
+    p.in[1] = part_of(v, B, N, H, dtype);
+    e = make_states<false>(p, m, sequences, dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_fwd states");
+  }
+  p.in[0] = part_of(q, B, N, H, dtype);
+  p.in[1] = part_of(k, B, N, H, dtype);
+  p.in[2] = part_of(v, B, N, H, dtype);
+  p.out[0] = part_of(o, B, N, H, dtype);
+  p.final = state_out;
+  e = dtype == ADALN_BF16 ? run_out<bf16, false, 1>(p, m, 0, s)
+                          : run_out<float, false, 1>(p, m, 0, s);
+  if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_fwd launch");
+  return ok();
+}
+
+ADALN_API size_t adaln_lin_attn_bwd_workspace_bytes(
+    int saved, const int64_t *seg_offsets, int64_t nseg, int64_t B, int64_t N,
+    int64_t H, int64_t d, int dtype) {
+  return (saved ? 1 : 2) * adaln_lin_attn_states_bytes(seg_offsets, nseg, B, N,
+                                                       H, d, dtype);
+}
+
+ADALN_API int adaln_lin_attn_bwd(
+    const adaln_heads_t *d_o, const adaln_heads_t *q, const adaln_heads_t *k,
+    const adaln_heads_t *v, const float *log_decay, float scale,
+    const float *state, const float *states, const float *dstate_out,
+    const adaln_heads_t *dq, const adaln_heads_t *dk, const adaln_heads_t *dv,
+    float *dstate, void *workspace, size_t workspace_bytes,
+    const int64_t *seg_offsets, int64_t nseg, int64_t B, int64_t N, int64_t H,
+    int64_t d, int dtype, void *stream) {
+  ADALN_TRY(check_lin(log_decay, scale, seg_offsets, nseg, B, N, H, d, dtype));
+  ADALN_TRY(check_heads(d_o, B, N, H, d, dtype, false, "do"));
+  ADALN_TRY(check_heads(q, B, N, H, d, dtype, false, "q"));
+  ADALN_TRY(check_heads(k, B, N, H, d, dtype, false, "k"));
+  ADALN_TRY(check_heads(v, B, N, H, d, dtype, false, "v"));
+  ADALN_TRY(check_heads(dq, B, N, H, d, dtype, true, "dq"));
+  ADALN_TRY(check_heads(dk, B, N, H, d, dtype, true, "dk"));
+  ADALN_TRY(check_heads(dv, B, N, H, d, dtype, true, "dv"));
+  ADALN_TRY(check_ptr(state, state != nullptr, "state"));
+  ADALN_TRY(check_ptr(states, states != nullptr, "states"));
+  ADALN_TRY(check_ptr(dstate_out, dstate_out != nullptr, "dstate_out"));
+  ADALN_TRY(check_ptr(dstate, dstate != nullptr, "dstate"));
+  if (B == 0 || H == 0) return ok();
+  Stretches m;
+  int64_t count;
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, &count))
+    return fail(kTooMany, "too many sequences and heads");
+  const size_t one = states_bytes(m, count, H, d);
+  ADALN_TRY(check_workspace(workspace, workspace_bytes,
+                            one * (states != nullptr ? 1 : 2), "workspace"));
+  const hipStream_t s = (hipStream_t)stream;
+  const int64_t sequences = seg_offsets != nullptr ? nseg : B;
+  float *ws = static_cast<float *>(workspace);
+  const Part pq = part_of(q, B, N, H, dtype), pk = part_of(k, B, N, H, dtype),
+             pv = part_of(v, B, N, H, dtype),
+             pdo = part_of(d_o, B, N, H, dtype);
+  Lin p = lin_of(log_decay, scale, H, d, count, dtype);
+  hipError_t e;
+  // dq, from the forward's states
+  p.init = state;
+  if (one > 0) {
+    if (states != nullptr) {
+      p.states = const_cast<float *>(states);
+    } else {
+      p.states = ws + one / sizeof(float);
+      p.in[0] = pk;
+      p.in[1] = pv;
+      e = make_states<false>(p, m, sequences, dtype, s);
+      if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd states");
+    }
+  }
+  p.in[0] = pdo;
+  p.in[1] = pv;
+  p.in[2] = pk;
+  p.out[0] = part_of(dq, B, N, H, dtype);
+  e = dtype == ADALN_BF16 ? run_out<bf16, false, 1>(p, m, 1, s)
+                          : run_out<float, false, 1>(p, m, 1, s);
+  if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd dq");
+  // dk and dv, from the states' gradients
+  p.init = dstate_out;
+  if (one > 0) {
+    p.states = ws;
+    p.in[0] = pq;
+    p.in[1] = pdo;
+    e = make_states<true>(p, m, sequences, dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd gradients");
+  }
+  p.in[0] = pq;
+  p.in[1] = pk;
+  p.in[2] = pv;
+  p.in[3] = pdo;
+  p.out[0] = part_of(dv, B, N, H, dtype);
+  p.out[1] = part_of(dk, B, N, H, dtype);
+  p.final = dstate;
+  e = dtype == ADALN_BF16 ? run_out<bf16, true, 2>(p, m, 2, s)
+                          : run_out<float, true, 2>(p, m, 2, s);
+  if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd dk, dv");
+  return ok();
+}
+
+ADALN_API int adaln_lin_attn_step(const adaln_heads_t *q,
+                                  const adaln_heads_t *k,
+                                  const adaln_heads_t *v,
+                                  const float *log_decay, float scale,
+                                  const float *state, const adaln_heads_t *o,
+                                  float *state_out, int64_t B, int64_t H,
+                                  int64_t d, int dtype, void *stream) {
+  ADALN_TRY(check_lin(log_decay, scale, nullptr, 0, B, 1, H, d, dtype));
+  ADALN_TRY(check_heads(q, B, 1, H, d, dtype, false, "q"));
+  ADALN_TRY(check_heads(k, B, 1, H, d, dtype, false, "k"));
+  ADALN_TRY(check_heads(v, B, 1, H, d, dtype, false, "v"));
+  ADALN_TRY(check_heads(o, B, 1, H, d, dtype, true, "o"));
+  const bool work = B > 0 && H > 0;
+  ADALN_TRY(check_ptr(state, work, "state"));
+  ADALN_TRY(check_ptr(state_out, work, "state_out"));
+  if (!work) return ok();
+  Step p = {};
+  p.q = part_of(q, B, 1, H, dtype);
+  p.k = part_of(k, B, 1, H, dtype);
+  p.v = part_of(v, B, 1, H, dtype);
+  p.o = part_of(o, B, 1, H, dtype);
+  p.log_decay = log_decay;
+  p.scale = scale;
+  p.state = state;
+  p.state_out = state_out;
+  p.H = (int32_t)H;
+  p.d = (int32_t)d;
+  // whole rows to a workgroup, or pieces of 32 columns where that would leave
+  // most CUs idle
+  const int quads = (int)(d / 4);
+  p.cols = B * H < kCUs ? std::min(quads, 8) : quads;
+  p.groups = (quads + p.cols - 1) / p.cols;
+  p.jobs = B * H * p.groups;
+  const hipError_t e =
+      dtype == ADALN_BF16
+          ? launch_kernel(step_kernel<bf16>, p.jobs, (hipStream_t)stream, p)
+          : launch_kernel(step_kernel<float>, p.jobs, (hipStream_t)stream, p);
+  if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_step launch");
+  return ok();
+}

@@ -426,6 +426,83 @@ int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
                   void *stream);
 
 /*
+ * Linear attention with a decay for each head: a state of d x d takes the
+ * place of all earlier tokens,
+ *     S_t = l S_{t-1} + k_t v_t^T     o_t = scale * S_t^T q_t
+ *   q, k, v, o   [B,N,H,d] dtype, adaln_heads as for the rotations; an output
+ *                must not overlap an input or another output
+ *   log_decay    device f32 [H]: l = exp(log_decay), at most 0 (0: nothing is
+ *                forgotten; -inf: each token sees itself alone).  A constant
+ *                of the head: there is no gradient of it.
+ *   state        [B,H,d,d] f32 in, or NULL (zero): S before the first token,
+ *                rows k's features, columns v's
+ *   state_out    [B,H,d,d] f32 out, or NULL: S behind the last token
+ *   states       f32 out, adaln_lin_attn_states_bytes bytes (0 for so few
+ *                tokens that none are needed; NULL will do then): the states
+ *                within the sequences, which the backward may have again
+ *   seg_offsets  NULL, or host int64 [nseg+1], 1 <= nseg <= 128: B is 1 and
+ *                the N tokens are nseg packed sequences, sequence s having
+ *                the tokens seg_offsets[s] up to seg_offsets[s+1]; state and
+ *                state_out are then [nseg,H,d,d].  Read during the call only.
+ * d is a multiple of 8 (bf16) or 4 (f32), at most 128; at most 4096 heads; B at
+ * most 2^20.  States and sums are float32; of bf16 inputs, what enters a
+ * product besides them (scores, decayed values, states) does so as two bf16.
+ * A sequence without tokens hands its state on.  Inputs are finite: one that is
+ * not spoils its own and all later tokens' outputs, as the formula has it, and
+ * may spoil those of up to 31 tokens before it.
+ */
+size_t adaln_lin_attn_states_bytes(const int64_t *seg_offsets, int64_t nseg,
+                                   int64_t B, int64_t N, int64_t H, int64_t d,
+                                   int dtype);
+
+int adaln_lin_attn_fwd(const adaln_heads_t *q, const adaln_heads_t *k,
+                       const adaln_heads_t *v, const float *log_decay,
+                       float scale, const float *state, const adaln_heads_t *o,
+                       float *state_out, float *states, size_t states_bytes,
+                       const int64_t *seg_offsets, int64_t nseg, int64_t B,
+                       int64_t N, int64_t H, int64_t d, int dtype,
+                       void *stream);
+
+/*
+ * Its gradient:
+ *     dq_t = scale * S_t do_t     dk_t = G_t v_t     dv_t = G_t^T k_t
+ *     G_t = scale * q_t do_t^T + l G_{t+1},  G_N = scale * q_N do_N^T + dS_N
+ *   d_o         gradient of o;  q, k, v, log_decay, scale, state: the forward's
+ *   states      as the forward of the same sizes wrote them, or NULL: computed
+ *               again
+ *   dstate_out  [B,H,d,d] f32 in, or NULL (zero): dS_N, gradient of state_out
+ *   dq, dk, dv  [B,N,H,d] dtype out
+ *   dstate      [B,H,d,d] f32 out, or NULL: gradient of state
+ *   workspace   adaln_lin_attn_bwd_workspace_bytes bytes; `saved`: whether
+ *               `states` is given
+ * Results are bitwise reproducible.
+ */
+size_t adaln_lin_attn_bwd_workspace_bytes(int saved,
+                                          const int64_t *seg_offsets,
+                                          int64_t nseg, int64_t B, int64_t N,
+                                          int64_t H, int64_t d, int dtype);
+
+int adaln_lin_attn_bwd(const adaln_heads_t *d_o, const adaln_heads_t *q,
+                       const adaln_heads_t *k, const adaln_heads_t *v,
+                       const float *log_decay, float scale, const float *state,
+                       const float *states, const float *dstate_out,
+                       const adaln_heads_t *dq, const adaln_heads_t *dk,
+                       const adaln_heads_t *dv, float *dstate, void *workspace,
+                       size_t workspace_bytes, const int64_t *seg_offsets,
+                       int64_t nseg, int64_t B, int64_t N, int64_t H,
+                       int64_t d, int dtype, void *stream);
+
+/*
+ * One token of each of B samples (token strides are not read): state_out = l
+ * state + k v^T, o = scale * state_out^T q.  state_out may be state.
+ */
+int adaln_lin_attn_step(const adaln_heads_t *q, const adaln_heads_t *k,
+                        const adaln_heads_t *v, const float *log_decay,
+                        float scale, const float *state,
+                        const adaln_heads_t *o, float *state_out, int64_t B,
+                        int64_t H, int64_t d, int dtype, void *stream);
+
+/*
  * The join of a branch with the residual stream: the gate that a block's
  * conditioning gives beside scale and shift, and dropout whose mask is never
  * stored.
