@@ -96,118 +96,165 @@ __device__ __forceinline__ void from_frag(float (&x)[8],
   for (int i = 0; i < 8; ++i) x[i] = f.v[i];
 }
 
-// acc += x b^T (or b x^T) with x in float32: of bf16 as the sum of two, so
-// that what the matrix cores are given is within 2^-16 of x.
-template <bool X_FIRST, typename T>
-__device__ __forceinline__ void mma_f32(f32x16 &acc, const float (&x)[8],
-                                        const Frag<T> &b) {
-  Frag<T> hi;
-  to_frag(hi, x);
-  if (X_FIRST)
-    mma(acc, hi, b);
-  else
-    mma(acc, b, hi);
-  if constexpr (sizeof(T) == 2) {
-    float back[8], rest[8];
-    from_frag(back, hi);
+// Float32 numbers as fragments: of bf16 the sum of PARTS, each the rounded rest
+// of those before it, so that what the matrix cores are given is within
+// 2^(-8 PARTS) of the number (three: as good as itself).  The rest of a pair is
+// x - 1 * hi - 0 * other, a dot product of the two packed numbers with (1, 0),
+// exact, in one instruction where unpacking and subtracting takes two.  (Its
+// constants stay in registers: as an inline constant of the instruction, (-1,
+// 0) was read as something else.)
+template <typename T, int PARTS>
+struct Parts {
+  static constexpr int kParts = sizeof(T) == 2 ? PARTS : 1;
+  Frag<T> f[kParts];
+
+  __device__ __forceinline__ void set(float (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rest[i] = x[i] - back[i];
-    Frag<T> lo;
-    to_frag(lo, rest);
-    if (X_FIRST)
-      mma(acc, lo, b);
-    else
-      mma(acc, b, lo);
+    for (int a = 0; a < kParts; ++a) {
+      to_frag(f[a], x);
+      if constexpr (sizeof(T) == 2) {
+        if (a + 1 == kParts) break;
+        uint32_t first = 0x0000bf80u, second = 0xbf800000u;
+        asm("" : "+s"(first), "+s"(second));
+        const Vec v = __builtin_bit_cast(Vec, f[a].v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x2 hi = __builtin_bit_cast(bf16x2, v.w[i]);
+          x[2 * i] = __builtin_amdgcn_fdot2_f32_bf16(
+              hi, __builtin_bit_cast(bf16x2, first), x[2 * i], false);
+          x[2 * i + 1] = __builtin_amdgcn_fdot2_f32_bf16(
+              hi, __builtin_bit_cast(bf16x2, second), x[2 * i + 1], false);
+        }
+      }
+    }
   }
+};
+
+template <typename T, int PARTS>
+__device__ __forceinline__ void mma(f32x16 &acc, const Parts<T, PARTS> &a,
+                                    const Frag<T> &b) {
+#pragma unroll
+  for (int i = 0; i < Parts<T, PARTS>::kParts; ++i) mma(acc, a.f[i], b);
+}
+template <typename T, int PARTS>
+__device__ __forceinline__ void mma(f32x16 &acc, const Frag<T> &a,
+                                    const Parts<T, PARTS> &b) {
+#pragma unroll
+  for (int i = 0; i < Parts<T, PARTS>::kParts; ++i) mma(acc, a, b.f[i]);
 }
 
 // ----------------------------------------------------------- tiles in LDS
 
-// A stage's tokens of one tensor, in units of four elements; unit u of token
-// r stands at u ^ turn(r), so that the units which 16 lanes read at a time (8
-// for f32), of as many rows or of four rows (two) beside each other, lie in
-// distinct banks.
+typedef __attribute__((address_space(3))) char lds_char;
+
+// 16 bytes per lane from memory to LDS at `lds` + 16 * lane: a wave-uniform
+// base and a 32-bit offset per lane.  The compiler does not see these loads:
+// arrive() waits for them.  (m0 takes the LDS address; the s_nop is the wait
+// state that the ISA asks for between writing m0 and a load to LDS.)
+__device__ __forceinline__ void dma(uint32_t lds, const void *base,
+                                    uint32_t offset) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(offset), "s"(base)
+      : "memory", "m0");
+}
+
+// Everything that this wavefront has under way has landed, then that of every
+// wavefront.
+__device__ __forceinline__ void arrive() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The 32 tokens of a chunk of one tensor, a row of kPieces pieces of 16 bytes
+// each.  Piece c of token r stands at c ^ turn(r), so that the rows which a
+// read takes together lie in distinct banks: 16 rows of 8 bytes, four rows of
+// 32 (a transposing read), or of f32 8 rows of 16 bytes, two of 128.  The loads
+// apply the turn to the addresses that they read from.  A turn's bits are the
+// pieces' own, so a lane's place for block b or columns 32 m is that for the
+// first by an exclusive or.
 template <typename T, int DP>
 struct Tile {
+  static constexpr bool kHalf = sizeof(T) == 2;
   static constexpr int E = Elems<T>::value;
-  static constexpr int kTokens = sizeof(T) == 2 ? 64 : 32;
-  static constexpr int kUnit = 4 * sizeof(T);
-  static constexpr int kUnits = sizeof(T) == 2 ? (DP <= 32   ? 8
-                                                  : DP <= 64 ? 16
-                                                             : 32)
-                                               : (DP <= 64 ? 16 : 32);
-  static constexpr int kBytes = kTokens * kUnits * kUnit;
   static constexpr int kRowVecs = DP / E;
-  static constexpr int kVecs = kTokens * kRowVecs;
+  static constexpr int kPieces = kHalf ? (DP <= 32   ? 4
+                                          : DP <= 64 ? 8
+                                                     : 16)
+                                       : (DP <= 64 ? 16 : 32);
+  static constexpr int kPitch = kPieces * 16;
+  static constexpr int kBytes = kChunk * kPitch;
+  static constexpr int kCols = kHalf ? 2 : 4;  // places of a column read
 
   static __device__ __forceinline__ int turn(int r) {
-    if (sizeof(T) == 4) return ((r >> 2 & 1) << 3) | (r & 3);
-    if (kUnits == 32) return ((r & 3) << 2) | (r >> 2 & 3);
-    if (kUnits == 16) return ((r >> 1 & 3) << 2) | (r >> 3 & 1);
+    if (!kHalf) return ((r >> 2 & 1) << 3) | (r & 3);
+    if (kPieces == 16) return ((r & 3) << 2) | (r >> 2 & 3);
+    if (kPieces == 8) return ((r >> 1 & 1) << 2) | (r >> 2 & 3);
     return r >> 2 & 3;
   }
-  static __device__ __forceinline__ char *at(char *tile, int r, int u) {
-    return tile + (r * kUnits + (u ^ turn(r))) * kUnit;
+  // the lane's place in rows()
+  static __device__ __forceinline__ int row_place() {
+    const int r = lane_id() % 32, h = half_of();
+    return kHalf ? r * kPitch + turn(r) * 16 + h * 8
+                 : r * kPitch + (turn(r) ^ h) * 16;
   }
-  static __device__ __forceinline__ const char *at(const char *tile, int r,
-                                                   int u) {
-    return tile + (r * kUnits + (u ^ turn(r))) * kUnit;
-  }
-  // vector j of token r
-  static __device__ __forceinline__ void put(char *tile, int r, int j,
-                                             const Vec &v) {
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<uint2 *>(at(tile, r, 2 * j)) =
-          make_uint2(v.w[0], v.w[1]);
-      *reinterpret_cast<uint2 *>(at(tile, r, 2 * j + 1)) =
-          make_uint2(v.w[2], v.w[3]);
-    } else {
-      store_vec(at(tile, r, j), v);
-    }
-  }
-  // Tokens r0 + lane % 32, features 16 b + slot(i).
-  static __device__ __forceinline__ Frag<T> rows(const char *tile, int r0,
-                                                 int b) {
-    const int r = r0 + lane_id() % 32, u = 4 * b + half_of();
+  // Token lane % 32, features 16 b + slot(i).
+  static __device__ __forceinline__ Frag<T> rows(const lds_char *tile,
+                                                 int place, int b) {
     Frag<T> f;
-    if constexpr (sizeof(T) == 2) {
-      const uint2 x = *reinterpret_cast<const uint2 *>(at(tile, r, u));
-      const uint2 y = *reinterpret_cast<const uint2 *>(at(tile, r, u + 2));
-      const u32x4 v = {x.x, x.y, y.x, y.y};
+    if constexpr (kHalf) {
+      typedef __attribute__((address_space(3))) const s16x4 lds_s16x4;
+      const s16x4 x = *(lds_s16x4 *)(tile + (place ^ (32 * b)));
+      const s16x4 y = *(lds_s16x4 *)(tile + (place ^ (32 * b) ^ 16));
+      const s16x8 v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
       f.v = __builtin_bit_cast(bf16x8, v);
     } else {
-      const Vec x = load_vec(at(tile, r, u)), y = load_vec(at(tile, r, u + 2));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f.v[i] = elem<float>(x, i);
-        f.v[4 + i] = elem<float>(y, i);
-      }
+      typedef float f32x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) const f32x4 lds_f4;
+      const f32x4 x = *(lds_f4 *)(tile + (place ^ (64 * b)));
+      const f32x4 y = *(lds_f4 *)(tile + (place ^ (64 * b) ^ 32));
+      f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return f;
   }
-  // Features c0 + lane % 32, tokens r0 + slot(i).
-  static __device__ __forceinline__ Frag<T> cols(const char *tile, int r0,
-                                                 int c0) {
-    const int l = lane_id();
+  // the lane's places in cols()
+  static __device__ __forceinline__ void col_places(int (&place)[kCols]) {
+    const int l = lane_id(), h = half_of();
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) {
+      if (kHalf) {
+        // 16 lanes read four tokens of 16 features, and get a feature's four
+        // tokens each
+        const int r = 8 * x + 4 * h + (l % 16) / 4;
+        const int c = (l >> 4 & 1) * 2 + (l >> 1 & 1);
+        place[x] = r * kPitch + (c ^ turn(r)) * 16 + (l & 1) * 8;
+      } else {
+        const int r = 4 * h + x;
+        place[x] = r * kPitch + ((l % 32 / 4) ^ turn(r)) * 16 + l % 4 * 4;
+      }
+    }
+  }
+  // Feature 32 m + lane % 32, tokens 16 j + slot(i).
+  static __device__ __forceinline__ Frag<T> cols(const lds_char *tile,
+                                                 const int (&place)[kCols],
+                                                 int j, int m) {
     Frag<T> f;
-    if constexpr (sizeof(T) == 2) {
-      // 16 lanes read four tokens of 16 features, and get a feature's four
-      // tokens each
-      const int r = r0 + 4 * half_of() + (l % 16) / 4;
-      const int u = c0 / 4 + (l >> 4 & 1) * 4 + (l & 3);
+    if constexpr (kHalf) {
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const s16x4 lo =
-          __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at(tile, r, u));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4 *)(tile + (place[0] ^ (64 * m)) + 16 * j * kPitch));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4 *)at(tile, r + 8, u));
+          (lds_s16x4 *)(tile + (place[1] ^ (64 * m)) + 16 * j * kPitch));
       const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       f.v = __builtin_bit_cast(bf16x8, v);
     } else {
-      const int c = c0 + l % 32;
+      typedef __attribute__((address_space(3))) const float lds_float;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        f.v[i] = *reinterpret_cast<const float *>(
-            at(tile, r0 + slot(i), c / 4) + c % 4 * 4);
+        f.v[i] = *(lds_float *)(tile + (place[i % 4] ^ (128 * m)) +
+                                (16 * j + 8 * (i / 4)) * kPitch);
     }
     return f;
   }
@@ -291,37 +338,47 @@ __device__ __forceinline__ float decay_of(const Lin &p, int h) {
   return g < -1e30f ? -1e30f : g;
 }
 
-// Registers for one stage of NT tensors, vectors of THREADS threads.
+// Chunks of NT tensors on their way to LDS, two at a time: one being worked
+// on, the next one's loads in flight.
 template <typename T, int DP, int NT, int THREADS>
-struct Loads {
+struct Chunks {
   typedef Tile<T, DP> Tl;
-  static constexpr int kPer = Tl::kVecs / THREADS;
-  Vec v[NT][kPer];
+  static constexpr int kSet = NT * Tl::kBytes;
+  static constexpr int kAll = kChunk * Tl::kPieces;
+  lds_char *lds;  // two sets of NT tiles
 
-  // n >= 1 tokens from `start`; what lies past them or past the features is
-  // read from the last one that exists, and cleared on its way to LDS
-  __device__ __forceinline__ void load(const Part (&in)[NT], int64_t start,
-                                       int n, int nvec) {
-#pragma unroll
-    for (int a = 0; a < NT; ++a)
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int x = threadIdx.x + i * THREADS;
-        const int r = min(x / Tl::kRowVecs, n - 1);
-        const int j = min(x % Tl::kRowVecs, nvec - 1);
-        v[a][i] = load_vec(in[a].data + ((start + r) * in[a].token + j) * 16);
-      }
+  // Pieces that no load fills hold zeros: features past the head's, and tokens
+  // past the end.
+  __device__ __forceinline__ void clear_all() const {
+    for (int x = threadIdx.x; x < 2 * kSet / 16; x += THREADS)
+      *(__attribute__((address_space(3))) u32x4 *)(lds + x * 16) =
+          u32x4{0, 0, 0, 0};
   }
-  __device__ __forceinline__ void put(char *tiles, int n, int nvec) const {
+  // n tokens from `start` into set `buf`, which nobody reads any more.
+  __device__ __forceinline__ void load(const Part (&in)[NT], int64_t start,
+                                       int n, int nvec, int buf) const {
+    if (n < kChunk) {
 #pragma unroll
-    for (int a = 0; a < NT; ++a)
+      for (int a = 0; a < NT; ++a)
+        for (int x = n * Tl::kPieces + threadIdx.x; x < kAll; x += THREADS)
+          *(__attribute__((address_space(3))) u32x4 *)(
+              lds + buf * kSet + a * Tl::kBytes + x * 16) = u32x4{0, 0, 0, 0};
+    }
+    const uint32_t wave = wave_id() * kWave;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int x = threadIdx.x + i * THREADS;
-        const int r = x / Tl::kRowVecs, j = x % Tl::kRowVecs;
-        Tl::put(tiles + a * Tl::kBytes, r, j,
-                r < n && j < nvec ? v[a][i] : vzero());
-      }
+    for (int i = 0; i < (kAll + THREADS - 1) / THREADS; ++i) {
+      if (kAll % THREADS != 0 && wave + i * THREADS >= kAll) break;
+      const int x = threadIdx.x + i * THREADS;
+      const int r = x / Tl::kPieces;
+      const int c = (x % Tl::kPieces) ^ Tl::turn(r);
+      if (r >= n || c >= nvec) continue;
+#pragma unroll
+      for (int a = 0; a < NT; ++a)
+        dma((uint32_t)(uintptr_t)lds + buf * kSet + a * Tl::kBytes +
+                (wave + i * THREADS) * 16,
+            in[a].data + start * in[a].token * 16,
+            ((uint32_t)r * (uint32_t)in[a].token + c) * 16);
+    }
   }
 };
 
@@ -363,13 +420,14 @@ struct State {
   }
 };
 
-// The powers of the decay that a chunk of n tokens needs, forward (REV: from
-// the last token to the first; then the state has c in it).
+// The powers of the decay on the way of a chunk's tokens into the state:
+// token 16 j + slot(i), of n.  (REV, from the last token to the first: the
+// state is a gradient's, with c in it.)
 template <bool REV>
 struct Powers {
-  float own;      // of the state, for the lane's token
-  float add[16];  // of token 16 j + slot(i) on its way into the state
-  float over;     // of the state over the chunk
+  float add[16];
+  float own;   // of the state, for the lane's token
+  float over;  // of the state over the chunk
   int n = 0;
 
   // (only a sequence's last chunk has less than 32: one of the two ends)
@@ -387,76 +445,78 @@ struct Powers {
   }
 };
 
-// The state over one chunk of 32 tokens from token r0 of the stage.
+// S += sum over the chunk's tokens of k (add w v)^T.  The decayed v enters as
+// three bf16: the state may be asked for in float32.
 template <typename T, int DP, bool REV>
-__device__ __forceinline__ void advance(State<DP> &S, const char *K,
-                                        const Frag<T> (&v)[2], int r0,
-                                        const Powers<REV> &pw) {
-  float x[2][8];
+__device__ __forceinline__ void gather(
+    State<DP> &S, const lds_char *K, const int (&place)[Tile<T, DP>::kCols],
+    const Frag<T> (&v)[2], const Powers<REV> &pw, float w) {
+  Parts<T, 3> x[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    from_frag(x[j], v[j]);
+    float y[8];
+    from_frag(y, v[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[j][i] *= pw.add[8 * j + i];
+    for (int i = 0; i < 8; ++i) y[i] *= pw.add[8 * j + i] * w;
+    x[j].set(y);
   }
 #pragma unroll
-  for (int m = 0; m < DP / 32; ++m) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) S.s[m][r] *= pw.over;
+  for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      mma_f32<false>(S.s[m], x[j], Tile<T, DP>::cols(K, r0 + 16 * j, 32 * m));
-  }
+      mma(S.s[m], Tile<T, DP>::cols(K, place, j, m), x[j]);
 }
 
 // What each stretch adds to the state (from zero): S of its own tokens, at the
-// place of the state that the next one starts from.
+// place of the state that the next one starts from.  It walks the stretch the
+// other way round than the pass behind it does, so that this one finds what
+// was read last in the caches.
 template <typename T, int DP, bool REV>
 __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) {
   typedef Tile<T, DP> Tl;
-  constexpr int kThreads = 2 * DP;
-  __shared__ __align__(1024) char tiles[2 * Tl::kBytes];
+  typedef Chunks<T, DP, 2, 2 * DP> Ch;
+  __shared__ __align__(1024) char tiles[2 * Ch::kSet];
+  const Ch ch = {(lds_char *)tiles};
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
   if (REV ? st.head : st.tail) return;  // nobody starts from its end
-  const Part in[2] = {
-      {p.in[0].data + (st.batch * p.in[0].batch + (int64_t)h * p.in[0].head) * 16,
-       0, p.in[0].token, 0},
-      {p.in[1].data + (st.batch * p.in[1].batch + (int64_t)h * p.in[1].head) * 16,
-       0, p.in[1].token, 0}};
+  Part in[2] = {p.in[0], p.in[1]};
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+    in[a].data += (st.batch * in[a].batch + (int64_t)h * in[a].head) * 16;
   const float g = decay_of(p, h);
-  const int c0 = 32 * wave_id();
+  int place[Tl::kCols], place_v[Tl::kCols];
+  Tl::col_places(place);
+#pragma unroll
+  for (int x = 0; x < Tl::kCols; ++x)
+    place_v[x] = place[x] ^ (wave_id() * (Tl::kHalf ? 64 : 128));
   State<DP> S;
   S.clear();
   Powers<REV> pw;
-  Loads<T, DP, 2, kThreads> ld;
-  const int stages = (st.n + Tl::kTokens - 1) / Tl::kTokens;
-  auto from = [&](int i) { return (REV ? stages - 1 - i : i) * Tl::kTokens; };
-  if (stages > 0)
-    ld.load(in, st.start + from(0), min(Tl::kTokens, st.n - from(0)), p.nvec);
-  for (int i = 0; i < stages; ++i) {
-    const int n = min(Tl::kTokens, st.n - from(i));
+  const int chunks = (st.n + kChunk - 1) / kChunk;
+  auto from = [&](int i) { return (REV ? i : chunks - 1 - i) * kChunk; };
+  auto load = [&](int i) {
+    ch.load(in, st.start + from(i), min(kChunk, st.n - from(i)), p.nvec, i & 1);
+  };
+  if (p.nvec < Tl::kRowVecs) {
+    ch.clear_all();
     __syncthreads();
-    ld.put(tiles, n, p.nvec);
-    __syncthreads();
-    if (i + 1 < stages)
-      ld.load(in, st.start + from(i + 1),
-              min(Tl::kTokens, st.n - from(i + 1)), p.nvec);
-#pragma unroll
-    for (int c = 0; c < Tl::kTokens / kChunk; ++c) {
-      const int r0 = REV ? Tl::kTokens - kChunk * (c + 1) : kChunk * c;
-      const int left = n - r0;
-      if (left <= 0) continue;
-      pw.set(g, p.scale, min(left, kChunk));
-      Frag<T> v[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        v[j] = Tl::cols(tiles + Tl::kBytes, r0 + 16 * j, c0);
-      advance<T, DP, REV>(S, tiles, v, r0, pw);
-    }
   }
-  S.store(p.states + job * p.d * p.d, p.d, c0);
+  if (chunks > 0) load(0);
+  for (int i = 0; i < chunks; ++i) {
+    const int n = min(kChunk, st.n - from(i));
+    arrive();
+    if (i + 1 < chunks) load(i + 1);
+    pw.set(g, p.scale, n);
+    const float w = exp2f(g * (REV ? from(i) : st.n - from(i) - n));
+    const lds_char *K = ch.lds + (i & 1) * Ch::kSet, *V = K + Tl::kBytes;
+    Frag<T> v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[j] = Tl::cols(V, place_v, j, 0);
+    gather<T, DP, REV>(S, K, place, v, pw, w);
+  }
+  S.store(p.states + job * p.d * p.d, p.d, 32 * wave_id());
 }
 
 // Along each sequence: states[j] = the state before stretch j.
@@ -506,14 +566,20 @@ __global__ __launch_bounds__(2 * DP * ROLES,
   constexpr int kWaves = kThreads / kWave;
   constexpr int kPitch = 36 * sizeof(T);  // of a token's 32 outputs in LDS
   constexpr int E = Elems<T>::value;
-  __shared__ __align__(1024) char tiles[NT * Tl::kBytes];
-  __shared__ __align__(16) char outs[kWaves][kChunk * kPitch];
+  typedef Chunks<T, DP, NT, kThreads> Ch;
+  __shared__ __align__(1024) char tiles[2 * Ch::kSet];
+  // f32: 16 bytes a lane as they stand, for which LDS has no room beside two
+  // sets of tiles anyway
+  __shared__ __align__(16) char outs[kWaves][Tl::kHalf ? kChunk * kPitch : 16];
+  float kept[Tl::kHalf ? 1 : 16];
+  const Ch ch = {(lds_char *)tiles};
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
   const int wave = wave_id(), lane = lane_id();
   const int role = ROLES == 1 ? 0 : wave / (DP / 32);
-  const int c0 = 32 * (ROLES == 1 ? wave : wave % (DP / 32));
+  const int m0 = ROLES == 1 ? wave : wave % (DP / 32);
+  const int c0 = 32 * m0;
   Part in[NT];
 #pragma unroll
   for (int a = 0; a < NT; ++a) {
@@ -523,11 +589,18 @@ __global__ __launch_bounds__(2 * DP * ROLES,
   const Part out = p.out[role];
   char *dst = const_cast<char *>(out.data) +
               (st.batch * out.batch + (int64_t)h * out.head) * 16;
-  const char *Q = tiles + (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
-  const char *K = tiles + (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
-  const char *V = tiles + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
   const float g = decay_of(p, h);
   const int64_t dd = (int64_t)p.d * p.d;
+  const int chunks = (st.n + kChunk - 1) / kChunk;
+  auto from = [&](int i) { return (REV ? chunks - 1 - i : i) * kChunk; };
+  auto load = [&](int i) {
+    ch.load(in, st.start + from(i), min(kChunk, st.n - from(i)), p.nvec, i & 1);
+  };
+  if (p.nvec < Tl::kRowVecs) {
+    ch.clear_all();
+    __syncthreads();
+  }
+  if (chunks > 0) load(0);
   State<DP> S;
   const float *src = p.states != nullptr ? p.states + job * dd
                      : p.init != nullptr
@@ -546,83 +619,107 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     near[r] = e >= 0 ? p.scale * exp2f(g * e) : 0.f;
   }
   Powers<REV> pw;
-  Loads<T, DP, NT, kThreads> ld;
-  const int stages = (st.n + Tl::kTokens - 1) / Tl::kTokens;
-  auto from = [&](int i) { return (REV ? stages - 1 - i : i) * Tl::kTokens; };
-  if (stages > 0)
-    ld.load(in, st.start + from(0), min(Tl::kTokens, st.n - from(0)), p.nvec);
-  for (int i = 0; i < stages; ++i) {
-    const int n = min(Tl::kTokens, st.n - from(i));
-    __syncthreads();
-    ld.put(tiles, n, p.nvec);
-    __syncthreads();
-    if (i + 1 < stages)
-      ld.load(in, st.start + from(i + 1),
-              min(Tl::kTokens, st.n - from(i + 1)), p.nvec);
+  const int row = Tl::row_place();
+  int place[Tl::kCols], place_v[Tl::kCols];
+  Tl::col_places(place);
 #pragma unroll
-    for (int c = 0; c < Tl::kTokens / kChunk; ++c) {
-      const int r0 = REV ? Tl::kTokens - kChunk * (c + 1) : kChunk * c;
-      const int left = n - r0;
-      if (left <= 0) continue;
-      pw.set(g, p.scale, min(left, kChunk));
-      // scores (rows s, columns t) and the state's part, in one pass over q
-      f32x16 a = {}, o = {};
-#pragma unroll
-      for (int b = 0; b < DP / 16; ++b) {
-        const Frag<T> q = Tl::rows(Q, r0, b);
-        mma(a, Tl::rows(K, r0, b), q);
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = S.s[b / 2][8 * (b % 2) + e];
-        mma_f32<true>(o, x, q);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[r] *= pw.own;
-      Frag<T> v[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        v[j] = Tl::cols(V, r0 + 16 * j, c0);
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = a[8 * j + e] * near[8 * j + e];
-        mma_f32<false>(o, x, v[j]);
-      }
-      advance<T, DP, REV>(S, K, v, r0, pw);
-      // o: rows are features, the lane's column its token; through LDS into
-      // rows of 32 features
+  for (int x = 0; x < Tl::kCols; ++x)
+    place_v[x] = place[x] ^ (m0 * (Tl::kHalf ? 64 : 128));
+  // the wavefront's outputs of a chunk, kept in LDS until the next one's loads
+  // are awaited: so a store has a chunk's time to complete
+  auto store = [&](int i) {
+    constexpr int kRow = 32 / E;  // vectors of 32 features
+    const int n = min(kChunk, st.n - from(i));
+    if constexpr (!Tl::kHalf) {
+      const int t = lane % 32;
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
-        char *at = outs[wave] + (lane % 32) * kPitch +
-                   (16 * (r / 8) + slot(r % 8)) * sizeof(T);
-        if constexpr (sizeof(T) == 2) {
-          const float x[8] = {o[r], o[r + 1], o[r + 2], o[r + 3], 0, 0, 0, 0};
-          const Vec y = pack<bf16>(x);
-          *reinterpret_cast<uint2 *>(at) = make_uint2(y.w[0], y.w[1]);
-        } else {
-          *reinterpret_cast<float4 *>(at) =
-              make_float4(o[r], o[r + 1], o[r + 2], o[r + 3]);
-        }
+        const int j = (c0 + 16 * (r / 8) + slot(r % 8)) / 4;
+        const float x[4] = {kept[r], kept[r + 1], kept[r + 2], kept[r + 3]};
+        if (t < n && j < p.nvec)
+          store_vec(dst + ((st.start + from(i) + t) * out.token + j) * 16,
+                    pack<float>(x));
       }
-      __builtin_amdgcn_wave_barrier();
-      constexpr int kRow = 32 / E;  // vectors of 32 features
-#pragma unroll
-      for (int x = lane; x < kChunk * kRow; x += kWave) {
-        const int t = x / kRow, j = x % kRow;
-        Vec y;
-        const uint2 *from_lds = reinterpret_cast<const uint2 *>(
-            outs[wave] + t * kPitch + j * 16);
-        const uint2 lo = from_lds[0], hi = from_lds[1];
-        y.w[0] = lo.x;
-        y.w[1] = lo.y;
-        y.w[2] = hi.x;
-        y.w[3] = hi.y;
-        if (t < left && c0 / E + j < p.nvec)
-          store_vec(dst + ((st.start + from(i) + r0 + t) * out.token + c0 / E +
-                           j) * 16,
-                    y);
-      }
-      __builtin_amdgcn_wave_barrier();
+      return;
     }
+#pragma unroll
+    for (int x = lane; x < kChunk * kRow; x += kWave) {
+      const int t = x / kRow, j = x % kRow;
+      Vec y;
+      const uint2 *from_lds =
+          reinterpret_cast<const uint2 *>(outs[wave] + t * kPitch + j * 16);
+      const uint2 lo = from_lds[0], hi = from_lds[1];
+      y.w[0] = lo.x;
+      y.w[1] = lo.y;
+      y.w[2] = hi.x;
+      y.w[3] = hi.y;
+      if (t < n && c0 / E + j < p.nvec)
+        store_vec(dst + ((st.start + from(i) + t) * out.token + c0 / E + j) * 16,
+                  y);
+    }
+  };
+  for (int i = 0; i < chunks; ++i) {
+    arrive();
+    if (i > 0) store(i - 1);
+    if (i + 1 < chunks) load(i + 1);
+    pw.set(g, p.scale, min(kChunk, st.n - from(i)));
+    const lds_char *tile = ch.lds + (i & 1) * Ch::kSet;
+    const lds_char *Q =
+        tile + (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
+    const lds_char *K =
+        tile + (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
+    const lds_char *V =
+        tile + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
+    // scores (rows s, columns t) and the state's part, in one pass over q
+    f32x16 a = {}, o = {};
+#pragma unroll
+    for (int b = 0; b < DP / 16; ++b) {
+      const Frag<T> q = Tl::rows(Q, row, b);
+      mma(a, Tl::rows(K, row, b), q);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = S.s[b / 2][8 * (b % 2) + e];
+      Parts<T, 2> y;
+      y.set(x);
+      mma(o, y, q);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[r] *= pw.own;
+    Frag<T> v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v[j] = Tl::cols(V, place_v, j, 0);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = a[8 * j + e] * near[8 * j + e];
+      Parts<T, 2> y;
+      y.set(x);
+      mma(o, v[j], y);
+    }
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S.s[m][r] *= pw.over;
+    gather<T, DP, REV>(S, K, place, v, pw, 1.f);
+    // o: rows are features, the lane's column its token
+    if constexpr (Tl::kHalf) {
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const float x[8] = {o[r], o[r + 1], o[r + 2], o[r + 3], 0, 0, 0, 0};
+        const Vec y = pack<bf16>(x);
+        *reinterpret_cast<uint2 *>(
+            outs[wave] + (lane % 32) * kPitch +
+            (16 * (r / 8) + slot(r % 8)) * sizeof(T)) =
+            make_uint2(y.w[0], y.w[1]);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) kept[r] = o[r];
+    }
+  }
+  if (chunks > 0) {
+    __builtin_amdgcn_wave_barrier();
+    store(chunks - 1);
   }
   if (p.final != nullptr && role == 0 && (REV ? st.head : st.tail))
     S.store(p.final + ((int64_t)st.seq * p.H + h) * dd, p.d, c0);
@@ -726,7 +823,6 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 // three times, is the traffic of some 200 tokens.
 constexpr int64_t kFill = 2 * kCUs;
 constexpr int64_t kShort = 128;
-constexpr int64_t kStage = 64;  // stretches are whole stages of either type
 
 // false: more stretches than can be numbered.
 bool make_stretches(Stretches &m, const int64_t *off, int64_t nseg, int64_t B,
@@ -734,7 +830,7 @@ bool make_stretches(Stretches &m, const int64_t *off, int64_t nseg, int64_t B,
   m = Stretches{};
   const int64_t tokens = off != nullptr ? (nseg > 0 ? off[nseg] : 0) : B * N;
   int64_t len = std::max(kShort, tokens * H / kFill);
-  len = (len + kStage - 1) / kStage * kStage;
+  len = (len + kChunk - 1) / kChunk * kChunk;
   m.N = N;
   m.len = len;
   if (off == nullptr) {
@@ -822,6 +918,17 @@ hipError_t make_states(const Lin &p, const Stretches &m, int64_t sequences,
   return hipLaunchKernel((const void *)scan_kernel<REV>,
                          dim3((unsigned)(sequences * p.H * blocks)),
                          dim3(kBlock), argv, 0, s);
+}
+
+// Offsets within a chunk are 32 bits.
+int check_part(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
+               int64_t d, int dtype, bool output, const char *name) {
+  ADALN_TRY(check_heads(t, B, N, H, d, dtype, output, name));
+  if (t != nullptr && B * N * H > 0 && N > 1 &&
+      t->token_stride / elems_per_vec(dtype) > (int64_t(1) << 22))
+    return fail(ADALN_ERR_UNSUPPORTED, "%s: tokens more than 64 MiB apart",
+                name);
+  return ADALN_OK;
 }
 
 Part part_of(const adaln_heads_t *t, int64_t B, int64_t N, int64_t H,
@@ -929,10 +1036,10 @@ ADALN_API int adaln_lin_attn_fwd(
     size_t states_size, const int64_t *seg_offsets, int64_t nseg, int64_t B,
     int64_t N, int64_t H, int64_t d, int dtype, void *stream) {
   ADALN_TRY(check_lin(log_decay, scale, seg_offsets, nseg, B, N, H, d, dtype));
-  ADALN_TRY(check_heads(q, B, N, H, d, dtype, false, "q"));
-  ADALN_TRY(check_heads(k, B, N, H, d, dtype, false, "k"));
-  ADALN_TRY(check_heads(v, B, N, H, d, dtype, false, "v"));
-  ADALN_TRY(check_heads(o, B, N, H, d, dtype, true, "o"));
+  ADALN_TRY(check_part(q, B, N, H, d, dtype, false, "q"));
+  ADALN_TRY(check_part(k, B, N, H, d, dtype, false, "k"));
+  ADALN_TRY(check_part(v, B, N, H, d, dtype, false, "v"));
+  ADALN_TRY(check_part(o, B, N, H, d, dtype, true, "o"));
   ADALN_TRY(check_ptr(state, state != nullptr, "state"));
   ADALN_TRY(check_ptr(state_out, state_out != nullptr, "state_out"));
   if (B == 0 || H == 0) return ok();
@@ -981,13 +1088,13 @@ ADALN_API int adaln_lin_attn_bwd(
     const int64_t *seg_offsets, int64_t nseg, int64_t B, int64_t N, int64_t H,
     int64_t d, int dtype, void *stream) {
   ADALN_TRY(check_lin(log_decay, scale, seg_offsets, nseg, B, N, H, d, dtype));
-  ADALN_TRY(check_heads(d_o, B, N, H, d, dtype, false, "do"));
-  ADALN_TRY(check_heads(q, B, N, H, d, dtype, false, "q"));
-  ADALN_TRY(check_heads(k, B, N, H, d, dtype, false, "k"));
-  ADALN_TRY(check_heads(v, B, N, H, d, dtype, false, "v"));
-  ADALN_TRY(check_heads(dq, B, N, H, d, dtype, true, "dq"));
-  ADALN_TRY(check_heads(dk, B, N, H, d, dtype, true, "dk"));
-  ADALN_TRY(check_heads(dv, B, N, H, d, dtype, true, "dv"));
+  ADALN_TRY(check_part(d_o, B, N, H, d, dtype, false, "do"));
+  ADALN_TRY(check_part(q, B, N, H, d, dtype, false, "q"));
+  ADALN_TRY(check_part(k, B, N, H, d, dtype, false, "k"));
+  ADALN_TRY(check_part(v, B, N, H, d, dtype, false, "v"));
+  ADALN_TRY(check_part(dq, B, N, H, d, dtype, true, "dq"));
+  ADALN_TRY(check_part(dk, B, N, H, d, dtype, true, "dk"));
+  ADALN_TRY(check_part(dv, B, N, H, d, dtype, true, "dv"));
   ADALN_TRY(check_ptr(state, state != nullptr, "state"));
   ADALN_TRY(check_ptr(states, states != nullptr, "states"));
   ADALN_TRY(check_ptr(dstate_out, dstate_out != nullptr, "dstate_out"));
@@ -1058,10 +1165,10 @@ ADALN_API int adaln_lin_attn_step(const adaln_heads_t *q,
                                   float *state_out, int64_t B, int64_t H,
                                   int64_t d, int dtype, void *stream) {
   ADALN_TRY(check_lin(log_decay, scale, nullptr, 0, B, 1, H, d, dtype));
-  ADALN_TRY(check_heads(q, B, 1, H, d, dtype, false, "q"));
-  ADALN_TRY(check_heads(k, B, 1, H, d, dtype, false, "k"));
-  ADALN_TRY(check_heads(v, B, 1, H, d, dtype, false, "v"));
-  ADALN_TRY(check_heads(o, B, 1, H, d, dtype, true, "o"));
+  ADALN_TRY(check_part(q, B, 1, H, d, dtype, false, "q"));
+  ADALN_TRY(check_part(k, B, 1, H, d, dtype, false, "k"));
+  ADALN_TRY(check_part(v, B, 1, H, d, dtype, false, "v"));
+  ADALN_TRY(check_part(o, B, 1, H, d, dtype, true, "o"));
   const bool work = B > 0 && H > 0;
   ADALN_TRY(check_ptr(state, work, "state"));
   ADALN_TRY(check_ptr(state_out, work, "state_out"));

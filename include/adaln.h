@@ -445,8 +445,9 @@ int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
  *                the tokens seg_offsets[s] up to seg_offsets[s+1]; state and
  *                state_out are then [nseg,H,d,d].  Read during the call only.
  * d is a multiple of 8 (bf16) or 4 (f32), at most 128; at most 4096 heads; B at
- * most 2^20.  States and sums are float32; of bf16 inputs, what enters a
- * product besides them (scores, decayed values, states) does so as two bf16.
+ * most 2^20; tokens at most 64 MiB apart.  States and sums are float32; of bf16
+ * inputs, what enters a product besides them does so as the sum of two bf16
+ * (scores, states) or three (decayed values on their way into a state).
  * A sequence without tokens hands its state on.  Inputs are finite: one that is
  * not spoils its own and all later tokens' outputs, as the formula has it, and
  * may spoil those of up to 31 tokens before it.
