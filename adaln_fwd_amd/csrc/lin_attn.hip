@@ -136,11 +136,14 @@ __device__ __forceinline__ void mma(f32x16 &acc, const Parts<T, PARTS> &a,
 #pragma unroll
   for (int i = 0; i < Parts<T, PARTS>::kParts; ++i) mma(acc, a.f[i], b);
 }
+// parts: how many of them
 template <typename T, int PARTS>
 __device__ __forceinline__ void mma(f32x16 &acc, const Frag<T> &a,
-                                    const Parts<T, PARTS> &b) {
+                                    const Parts<T, PARTS> &b,
+                                    int parts = PARTS) {
 #pragma unroll
-  for (int i = 0; i < Parts<T, PARTS>::kParts; ++i) mma(acc, a, b.f[i]);
+  for (int i = 0; i < Parts<T, PARTS>::kParts; ++i)
+    if (i < parts) mma(acc, a, b.f[i]);
 }
 
 // ----------------------------------------------------------- tiles in LDS
@@ -162,10 +165,13 @@ __device__ __forceinline__ void dma(uint32_t lds, const void *base,
       : "memory", "m0");
 }
 
-// Everything that this wavefront has under way has landed, then that of every
-// wavefront.
+// Everything that this wavefront has under way but its last LATER loads (loads
+// return in order; with stores among them LATER has to be 0) has landed, then
+// that of every wavefront.
+template <int LATER>
 __device__ __forceinline__ void arrive() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER)
+               : "memory");
 }
 
 // The 32 tokens of a chunk of one tensor, a row of kPieces pieces of 16 bytes
@@ -338,29 +344,41 @@ __device__ __forceinline__ float decay_of(const Lin &p, int h) {
   return g < -1e30f ? -1e30f : g;
 }
 
-// Chunks of NT tensors on their way to LDS, two at a time: one being worked
-// on, the next one's loads in flight.
-template <typename T, int DP, int NT, int THREADS>
+// The same number, but new to the compiler: what a loop computes from it is
+// computed where it is used, an instruction or two, and not kept in registers
+// throughout, where it would push others out (its scratch loads would then wait
+// behind the loads in flight).
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// Chunks of NT tensors on their way to LDS, SETS at a time: one being worked
+// on, the next ones' loads in flight.
+template <typename T, int DP, int NT, int THREADS, int SETS>
 struct Chunks {
   typedef Tile<T, DP> Tl;
   static constexpr int kSet = NT * Tl::kBytes;
   static constexpr int kAll = kChunk * Tl::kPieces;
-  lds_char *lds;  // two sets of NT tiles
+  // loads that every wavefront has of a whole chunk, at least
+  static constexpr int kLoads = NT * (kAll / THREADS);
+  lds_char *lds;  // SETS sets of NT tiles
 
   // Pieces that no load fills hold zeros: features past the head's, and tokens
   // past the end.
   __device__ __forceinline__ void clear_all() const {
-    for (int x = threadIdx.x; x < 2 * kSet / 16; x += THREADS)
+    for (int x = threadIdx.x; x < SETS * kSet / 16; x += THREADS)
       *(__attribute__((address_space(3))) u32x4 *)(lds + x * 16) =
           u32x4{0, 0, 0, 0};
   }
   // n tokens from `start` into set `buf`, which nobody reads any more.
   __device__ __forceinline__ void load(const Part (&in)[NT], int64_t start,
                                        int n, int nvec, int buf) const {
+    const int tid = fresh(threadIdx.x);
     if (n < kChunk) {
 #pragma unroll
       for (int a = 0; a < NT; ++a)
-        for (int x = n * Tl::kPieces + threadIdx.x; x < kAll; x += THREADS)
+        for (int x = n * Tl::kPieces + tid; x < kAll; x += THREADS)
           *(__attribute__((address_space(3))) u32x4 *)(
               lds + buf * kSet + a * Tl::kBytes + x * 16) = u32x4{0, 0, 0, 0};
     }
@@ -368,7 +386,7 @@ struct Chunks {
 #pragma unroll
     for (int i = 0; i < (kAll + THREADS - 1) / THREADS; ++i) {
       if (kAll % THREADS != 0 && wave + i * THREADS >= kAll) break;
-      const int x = threadIdx.x + i * THREADS;
+      const int x = tid + i * THREADS;
       const int r = x / Tl::kPieces;
       const int c = (x % Tl::kPieces) ^ Tl::turn(r);
       if (r >= n || c >= nvec) continue;
@@ -378,6 +396,44 @@ struct Chunks {
                 (wave + i * THREADS) * 16,
             in[a].data + start * in[a].token * 16,
             ((uint32_t)r * (uint32_t)in[a].token + c) * 16);
+    }
+  }
+};
+
+// The chunk's V of one wavefront: its own 32 columns, in two tiles of its own,
+// which take its outputs once V has been read.
+template <typename T, int THREADS>
+struct OwnChunk {
+  typedef Tile<T, 32> Tl;
+  static constexpr int kSet = THREADS / kWave * Tl::kBytes;
+  lds_char *lds;  // the wavefront's in the first set
+
+  __device__ __forceinline__ void clear_all() const {
+    for (int x = lane_id(); x < Tl::kBytes / 16; x += kWave)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        *(__attribute__((address_space(3))) u32x4 *)(lds + b * kSet + x * 16) =
+            u32x4{0, 0, 0, 0};
+  }
+  // vector j0 is its first column's
+  __device__ __forceinline__ void load(const Part &in, int64_t start, int n,
+                                       int nvec, int j0, int buf) const {
+    constexpr int kAll = kChunk * Tl::kPieces;
+    const int lane = fresh(lane_id());
+    if (n < kChunk)
+      for (int x = n * Tl::kPieces + lane; x < kAll; x += kWave)
+        *(__attribute__((address_space(3))) u32x4 *)(lds + buf * kSet +
+                                                     x * 16) =
+            u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kAll / kWave; ++i) {
+      const int x = lane + i * kWave;
+      const int r = x / Tl::kPieces;
+      const int c = j0 + ((x % Tl::kPieces) ^ Tl::turn(r));
+      if (r < n && c < nvec)
+        dma((uint32_t)(uintptr_t)lds + buf * kSet + i * kWave * 16,
+            in.data + start * in.token * 16,
+            ((uint32_t)r * (uint32_t)in.token + c) * 16);
     }
   }
 };
@@ -446,11 +502,12 @@ struct Powers {
 };
 
 // S += sum over the chunk's tokens of k (add w v)^T.  The decayed v enters as
-// three bf16: the state may be asked for in float32.
+// two bf16 on the way to outputs in bf16, as three on the way to a state in
+// float32.
 template <typename T, int DP, bool REV>
 __device__ __forceinline__ void gather(
     State<DP> &S, const lds_char *K, const int (&place)[Tile<T, DP>::kCols],
-    const Frag<T> (&v)[2], const Powers<REV> &pw, float w) {
+    const Frag<T> (&v)[2], const Powers<REV> &pw, float w, int parts) {
   Parts<T, 3> x[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -464,7 +521,7 @@ __device__ __forceinline__ void gather(
   for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      mma(S.s[m], Tile<T, DP>::cols(K, place, j, m), x[j]);
+      mma(S.s[m], Tile<T, DP>::cols(K, place, j, m), x[j], parts);
 }
 
 // What each stretch adds to the state (from zero): S of its own tokens, at the
@@ -474,13 +531,17 @@ __device__ __forceinline__ void gather(
 template <typename T, int DP, bool REV>
 __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) {
   typedef Tile<T, DP> Tl;
-  typedef Chunks<T, DP, 2, 2 * DP> Ch;
-  __shared__ __align__(1024) char tiles[2 * Ch::kSet];
+  // bf16: three sets of chunks.  Little is computed here, and two chunks' loads
+  // in flight hide the memory's latency where one's do not.
+  constexpr int kSets = Tl::kHalf ? 3 : 2;
+  typedef Chunks<T, DP, 2, 2 * DP, kSets> Ch;
+  __shared__ __align__(1024) char tiles[kSets * Ch::kSet];
   const Ch ch = {(lds_char *)tiles};
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
-  if (REV ? st.head : st.tail) return;  // nobody starts from its end
+  // nobody starts from the last one's end
+  if ((REV ? st.head : st.tail) && p.final == nullptr) return;
   Part in[2] = {p.in[0], p.in[1]};
 #pragma unroll
   for (int a = 0; a < 2; ++a)
@@ -497,29 +558,35 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
   const int chunks = (st.n + kChunk - 1) / kChunk;
   auto from = [&](int i) { return (REV ? i : chunks - 1 - i) * kChunk; };
   auto load = [&](int i) {
-    ch.load(in, st.start + from(i), min(kChunk, st.n - from(i)), p.nvec, i & 1);
+    ch.load(in, st.start + from(i), min(kChunk, st.n - from(i)), p.nvec,
+            i % kSets);
   };
   if (p.nvec < Tl::kRowVecs) {
     ch.clear_all();
     __syncthreads();
   }
-  if (chunks > 0) load(0);
+  for (int i = 0; i < min(chunks, kSets - 1); ++i) load(i);
   for (int i = 0; i < chunks; ++i) {
     const int n = min(kChunk, st.n - from(i));
-    arrive();
-    if (i + 1 < chunks) load(i + 1);
+    // (a chunk that is not whole may have fewer loads)
+    if (kSets > 2 && i + 1 < chunks && from(i + 1) + kChunk <= st.n)
+      arrive<(kSets - 2) * Ch::kLoads>();
+    else
+      arrive<0>();
+    if (i + kSets - 1 < chunks) load(i + kSets - 1);
     pw.set(g, p.scale, n);
     const float w = exp2f(g * (REV ? from(i) : st.n - from(i) - n));
-    const lds_char *K = ch.lds + (i & 1) * Ch::kSet, *V = K + Tl::kBytes;
+    const lds_char *K = ch.lds + i % kSets * Ch::kSet, *V = K + Tl::kBytes;
     Frag<T> v[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) v[j] = Tl::cols(V, place_v, j, 0);
-    gather<T, DP, REV>(S, K, place, v, pw, w);
+    gather<T, DP, REV>(S, K, place, v, pw, w, 3);
   }
   S.store(p.states + job * p.d * p.d, p.d, 32 * wave_id());
 }
 
-// Along each sequence: states[j] = the state before stretch j.
+// Along each sequence: states[j] = the state before stretch j, and the state
+// behind the last.
 template <bool REV>
 __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
                                                       int32_t blocks) {
@@ -541,7 +608,7 @@ __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
     float4 *s = reinterpret_cast<float4 *>(
         p.states + ((int64_t)(first + j) * p.H + h) * dd + at);
     const float4 before = run;
-    if (i + 1 < count) {
+    if (i + 1 < count || p.final != nullptr) {
       const float4 own = *s;
       const float over = exp2f(g * (float)min(map.len, tokens - j * map.len));
       run.x = fmaf(run.x, over, own.x);
@@ -551,6 +618,70 @@ __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
     }
     *s = before;
   }
+  if (p.final != nullptr)
+    *reinterpret_cast<float4 *>(p.final + row * dd + at) = run;
+}
+
+template <typename T>
+constexpr int kOutWaves = sizeof(T) == 2 ? 3 : 2;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// a[s][t] = k_s . q_t for 16 tokens each: rows s0 + ..., t0 + ... of the tiles.
+// Lane l has row l % 16 of either operand, and as long as both take the
+// features in the same order, any will do: piece 4 b + l / 16 of block b.
+template <typename T, int DP>
+__device__ __forceinline__ void score(f32x4 &a, const lds_char *K,
+                                      const lds_char *Q, int s0, int t0) {
+  typedef Tile<T, DP> Tl;
+  typedef __attribute__((address_space(3))) const u32x4 lds_u4;
+  const int l = fresh(lane_id());
+  const int s = s0 + l % 16, t = t0 + l % 16;
+#pragma unroll
+  for (int b = 0; b < Tl::kRowVecs / 4; ++b) {
+    const int c = 4 * b + l / 16;
+    const u32x4 k = *(lds_u4 *)(K + s * Tl::kPitch + (c ^ Tl::turn(s)) * 16);
+    const u32x4 q = *(lds_u4 *)(Q + t * Tl::kPitch + (c ^ Tl::turn(t)) * 16);
+    if constexpr (Tl::kHalf) {
+      a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q), a, 0,
+          0, 0);
+    } else {
+      const f32x4 kf = __builtin_bit_cast(f32x4, k),
+                  qf = __builtin_bit_cast(f32x4, q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[i], qf[i], a, 0, 0, 0);
+    }
+  }
+}
+
+// Four scores of token t, s = 4 u + [0, 4), into the tiles of their parts.
+template <typename T>
+__device__ __forceinline__ void put_scores(lds_char *P, float (&x)[8], int t,
+                                           int u) {
+  typedef Tile<T, 32> Sc;
+  if constexpr (Sc::kHalf) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    Parts<T, 2> y;
+    y.set(x);
+    const int at = t * Sc::kPitch + ((u / 2) ^ Sc::turn(t)) * 16 + u % 2 * 8;
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const s16x8 v = __builtin_bit_cast(s16x8, y.f[part].v);
+      *(lds_s16x4 *)(P + part * Sc::kBytes + at) =
+          __builtin_shufflevector(v, v, 0, 1, 2, 3);
+    }
+  } else {
+    typedef __attribute__((address_space(3))) f32x4 lds_f4;
+    const f32x4 v = {x[0], x[1], x[2], x[3]};
+    *(lds_f4 *)(P + t * Sc::kPitch + (u ^ Sc::turn(t)) * 16) = v;
+  }
+}
+
+// What this wavefront has written to LDS is there, then that of every one.
+__device__ __forceinline__ void arrive_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // The outputs of a stretch, from the state before it.  ROLES 1: in = q, k, v.
@@ -559,20 +690,28 @@ __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
 // (bit by role): the states in memory are the transpose of this role's.
 template <typename T, int DP, bool REV, int ROLES>
 __global__ __launch_bounds__(2 * DP * ROLES,
-                             ROLES == 1 ? 2 : 1) void out_kernel(
+                             ROLES == 1 ? kOutWaves<T> : 1) void out_kernel(
     Lin p, Stretches map, int32_t across) {
   typedef Tile<T, DP> Tl;
   constexpr int kThreads = 2 * DP * ROLES, NT = ROLES + 2;
   constexpr int kWaves = kThreads / kWave;
-  constexpr int kPitch = 36 * sizeof(T);  // of a token's 32 outputs in LDS
+  constexpr bool kOwn = Tl::kHalf && ROLES == 1;
+  constexpr int kShared = kOwn ? 2 : NT;  // tensors with a tile for all
   constexpr int E = Elems<T>::value;
-  typedef Chunks<T, DP, NT, kThreads> Ch;
-  __shared__ __align__(1024) char tiles[2 * Ch::kSet];
-  // f32: 16 bytes a lane as they stand, for which LDS has no room beside two
-  // sets of tiles anyway
-  __shared__ __align__(16) char outs[kWaves][Tl::kHalf ? kChunk * kPitch : 16];
+  typedef Chunks<T, DP, kShared, kThreads, 2> Ch;
+  typedef OwnChunk<T, kThreads> Own;
+  __shared__ __align__(1024) char tiles[2 * Ch::kSet + (kOwn ? 2 * Own::kSet : 0)];
+  // outputs on their way out (f32: 16 bytes a lane as they stand, for which
+  // LDS has no room beside two sets of tiles anyway)
+  __shared__ __align__(16) char outs[Tl::kHalf && !kOwn ? kWaves : 1][kOwn || !Tl::kHalf ? 16 : kChunk * 64];
+  // the scores, decayed, in two parts: rows are the tokens t, 32 scores each
+  typedef Tile<T, 32> Sc;
+  constexpr int kScParts = Parts<T, 2>::kParts;
+  __shared__ __align__(1024) char scores[ROLES * kScParts * Sc::kBytes];
   float kept[Tl::kHalf ? 1 : 16];
   const Ch ch = {(lds_char *)tiles};
+  const Own own = {(lds_char *)tiles + 2 * Ch::kSet +
+                   wave_id() * Own::Tl::kBytes};
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
@@ -591,13 +730,25 @@ __global__ __launch_bounds__(2 * DP * ROLES,
               (st.batch * out.batch + (int64_t)h * out.head) * 16;
   const float g = decay_of(p, h);
   const int64_t dd = (int64_t)p.d * p.d;
+  // the one stretch of a sequence also makes the state behind it
+  const int parts = p.states == nullptr ? 3 : 2;
   const int chunks = (st.n + kChunk - 1) / kChunk;
   auto from = [&](int i) { return (REV ? chunks - 1 - i : i) * kChunk; };
+  Part both[kShared];
+#pragma unroll
+  for (int a = 0; a < kShared; ++a) both[a] = in[a];
+  // the block of scores that does not count is never written
+  for (int x = threadIdx.x; x < (int)sizeof scores / 16; x += kThreads)
+    store_vec(scores + x * 16, vzero());
   auto load = [&](int i) {
-    ch.load(in, st.start + from(i), min(kChunk, st.n - from(i)), p.nvec, i & 1);
+    const int n = min(kChunk, st.n - from(i));
+    ch.load(both, st.start + from(i), n, p.nvec, i & 1);
+    if constexpr (kOwn)
+      own.load(in[2], st.start + from(i), n, p.nvec, c0 / E, i & 1);
   };
   if (p.nvec < Tl::kRowVecs) {
     ch.clear_all();
+    if constexpr (kOwn) own.clear_all();
     __syncthreads();
   }
   if (chunks > 0) load(0);
@@ -610,26 +761,47 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     S.load(src, p.d, c0, across >> role & 1);
   else
     S.clear();
-  // powers of the scores: rows are s, the lane's column t
-  float near[16];
+  // Of the 32 x 32 scores of a chunk only those of t >= s (REV: s >= t) count:
+  // of their four blocks of 16 x 16 three, a wavefront of the role each (one
+  // wavefront, or two, take them in turn).
+  constexpr int kTeam = DP / 32;
+  constexpr int kTurns = (2 + kTeam) / kTeam;
+  auto block_s = [](int i) { return REV ? (i > 0) : (i == 2); };
+  auto block_t = [](int i) { return REV ? (i == 2) : (i > 0); };
+  // powers of the lane's scores: s = 4 (lane / 16) + r, t = lane % 16; those
+  // of the block off the diagonal are 16 tokens further apart
+  float near[4], far[4];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int s = 16 * (r / 8) + slot(r % 8), t = lane % 32;
+  for (int r = 0; r < 4; ++r) {
+    const int s = 4 * (lane / 16) + r, t = lane % 16;
     const int e = REV ? s - t : t - s;
     near[r] = e >= 0 ? p.scale * exp2f(g * e) : 0.f;
+    far[r] = p.scale * exp2f(g * (e + 16));
   }
   Powers<REV> pw;
-  const int row = Tl::row_place();
-  int place[Tl::kCols], place_v[Tl::kCols];
-  Tl::col_places(place);
+  const int row0 = Tl::row_place();
+  int place0[Tl::kCols], place_v0[Tl::kCols];
+  Tl::col_places(place0);
+  if constexpr (kOwn) {
+    Own::Tl::col_places(place_v0);
+  } else {
 #pragma unroll
-  for (int x = 0; x < Tl::kCols; ++x)
-    place_v[x] = place[x] ^ (m0 * (Tl::kHalf ? 64 : 128));
+    for (int x = 0; x < Tl::kCols; ++x)
+      place_v0[x] = place0[x] ^ (m0 * (Tl::kHalf ? 64 : 128));
+  }
+  // where 4 outputs of a token stand: 8 bytes, turned for the banks' sake
+  auto out_at = [&](int i, int t, int u) {
+    char *base = kOwn ? tiles + 2 * Ch::kSet + (i & 1) * Own::kSet +
+                            wave * Own::Tl::kBytes
+                      : outs[kOwn ? 0 : wave];
+    return reinterpret_cast<uint2 *>(base + t * 64 + (u ^ (t >> 2 & 3)) * 8);
+  };
   // the wavefront's outputs of a chunk, kept in LDS until the next one's loads
   // are awaited: so a store has a chunk's time to complete
   auto store = [&](int i) {
     constexpr int kRow = 32 / E;  // vectors of 32 features
     const int n = min(kChunk, st.n - from(i));
+    const int lane = fresh(lane_id());
     if constexpr (!Tl::kHalf) {
       const int t = lane % 32;
 #pragma unroll
@@ -646,9 +818,7 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     for (int x = lane; x < kChunk * kRow; x += kWave) {
       const int t = x / kRow, j = x % kRow;
       Vec y;
-      const uint2 *from_lds =
-          reinterpret_cast<const uint2 *>(outs[wave] + t * kPitch + j * 16);
-      const uint2 lo = from_lds[0], hi = from_lds[1];
+      const uint2 lo = *out_at(i, t, 2 * j), hi = *out_at(i, t, 2 * j + 1);
       y.w[0] = lo.x;
       y.w[1] = lo.y;
       y.w[2] = hi.x;
@@ -659,69 +829,99 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     }
   };
   for (int i = 0; i < chunks; ++i) {
-    arrive();
+    arrive<0>();
     if (i > 0) store(i - 1);
     if (i + 1 < chunks) load(i + 1);
     pw.set(g, p.scale, min(kChunk, st.n - from(i)));
+    const int row = fresh(row0), lane = fresh(lane_id());
+    const int score_row = Sc::row_place();
+    int place[Tl::kCols], place_v[Tl::kCols];
+#pragma unroll
+    for (int x = 0; x < Tl::kCols; ++x) {
+      place[x] = fresh(place0[x]);
+      place_v[x] = fresh(place_v0[x]);
+    }
     const lds_char *tile = ch.lds + (i & 1) * Ch::kSet;
     const lds_char *Q =
         tile + (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
     const lds_char *K =
         tile + (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
     const lds_char *V =
-        tile + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
-    // scores (rows s, columns t) and the state's part, in one pass over q
-    f32x16 a = {}, o = {};
+        kOwn ? own.lds + (i & 1) * Own::kSet
+             : tile + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
+    lds_char *P = (lds_char *)scores + role * kScParts * Sc::kBytes;
+#pragma unroll
+    for (int turn = 0; turn < kTurns; ++turn) {
+      const int i3 = m0 + turn * kTeam;
+      if (i3 < 3) {
+        const int s0 = 16 * block_s(i3), t0 = 16 * block_t(i3);
+        f32x4 a = {};
+        score<T, DP>(a, K, Q, s0, t0);
+        // s along the lane's row of the tile: four of them side by side
+        float x[8] = {};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = a[r] * (i3 == 1 ? far[r] : near[r]);
+        const int t = t0 + lane % 16;
+        put_scores<T>(P, x, t, s0 / 4 + lane / 16);
+      }
+    }
+    // the state's part
+    f32x16 o = {};
 #pragma unroll
     for (int b = 0; b < DP / 16; ++b) {
       const Frag<T> q = Tl::rows(Q, row, b);
-      mma(a, Tl::rows(K, row, b), q);
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = S.s[b / 2][8 * (b % 2) + e];
       Parts<T, 2> y;
       y.set(x);
       mma(o, y, q);
+      if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kTeam > 1) {
+      arrive_lds();
+    } else {
+      __builtin_amdgcn_wave_barrier();
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[r] *= pw.own;
     Frag<T> v[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      v[j] = Tl::cols(V, place_v, j, 0);
-      float x[8];
+      if constexpr (kOwn)
+        v[j] = Own::Tl::cols(V, place_v, j, 0);
+      else
+        v[j] = Tl::cols(V, place_v, j, 0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = a[8 * j + e] * near[8 * j + e];
-      Parts<T, 2> y;
-      y.set(x);
-      mma(o, v[j], y);
+      for (int part = 0; part < kScParts; ++part)
+        mma(o, v[j], Sc::rows(P + part * Sc::kBytes, score_row, j));
     }
-#pragma unroll
-    for (int m = 0; m < DP / 32; ++m)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) S.s[m][r] *= pw.over;
-    gather<T, DP, REV>(S, K, place, v, pw, 1.f);
+    __builtin_amdgcn_sched_barrier(0);
     // o: rows are features, the lane's column its token
     if constexpr (Tl::kHalf) {
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const float x[8] = {o[r], o[r + 1], o[r + 2], o[r + 3], 0, 0, 0, 0};
         const Vec y = pack<bf16>(x);
-        *reinterpret_cast<uint2 *>(
-            outs[wave] + (lane % 32) * kPitch +
-            (16 * (r / 8) + slot(r % 8)) * sizeof(T)) =
+        *out_at(i, lane % 32, (16 * (r / 8) + slot(r % 8)) / 4) =
             make_uint2(y.w[0], y.w[1]);
       }
     } else {
 #pragma unroll
       for (int r = 0; r < 16; ++r) kept[r] = o[r];
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S.s[m][r] *= pw.over;
+    gather<T, DP, REV>(S, K, place, v, pw, 1.f, parts);
   }
   if (chunks > 0) {
     __builtin_amdgcn_wave_barrier();
     store(chunks - 1);
   }
-  if (p.final != nullptr && role == 0 && (REV ? st.head : st.tail))
+  if (p.final != nullptr && p.states == nullptr && role == 0)
     S.store(p.final + ((int64_t)st.seq * p.H + h) * dd, p.d, c0);
 }
 
@@ -821,7 +1021,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 // Stretches are long enough that the GPU is filled about twice, and not
 // shorter than 128 tokens: what a stretch adds, its state written and read
 // three times, is the traffic of some 200 tokens.
-constexpr int64_t kFill = 2 * kCUs;
+constexpr int64_t kFill = 3 * kCUs;
 constexpr int64_t kShort = 128;
 
 // false: more stretches than can be numbered.
@@ -1054,6 +1254,7 @@ ADALN_API int adaln_lin_attn_fwd(
   Lin p = lin_of(log_decay, scale, H, d, count, dtype);
   p.init = state;
   p.states = need > 0 ? states : nullptr;
+  p.final = state_out;
   hipError_t e = hipSuccess;
   if (need > 0) {
     p.in[0] = part_of(k, B, N, H, dtype);
@@ -1065,7 +1266,6 @@ ADALN_API int adaln_lin_attn_fwd(
   p.in[1] = part_of(k, B, N, H, dtype);
   p.in[2] = part_of(v, B, N, H, dtype);
   p.out[0] = part_of(o, B, N, H, dtype);
-  p.final = state_out;
   e = dtype == ADALN_BF16 ? run_out<bf16, false, 1>(p, m, 0, s)
                           : run_out<float, false, 1>(p, m, 0, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_fwd launch");
@@ -1137,6 +1337,7 @@ ADALN_API int adaln_lin_attn_bwd(
   if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd dq");
   // dk and dv, from the states' gradients
   p.init = dstate_out;
+  p.final = dstate;
   if (one > 0) {
     p.states = ws;
     p.in[0] = pq;
@@ -1150,7 +1351,6 @@ ADALN_API int adaln_lin_attn_bwd(
   p.in[3] = pdo;
   p.out[0] = part_of(dv, B, N, H, dtype);
   p.out[1] = part_of(dk, B, N, H, dtype);
-  p.final = dstate;
   e = dtype == ADALN_BF16 ? run_out<bf16, true, 2>(p, m, 2, s)
                           : run_out<float, true, 2>(p, m, 2, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd dk, dv");
