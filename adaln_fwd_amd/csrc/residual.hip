@@ -26,7 +26,8 @@ namespace adaln {
 namespace {
 
 constexpr int kThreads = 512;     // most threads of a workgroup
-constexpr int kUnroll = 2;        // rows a lane has in flight
+// Rows a lane takes at a time; the next ones' loads are in flight meanwhile.
+constexpr int unroll_of(bool bwd) { return bwd ? 1 : 2; }
 constexpr int kSumCols = 64;      // of the sum over the partial rows
 constexpr int kSumSlices = 16;
 
@@ -87,10 +88,23 @@ __device__ __forceinline__ void kept(const Residual &p, uint64_t row, int j,
     keep[e] = ((e & 1) ? x[e / 2] >> 16 : x[e / 2] & 0xffffu) < p.limit;
 }
 
-template <typename T, bool DROP, bool BWD, typename Map>
+template <bool STREAM>
+__device__ __forceinline__ Vec load_as(const void *p) {
+  return STREAM ? load_stream(p) : load_vec(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_as(void *p, const Vec &v) {
+  if (STREAM)
+    store_stream(p, v);
+  else
+    store_vec(p, v);
+}
+
+template <typename T, bool DROP, bool BWD, bool STREAM, typename Map>
 __global__ __launch_bounds__(kThreads) void residual_kernel(Residual p,
                                                             Map map) {
   constexpr int E = Elems<T>::value;
+  constexpr int kUnroll = unroll_of(BWD);
   __shared__ float stage[BWD ? kThreads : 1][BWD ? E : 1];
   const int t = threadIdx.x;
   const int slot = t / p.w;
@@ -115,17 +129,29 @@ __global__ __launch_bounds__(kThreads) void residual_kernel(Residual p,
 #pragma unroll
         for (int e = 0; e < E; ++e) g[e] = elem<T>(v, e);
       }
+      // rows n, n + step, ..., kUnroll of them at a time, the next ones' loads
+      // in flight meanwhile
       const int64_t step = (int64_t)bps * p.r;
-      for (int64_t n = (int64_t)k_in * p.r + slot; n < rows;
-           n += kUnroll * step) {
-        Vec a[kUnroll], h[kUnroll];
+      int64_t n = (int64_t)k_in * p.r + slot;
+      Vec a[kUnroll], h[kUnroll];
+      auto load = [&](int64_t from) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-          if (n + u * step >= rows) break;
-          const int64_t at = ((row0 + n + u * step) * p.nvec + j) * 16;
-          a[u] = p.a != nullptr ? load_vec(p.a + at) : vzero();
-          h[u] = p.h != nullptr ? load_vec(p.h + at) : vzero();
+          if (from + u * step >= rows) break;
+          const int64_t at = ((row0 + from + u * step) * p.nvec + j) * 16;
+          a[u] = p.a != nullptr ? load_as<STREAM>(p.a + at) : vzero();
+          h[u] = p.h != nullptr ? load_as<STREAM>(p.h + at) : vzero();
         }
+      };
+      load(n);
+      for (; n < rows; n += kUnroll * step) {
+        Vec av[kUnroll], hv[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          av[u] = a[u];
+          hv[u] = h[u];
+        }
+        load(n + kUnroll * step);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           if (n + u * step >= rows) break;
@@ -135,20 +161,20 @@ __global__ __launch_bounds__(kThreads) void residual_kernel(Residual p,
           float out[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float av = elem<T>(a[u], e);
-            const float hs = DROP ? elem<T>(h[u], e) * p.scale
-                                  : elem<T>(h[u], e);
+            const float x = elem<T>(av[u], e);
+            const float hs = DROP ? elem<T>(hv[u], e) * p.scale
+                                  : elem<T>(hv[u], e);
             // selected, not multiplied by zero: what is dropped leaves
             // nothing behind, be it infinite or no number
             if (BWD) {
-              const float d = DROP ? av * p.scale * g[e] : av * g[e];
+              const float d = DROP ? x * p.scale * g[e] : x * g[e];
               out[e] = !DROP || keep[e] ? d : 0.f;
-              sum[e] += !DROP || keep[e] ? av * hs : 0.f;
+              sum[e] += !DROP || keep[e] ? x * hs : 0.f;
             } else {
-              out[e] = !DROP || keep[e] ? fmaf(g[e], hs, av) : av;
+              out[e] = !DROP || keep[e] ? fmaf(g[e], hs, x) : x;
             }
           }
-          store_vec(p.out + (row * p.nvec + j) * 16, pack<T>(out));
+          store_as<STREAM>(p.out + (row * p.nvec + j) * 16, pack<T>(out));
         }
       }
     }
@@ -243,14 +269,16 @@ Shape shape_of(int64_t D, int dtype) {
 }
 
 // Workgroups of rows.  The forward covers the rows with its grid, four steps
-// of its rows each.  The backward runs as many workgroups as the GPU holds at
-// a time, so that few partial rows of dgate are left to add up.
+// of its rows each.  The backward runs a fixed number of workgroups on every
+// CU, so that few partial rows of dgate are left to add up: a whole number,
+// since the CUs with one more end last (MI355X, 75600 x 5120 bf16: 818
+// workgroups of 320 threads 476-518 us, 1024, four to a CU, 457).
 constexpr int64_t kFwdSteps = 4;
-constexpr int64_t kBwdThreads = int64_t(kCUs) * 1024;
+constexpr int64_t kBwdThreads = 1280;  // of a CU, at most
 
 int64_t most_groups(const Shape &s, bool bwd) {
-  return bwd ? std::max<int64_t>(1, kBwdThreads / (s.threads * s.tiles))
-             : kMaxGrid;
+  if (!bwd) return kMaxGrid;
+  return std::max<int64_t>(1, kCUs * (kBwdThreads / s.threads) / s.tiles);
 }
 
 UniformMap uniform_map(int64_t B, int64_t N, const Shape &s, bool bwd) {
@@ -288,6 +316,8 @@ SegMap seg_map(const int64_t *off, const int32_t *mod, int64_t nseg,
 
 int64_t grid_of(const UniformMap &m) { return (int64_t)m.bps * m.groups; }
 int64_t grid_of(const SegMap &m) { return m.wg_start[m.nseg]; }
+int64_t rows_of(const UniformMap &m) { return (int64_t)m.B * m.N; }
+int64_t rows_of(const SegMap &m) { return m.row_start[m.nseg]; }
 int64_t part_rows(const UniformMap &m) {
   return m.N > 0 ? (int64_t)m.B * m.bps : 0;
 }
@@ -297,15 +327,24 @@ int hip_fail(hipError_t e, const char *what) {
   return fail(ADALN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+// Inputs that another kernel has just written may still lie in the 256 MB
+// Infinity Cache, and the next one finds the output there: up to kCachedBytes
+// read and written a call takes plain accesses, past it the streaming hint.
+constexpr int64_t kCachedBytes = int64_t(192) << 20;
+
 template <typename T, bool BWD, typename Map>
 hipError_t launch_residual(const Residual &p, const Map &map, const Shape &s,
-                           hipStream_t stream) {
+                           int64_t rows, hipStream_t stream) {
   const int64_t grid = grid_of(map);
   if (grid <= 0) return hipSuccess;
   void *argv[] = {(void *)&p, (void *)&map};
-  void (*k)(Residual, Map) = p.rng != nullptr
-                                 ? residual_kernel<T, true, BWD, Map>
-                                 : residual_kernel<T, false, BWD, Map>;
+  const bool stream_hint = rows * s.nvec * 16 * 3 > kCachedBytes;
+  void (*k)(Residual, Map) =
+      p.rng != nullptr
+          ? (stream_hint ? residual_kernel<T, true, BWD, true, Map>
+                         : residual_kernel<T, true, BWD, false, Map>)
+          : (stream_hint ? residual_kernel<T, false, BWD, true, Map>
+                         : residual_kernel<T, false, BWD, false, Map>);
   return hipLaunchKernel((const void *)k, dim3((unsigned)grid, s.tiles),
                          dim3(s.threads), argv, 0, stream);
 }
@@ -334,8 +373,8 @@ int residual_fwd(Residual job, const Map &map, const Shape &s, int dtype,
   job.r = s.r;
   const hipStream_t st = (hipStream_t)stream;
   const hipError_t e = dtype == ADALN_BF16
-                           ? launch_residual<bf16, false>(job, map, s, st)
-                           : launch_residual<float, false>(job, map, s, st);
+                           ? launch_residual<bf16, false>(job, map, s, rows_of(map), st)
+                           : launch_residual<float, false>(job, map, s, rows_of(map), st);
   if (e != hipSuccess) return hip_fail(e, "adaln_residual_fwd launch");
   return ok();
 }
@@ -372,8 +411,8 @@ int residual_bwd(Residual job, const Map &map, const Shape &s, float *dgate,
     job.part = direct(map) ? dgate : static_cast<float *>(workspace);
   }
   hipError_t e = dtype == ADALN_BF16
-                     ? launch_residual<bf16, true>(job, map, s, st)
-                     : launch_residual<float, true>(job, map, s, st);
+                     ? launch_residual<bf16, true>(job, map, s, rows_of(map), st)
+                     : launch_residual<float, true>(job, map, s, rows_of(map), st);
   if (e != hipSuccess) return hip_fail(e, "adaln_residual_bwd launch");
   if (dgate != nullptr && !direct(map)) {
     const int32_t D = s.nvec * elems_per_vec(dtype);
