@@ -172,124 +172,173 @@ struct Move {
   int32_t tiles;        // wavefronts a row is shared between
 };
 
-constexpr int kTileVecs = 4;  // vectors a lane holds of a row
+constexpr int kTileVecs = 2;  // vectors a lane holds of a row at a time
 constexpr int kTile = kTileVecs * kWave;
+constexpr int kAtOnce = 4;    // sorted rows whose loads are in flight together
+// The same for the join's backward.  (MI355X, bf16: 32760 tokens, 4 choices of
+// 64 experts, 5120 features: 588 us, 586 by tiles of two vectors and four rows;
+// 4096 tokens, 8 choices, 4096 features: 110 and 120.)
+constexpr int kBwdVecs = 4;
+constexpr int kBwdAtOnce = 2;
 
 enum { kScatter, kGather };
 
-// A wavefront takes a tile of 256 vectors of a token's row.  kScatter: the
-// token's row to its places, times w if there is one.  kGather: the sum of the
-// rows at its places.  Sums are f32, in the order of the choices.
-template <typename T, int OP>
+template <bool STREAM>
+__device__ __forceinline__ Vec load_as(const void *p) {
+  return STREAM ? load_stream(p) : load_vec(p);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_as(void *p, const Vec &v) {
+  if (STREAM)
+    store_stream(p, v);
+  else
+    store_vec(p, v);
+}
+
+// The sorted row of a token's choice, lane j's of choice j; -1 for none.
+__device__ __forceinline__ int slot_of(const Move &p, int64_t t, int lane) {
+  if (lane >= p.k) return -1;
+  const int s = p.slot[t * p.k + lane];
+  return s < p.rows ? s : -1;
+}
+
+// A wavefront takes a tile of 128 vectors of a token's row.  kScatter: the
+// token's row to its places.  kGather: the sum of the rows at its places, times
+// w if there is one, in float32, in the order of the choices.
+template <typename T, int OP, bool STREAM>
 __device__ __forceinline__ void move_tile(const Move &p, int64_t id) {
   constexpr int E = Elems<T>::value;
   const int lane = lane_id();
   const int64_t t = id / p.tiles;
   const int v0 = (int)(id - t * p.tiles) * kTile + lane;
-  int my_slot = -1;
-  float my_w = 1.f;
-  if (lane < p.k) {
-    my_slot = p.slot[t * p.k + lane];
-    if (p.w != nullptr) my_w = p.w[t * p.k + lane];
-  }
-  if (my_slot >= p.rows) my_slot = -1;
+  const int my_slot = slot_of(p, t, lane);
   if constexpr (OP == kScatter) {
     Vec x[kTileVecs];
 #pragma unroll
     for (int i = 0; i < kTileVecs; ++i)
       if (v0 + i * kWave < p.nvec)
-        x[i] = load_vec(p.one + (t * p.nvec + v0 + i * kWave) * 16);
+        x[i] = load_as<STREAM>(p.one + (t * p.nvec + v0 + i * kWave) * 16);
     for (int j = 0; j < p.k; ++j) {
       const int s = __builtin_amdgcn_readlane(my_slot, j);
       if (s < 0) continue;
-      const float w = lane_read(my_w, j);
 #pragma unroll
-      for (int i = 0; i < kTileVecs; ++i) {
-        if (v0 + i * kWave >= p.nvec) break;
-        Vec o = x[i];
-        if (p.w != nullptr) {
-          float f[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) f[e] = elem<T>(x[i], e) * w;
-          o = pack<T>(f);
-        }
-        store_vec(p.many_out + ((int64_t)s * p.nvec + v0 + i * kWave) * 16, o);
-      }
+      for (int i = 0; i < kTileVecs; ++i)
+        if (v0 + i * kWave < p.nvec)
+          store_as<STREAM>(
+              p.many_out + ((int64_t)s * p.nvec + v0 + i * kWave) * 16, x[i]);
     }
   } else {
+    float my_w = 1.f;
+    if (p.w != nullptr && lane < p.k) my_w = p.w[t * p.k + lane];
     float sum[kTileVecs][E] = {};
-    for (int j = 0; j < p.k; ++j) {
-      const int s = __builtin_amdgcn_readlane(my_slot, j);
-      if (s < 0) continue;
-      const float w = lane_read(my_w, j);
+    for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
+      Vec v[kAtOnce][kTileVecs];
+      int s[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < kTileVecs; ++i) {
-        if (v0 + i * kWave >= p.nvec) break;
-        const Vec v =
-            load_vec(p.many + ((int64_t)s * p.nvec + v0 + i * kWave) * 16);
+      for (int j = 0; j < kAtOnce; ++j) {
+        s[j] = j0 + j < p.k ? __builtin_amdgcn_readlane(my_slot, j0 + j) : -1;
+        if (s[j] < 0) continue;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          sum[i][e] = p.w != nullptr ? fmaf(w, elem<T>(v, e), sum[i][e])
-                                     : sum[i][e] + elem<T>(v, e);
+        for (int i = 0; i < kTileVecs; ++i)
+          if (v0 + i * kWave < p.nvec)
+            v[j][i] = load_as<STREAM>(
+                p.many + ((int64_t)s[j] * p.nvec + v0 + i * kWave) * 16);
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (s[j] < 0) continue;
+        const float w = lane_read(my_w, j0 + j);
+#pragma unroll
+        for (int i = 0; i < kTileVecs; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            sum[i][e] = fmaf(w, elem<T>(v[j][i], e), sum[i][e]);
       }
     }
 #pragma unroll
     for (int i = 0; i < kTileVecs; ++i)
       if (v0 + i * kWave < p.nvec)
-        store_vec(p.one_out + (t * p.nvec + v0 + i * kWave) * 16,
-                  pack<T>(sum[i]));
+        store_as<STREAM>(p.one_out + (t * p.nvec + v0 + i * kWave) * 16,
+                         pack<T>(sum[i]));
   }
 }
 
-template <typename T, int OP>
+template <typename T, int OP, bool STREAM>
 __global__ __launch_bounds__(kBlock) void move_kernel(Move p) {
   const int64_t ids = p.T * p.tiles;
   for (int64_t id = (int64_t)blockIdx.x * (kBlock / kWave) + wave_id();
        id < ids; id += (int64_t)gridDim.x * (kBlock / kWave))
-    move_tile<T, OP>(p, id);
+    move_tile<T, OP, STREAM>(p, id);
 }
 
-// The join's gradients in one pass: a wavefront takes a token, reads its dy
-// and its k rows of ys, writes its k rows of dys and adds up dw.
-template <typename T>
+// The join's gradients in one pass: a wavefront takes a token and two of its
+// choices at a time, reads its dy and their rows of ys, writes their rows of
+// dys (which may stand in ys' place: a lane reads what it writes before) and
+// adds up dw.
+template <typename T, bool STREAM>
 __device__ __forceinline__ void join_bwd_row(const Move &p, int64_t t) {
   constexpr int E = Elems<T>::value;
   const int lane = lane_id();
-  int my_slot = -1;
+  const int my_slot = slot_of(p, t, lane);
   float my_w = 0.f, my_dw = 0.f;
-  if (lane < p.k) {
-    my_slot = p.slot[t * p.k + lane];
-    my_w = p.w[t * p.k + lane];
-  }
-  if (my_slot >= p.rows) my_slot = -1;
-  for (int j = 0; j < p.k; ++j) {
-    const int s = __builtin_amdgcn_readlane(my_slot, j);
-    if (s < 0) continue;
-    const float w = lane_read(my_w, j);
-    float dot = 0.f;
-    for (int v = lane; v < p.nvec; v += kWave) {
-      const Vec dy = load_vec(p.one + (t * p.nvec + v) * 16);
-      const Vec ys = load_vec(p.many + ((int64_t)s * p.nvec + v) * 16);
-      float f[E];
+  if (lane < p.k) my_w = p.w[t * p.k + lane];
+  for (int j0 = 0; j0 < p.k; j0 += kBwdAtOnce) {
+    int s[kBwdAtOnce];
+    float w[kBwdAtOnce], dot[kBwdAtOnce];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float g = elem<T>(dy, e);
-        dot = fmaf(g, elem<T>(ys, e), dot);
-        f[e] = w * g;
-      }
-      store_vec(p.many_out + ((int64_t)s * p.nvec + v) * 16, pack<T>(f));
+    for (int j = 0; j < kBwdAtOnce; ++j) {
+      s[j] = j0 + j < p.k ? __builtin_amdgcn_readlane(my_slot, j0 + j) : -1;
+      w[j] = lane_read(my_w, min(j0 + j, kWave - 1));
+      dot[j] = 0.f;
     }
-    const float all = wave_sum(dot);
-    if (lane == j) my_dw = all;
+    for (int v0 = lane; v0 < p.nvec; v0 += kBwdVecs * kWave) {
+      Vec dy[kBwdVecs], ys[kBwdAtOnce][kBwdVecs];
+#pragma unroll
+      for (int i = 0; i < kBwdVecs; ++i)
+        if (v0 + i * kWave < p.nvec)
+          dy[i] = load_vec(p.one + (t * p.nvec + v0 + i * kWave) * 16);
+#pragma unroll
+      for (int j = 0; j < kBwdAtOnce; ++j)
+        if (s[j] >= 0)
+#pragma unroll
+          for (int i = 0; i < kBwdVecs; ++i)
+            if (v0 + i * kWave < p.nvec)
+              ys[j][i] = load_as<STREAM>(
+                  p.many + ((int64_t)s[j] * p.nvec + v0 + i * kWave) * 16);
+#pragma unroll
+      for (int j = 0; j < kBwdAtOnce; ++j) {
+        if (s[j] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < kBwdVecs; ++i) {
+          if (v0 + i * kWave >= p.nvec) break;
+          float f[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float g = elem<T>(dy[i], e);
+            dot[j] = fmaf(g, elem<T>(ys[j][i], e), dot[j]);
+            f[e] = w[j] * g;
+          }
+          store_as<STREAM>(
+              p.many_out + ((int64_t)s[j] * p.nvec + v0 + i * kWave) * 16,
+              pack<T>(f));
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBwdAtOnce; ++j) {
+      if (s[j] < 0) continue;
+      const float all = wave_sum(dot[j]);
+      if (lane == j0 + j) my_dw = all;
+    }
   }
   if (lane < p.k) p.dw[t * p.k + lane] = my_dw;
 }
 
-template <typename T>
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(kBlock) void join_bwd_kernel(Move p) {
   for (int64_t t = (int64_t)blockIdx.x * (kBlock / kWave) + wave_id();
        t < p.T; t += (int64_t)gridDim.x * (kBlock / kWave))
-    join_bwd_row<T>(p, t);
+    join_bwd_row<T, STREAM>(p, t);
 }
 
 // ------------------------------------------------------------------- checks
@@ -344,14 +393,27 @@ hipError_t launch_waves(K k, int64_t waves, hipStream_t s, const Move &p) {
                        p);
 }
 
+// Rows that another kernel has just written may still lie in the 256 MB
+// Infinity Cache, and the next one finds them there: up to kCachedBytes read
+// and written a call takes plain accesses, past it the streaming hint.
+constexpr int64_t kCachedBytes = int64_t(192) << 20;
+
+bool past_caches(const Move &p, int rows) {
+  return p.T * rows * p.nvec * 16 > kCachedBytes;
+}
+
 template <int OP>
 int move(const Move &p, int dtype, void *stream, const char *what) {
   if (p.T == 0) return ok();
   const hipStream_t s = (hipStream_t)stream;
+  const int64_t n = p.T * p.tiles;
+  const bool hint = past_caches(p, 1 + p.k);
   const hipError_t e =
       dtype == ADALN_BF16
-          ? launch_waves(move_kernel<bf16, OP>, p.T * p.tiles, s, p)
-          : launch_waves(move_kernel<float, OP>, p.T * p.tiles, s, p);
+          ? launch_waves(hint ? move_kernel<bf16, OP, true>
+                              : move_kernel<bf16, OP, false>, n, s, p)
+          : launch_waves(hint ? move_kernel<float, OP, true>
+                              : move_kernel<float, OP, false>, n, s, p);
   if (e != hipSuccess) return hip_fail(e, what);
   return ok();
 }
@@ -473,9 +535,13 @@ ADALN_API int adaln_experts_join_bwd(const void *dy, const void *ys,
   p.w = w;
   p.dw = dw;
   const hipStream_t s = (hipStream_t)stream;
-  const hipError_t e = dtype == ADALN_BF16
-                           ? launch_waves(join_bwd_kernel<bf16>, T, s, p)
-                           : launch_waves(join_bwd_kernel<float>, T, s, p);
+  const bool hint = past_caches(p, 1 + 2 * p.k);
+  const hipError_t e =
+      dtype == ADALN_BF16
+          ? launch_waves(hint ? join_bwd_kernel<bf16, true>
+                              : join_bwd_kernel<bf16, false>, T, s, p)
+          : launch_waves(hint ? join_bwd_kernel<float, true>
+                              : join_bwd_kernel<float, false>, T, s, p);
   if (e != hipSuccess) return hip_fail(e, "adaln_experts_join_bwd launch");
   return ok();
 }
