@@ -200,7 +200,7 @@ struct Tile {
     if (kPieces == 8) return ((r >> 1 & 1) << 2) | (r >> 2 & 3);
     return r >> 2 & 3;
   }
-  // the lane's place in rows()
+  // The lane's place in rows(); PAIRED: in pairs().
   static __device__ __forceinline__ int row_place() {
     const int r = lane_id() % 32, h = half_of();
     return kHalf ? r * kPitch + turn(r) * 16 + h * 8
@@ -225,7 +225,26 @@ struct Tile {
     }
     return f;
   }
+  // The same in the order of a state's rows (state_row): bf16, eight features
+  // side by side, one read.
+  static __device__ __forceinline__ int pair_place() {
+    const int r = lane_id() % 32, h = half_of();
+    return kHalf ? r * kPitch + (turn(r) ^ h) * 16 : row_place();
+  }
+  static __device__ __forceinline__ Frag<T> pairs(const lds_char *tile,
+                                                  int place, int b) {
+    if constexpr (kHalf) {
+      typedef __attribute__((address_space(3))) const u32x4 lds_u4;
+      Frag<T> f;
+      f.v = __builtin_bit_cast(bf16x8, *(lds_u4 *)(tile + (place ^ (32 * b))));
+      return f;
+    } else {
+      return rows(tile, place, b);
+    }
+  }
   // the lane's places in cols()
+  // (STATE: of features in the order of a state's rows)
+  template <bool STATE = false>
   static __device__ __forceinline__ void col_places(int (&place)[kCols]) {
     const int l = lane_id(), h = half_of();
 #pragma unroll
@@ -234,8 +253,10 @@ struct Tile {
         // 16 lanes read four tokens of 16 features, and get a feature's four
         // tokens each
         const int r = 8 * x + 4 * h + (l % 16) / 4;
-        const int c = (l >> 4 & 1) * 2 + (l >> 1 & 1);
-        place[x] = r * kPitch + (c ^ turn(r)) * 16 + (l & 1) * 8;
+        // (the lanes' units of four features: 0, 1, 2, 3, or 0, 2, 1, 3)
+        const int c = (l >> 4 & 1) * 2 + (STATE ? l & 1 : l >> 1 & 1);
+        place[x] = r * kPitch + (c ^ turn(r)) * 16 +
+                   (STATE ? l >> 1 & 1 : l & 1) * 8;
       } else {
         const int r = 4 * h + x;
         place[x] = r * kPitch + ((l % 32 / 4) ^ turn(r)) * 16 + l % 4 * 4;
@@ -353,93 +374,81 @@ __device__ __forceinline__ int fresh(int x) {
   return x;
 }
 
-// Chunks of NT tensors on their way to LDS, SETS at a time: one being worked
-// on, the next ones' loads in flight.
-template <typename T, int DP, int NT, int THREADS, int SETS>
-struct Chunks {
-  typedef Tile<T, DP> Tl;
-  static constexpr int kSet = NT * Tl::kBytes;
-  static constexpr int kAll = kChunk * Tl::kPieces;
-  // loads that every wavefront has of a whole chunk, at least
-  static constexpr int kLoads = NT * (kAll / THREADS);
-  lds_char *lds;  // SETS sets of NT tiles
+// Pieces that no load fills hold zeros: features past the head's, and tokens
+// past the end.
+__device__ __forceinline__ void clear(lds_char *lds, int from, int to, int id,
+                                      int threads) {
+  for (int x = from + id; x < to; x += threads)
+    *(__attribute__((address_space(3))) u32x4 *)(lds + x * 16) =
+        u32x4{0, 0, 0, 0};
+}
 
-  // Pieces that no load fills hold zeros: features past the head's, and tokens
-  // past the end.
-  __device__ __forceinline__ void clear_all() const {
-    for (int x = threadIdx.x; x < SETS * kSet / 16; x += THREADS)
-      *(__attribute__((address_space(3))) u32x4 *)(lds + x * 16) =
-          u32x4{0, 0, 0, 0};
-  }
-  // n tokens from `start` into set `buf`, which nobody reads any more.
-  __device__ __forceinline__ void load(const Part (&in)[NT], int64_t start,
-                                       int n, int nvec, int buf) const {
-    const int tid = fresh(threadIdx.x);
-    if (n < kChunk) {
+// A tile's chunks on their way to LDS, a set of tiles for each that is there or
+// under way: the loads of TEAM threads (`id` of them), pieces x = id, id +
+// TEAM, ... of each chunk.
+template <typename Tl, int TEAM>
+struct Loader {
+  static constexpr int kAll = kChunk * Tl::kPieces;
+  static constexpr int kPer = (kAll + TEAM - 1) / TEAM;
+  // loads that every wavefront has of a whole chunk, at least
+  static constexpr int kLoads = kAll / TEAM;
+  const char *next;  // the next chunk's first token
+  int64_t step;      // from chunk to chunk, bytes
+  uint32_t off[kPer];
+  bool ok[kPer];
+  bool whole;        // every piece has a vector
+
+  // j0: the tile's first vector of nvec; tokens from `start`, chunk by chunk,
+  // forwards or backwards
+  __device__ __forceinline__ void init(const Part &in, int64_t start, int dir,
+                                       int j0, int nvec, int id) {
+    next = in.data + start * in.token * 16;
+    step = dir * in.token * (kChunk * 16);
+    whole = Tl::kPieces == Tl::kRowVecs && j0 + Tl::kRowVecs <= nvec;
 #pragma unroll
-      for (int a = 0; a < NT; ++a)
-        for (int x = n * Tl::kPieces + tid; x < kAll; x += THREADS)
-          *(__attribute__((address_space(3))) u32x4 *)(
-              lds + buf * kSet + a * Tl::kBytes + x * 16) = u32x4{0, 0, 0, 0};
-    }
-    const uint32_t wave = wave_id() * kWave;
-#pragma unroll
-    for (int i = 0; i < (kAll + THREADS - 1) / THREADS; ++i) {
-      if (kAll % THREADS != 0 && wave + i * THREADS >= kAll) break;
-      const int x = tid + i * THREADS;
+    for (int i = 0; i < kPer; ++i) {
+      const int x = id + i * TEAM;
       const int r = x / Tl::kPieces;
       const int c = (x % Tl::kPieces) ^ Tl::turn(r);
-      if (r >= n || c >= nvec) continue;
-#pragma unroll
-      for (int a = 0; a < NT; ++a)
-        dma((uint32_t)(uintptr_t)lds + buf * kSet + a * Tl::kBytes +
-                (wave + i * THREADS) * 16,
-            in[a].data + start * in[a].token * 16,
-            ((uint32_t)r * (uint32_t)in[a].token + c) * 16);
+      off[i] = ((uint32_t)r * (uint32_t)in.token + j0 + c) * 16;
+      ok[i] = x < kAll && c < Tl::kRowVecs && j0 + c < nvec;
     }
+  }
+  // n tokens into the tile at `lds`, which nobody reads any more; wave: the
+  // wavefront's first id.
+  __device__ __forceinline__ void load(uint32_t lds, uint32_t wave, int n,
+                                       int id) {
+    if (n == kChunk && whole) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (kAll % TEAM == 0 || (int)wave + i * TEAM < kAll)
+          dma(lds + (wave + i * TEAM) * 16, next, off[i]);
+    } else if (n == kChunk) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (ok[i]) dma(lds + (wave + i * TEAM) * 16, next, off[i]);
+    } else {
+      clear((lds_char *)(uintptr_t)lds, n * Tl::kPieces, kAll, id, TEAM);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (ok[i] && (id + i * TEAM) / Tl::kPieces < n)
+          dma(lds + (wave + i * TEAM) * 16, next, off[i]);
+    }
+    next += step;
   }
 };
 
-// The chunk's V of one wavefront: its own 32 columns, in two tiles of its own,
-// which take its outputs once V has been read.
-template <typename T, int THREADS>
-struct OwnChunk {
-  typedef Tile<T, 32> Tl;
-  static constexpr int kSet = THREADS / kWave * Tl::kBytes;
-  lds_char *lds;  // the wavefront's in the first set
+// A state's row in the order in which its rows are summed: of 16 rows, 0 to 3,
+// 8 to 11, 4 to 7 and 12 to 15, which gives a lane's eight summed elements,
+// slot(i), eight features side by side.
+template <typename T>
+__device__ __forceinline__ int state_row(int x) {
+  return sizeof(T) == 2 ? (x & ~12) | (x & 4) << 1 | (x & 8) >> 1 : x;
+}
 
-  __device__ __forceinline__ void clear_all() const {
-    for (int x = lane_id(); x < Tl::kBytes / 16; x += kWave)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        *(__attribute__((address_space(3))) u32x4 *)(lds + b * kSet + x * 16) =
-            u32x4{0, 0, 0, 0};
-  }
-  // vector j0 is its first column's
-  __device__ __forceinline__ void load(const Part &in, int64_t start, int n,
-                                       int nvec, int j0, int buf) const {
-    constexpr int kAll = kChunk * Tl::kPieces;
-    const int lane = fresh(lane_id());
-    if (n < kChunk)
-      for (int x = n * Tl::kPieces + lane; x < kAll; x += kWave)
-        *(__attribute__((address_space(3))) u32x4 *)(lds + buf * kSet +
-                                                     x * 16) =
-            u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kAll / kWave; ++i) {
-      const int x = lane + i * kWave;
-      const int r = x / Tl::kPieces;
-      const int c = j0 + ((x % Tl::kPieces) ^ Tl::turn(r));
-      if (r < n && c < nvec)
-        dma((uint32_t)(uintptr_t)lds + buf * kSet + i * kWave * 16,
-            in.data + start * in.token * 16,
-            ((uint32_t)r * (uint32_t)in.token + c) * 16);
-    }
-  }
-};
-
-// A wavefront's 32 columns of a state, rows by blocks of 32.
-template <int DP>
+// A wavefront's 32 columns of a state, rows by blocks of 32, in the order of
+// state_row.
+template <typename T, int DP>
 struct State {
   f32x16 s[DP / 32];
 
@@ -457,7 +466,7 @@ struct State {
     for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int row = 32 * m + 16 * (r / 8) + slot(r % 8);
+        const int row = state_row<T>(32 * m + 16 * (r / 8) + slot(r % 8));
         const bool in = row < d && c < d;
         const int at = across ? c * d + row : row * d + c;
         const float x = src[in ? at : 0];
@@ -470,7 +479,7 @@ struct State {
     for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int row = 32 * m + 16 * (r / 8) + slot(r % 8);
+        const int row = state_row<T>(32 * m + 16 * (r / 8) + slot(r % 8));
         if (row < d && c < d) dst[row * d + c] = s[m][r];
       }
   }
@@ -501,14 +510,12 @@ struct Powers {
   }
 };
 
-// S += sum over the chunk's tokens of k (add w v)^T.  The decayed v enters as
-// two bf16 on the way to outputs in bf16, as three on the way to a state in
-// float32.
-template <typename T, int DP, bool REV>
-__device__ __forceinline__ void gather(
-    State<DP> &S, const lds_char *K, const int (&place)[Tile<T, DP>::kCols],
-    const Frag<T> (&v)[2], const Powers<REV> &pw, float w, int parts) {
-  Parts<T, 3> x[2];
+// v on its way into the state, add w v: as two bf16 on the way to outputs in
+// bf16, as three on the way to a state in float32.
+template <typename T, bool REV>
+__device__ __forceinline__ void decayed(Parts<T, 3> (&x)[2],
+                                        const Frag<T> (&v)[2],
+                                        const Powers<REV> &pw, float w) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     float y[8];
@@ -517,11 +524,21 @@ __device__ __forceinline__ void gather(
     for (int i = 0; i < 8; ++i) y[i] *= pw.add[8 * j + i] * w;
     x[j].set(y);
   }
+}
+
+// S = over S + sum over the chunk's tokens of k x^T.
+template <int PARTS, typename T, int DP>
+__device__ __forceinline__ void gather(
+    State<T, DP> &S, const lds_char *K, const int (&place)[Tile<T, DP>::kCols],
+    const Parts<T, 3> (&x)[2], float over) {
 #pragma unroll
-  for (int m = 0; m < DP / 32; ++m)
+  for (int m = 0; m < DP / 32; ++m) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S.s[m][r] *= over;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      mma(S.s[m], Tile<T, DP>::cols(K, place, j, m), x[j], parts);
+      mma(S.s[m], Tile<T, DP>::cols(K, place, j, m), x[j], PARTS);
+  }
 }
 
 // What each stretch adds to the state (from zero): S of its own tokens, at the
@@ -534,53 +551,65 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
   // bf16: three sets of chunks.  Little is computed here, and two chunks' loads
   // in flight hide the memory's latency where one's do not.
   constexpr int kSets = Tl::kHalf ? 3 : 2;
-  typedef Chunks<T, DP, 2, 2 * DP, kSets> Ch;
-  __shared__ __align__(1024) char tiles[kSets * Ch::kSet];
-  const Ch ch = {(lds_char *)tiles};
+  constexpr int kSet = 2 * Tl::kBytes;
+  typedef Loader<Tl, 2 * DP> Ld;
+  __shared__ __align__(1024) char tiles[kSets * kSet];
+  lds_char *lds = (lds_char *)tiles;
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
   // nobody starts from the last one's end
   if ((REV ? st.head : st.tail) && p.final == nullptr) return;
-  Part in[2] = {p.in[0], p.in[1]};
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-    in[a].data += (st.batch * in[a].batch + (int64_t)h * in[a].head) * 16;
-  const float g = decay_of(p, h);
-  int place[Tl::kCols], place_v[Tl::kCols];
-  Tl::col_places(place);
-#pragma unroll
-  for (int x = 0; x < Tl::kCols; ++x)
-    place_v[x] = place[x] ^ (wave_id() * (Tl::kHalf ? 64 : 128));
-  State<DP> S;
-  S.clear();
-  Powers<REV> pw;
   const int chunks = (st.n + kChunk - 1) / kChunk;
   auto from = [&](int i) { return (REV ? i : chunks - 1 - i) * kChunk; };
+  const int tid = threadIdx.x;
+  const uint32_t wave0 = wave_id() * kWave;
+  Ld ld[2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    Part in = p.in[a];
+    in.data += (st.batch * in.batch + (int64_t)h * in.head) * 16;
+    ld[a].init(in, st.start + from(0), REV ? 1 : -1, 0, p.nvec, tid);
+  }
   auto load = [&](int i) {
-    ch.load(in, st.start + from(i), min(kChunk, st.n - from(i)), p.nvec,
-            i % kSets);
+    const int n = min(kChunk, st.n - from(i));
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+      ld[a].load((uint32_t)(uintptr_t)lds + i % kSets * kSet + a * Tl::kBytes,
+                 wave0, n, tid);
   };
   if (p.nvec < Tl::kRowVecs) {
-    ch.clear_all();
+    clear(lds, 0, kSets * kSet / 16, tid, 2 * DP);
     __syncthreads();
   }
   for (int i = 0; i < min(chunks, kSets - 1); ++i) load(i);
+  const float g = decay_of(p, h);
+  int place[Tl::kCols], place_v[Tl::kCols];
+  Tl::template col_places<true>(place);
+  Tl::col_places(place_v);
+#pragma unroll
+  for (int x = 0; x < Tl::kCols; ++x)
+    place_v[x] ^= wave_id() * (Tl::kHalf ? 64 : 128);
+  State<T, DP> S;
+  S.clear();
+  Powers<REV> pw;
   for (int i = 0; i < chunks; ++i) {
     const int n = min(kChunk, st.n - from(i));
     // (a chunk that is not whole may have fewer loads)
     if (kSets > 2 && i + 1 < chunks && from(i + 1) + kChunk <= st.n)
-      arrive<(kSets - 2) * Ch::kLoads>();
+      arrive<(kSets - 2) * 2 * Ld::kLoads>();
     else
       arrive<0>();
     if (i + kSets - 1 < chunks) load(i + kSets - 1);
     pw.set(g, p.scale, n);
     const float w = exp2f(g * (REV ? from(i) : st.n - from(i) - n));
-    const lds_char *K = ch.lds + i % kSets * Ch::kSet, *V = K + Tl::kBytes;
+    const lds_char *K = lds + i % kSets * kSet, *V = K + Tl::kBytes;
     Frag<T> v[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) v[j] = Tl::cols(V, place_v, j, 0);
-    gather<T, DP, REV>(S, K, place, v, pw, w, 3);
+    Parts<T, 3> x[2];
+    decayed<T, REV>(x, v, pw, w);
+    gather<3, T, DP>(S, K, place, x, 1.f);
   }
   S.store(p.states + job * p.d * p.d, p.d, 32 * wave_id());
 }
@@ -621,9 +650,6 @@ __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
   if (p.final != nullptr)
     *reinterpret_cast<float4 *>(p.final + row * dd + at) = run;
 }
-
-template <typename T>
-constexpr int kOutWaves = sizeof(T) == 2 ? 3 : 2;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -686,74 +712,91 @@ __device__ __forceinline__ void arrive_lds() {
 
 // The outputs of a stretch, from the state before it.  ROLES 1: in = q, k, v.
 // ROLES 2, the two gradients that run backwards: in = q, k, v, do, out = dv
-// (of k, q, do) and dk (of v, do, q), a set of wavefronts for each.  `across`
-// (bit by role): the states in memory are the transpose of this role's.
-template <typename T, int DP, bool REV, int ROLES>
+// (of k, q, do) and dk (of v, do, q), a set of wavefronts for each.  ONE: each
+// sequence is one stretch, which starts from its initial state and also makes
+// the state behind it.  `across` (bit by role): the states in memory are the
+// transpose of this role's.
+template <typename T, int DP, bool REV, int ROLES, bool ONE>
 __global__ __launch_bounds__(2 * DP * ROLES,
-                             ROLES == 1 ? kOutWaves<T> : 1) void out_kernel(
+                             ROLES == 1 ? 2 : 1) void out_kernel(
     Lin p, Stretches map, int32_t across) {
   typedef Tile<T, DP> Tl;
+  typedef Tile<T, 32> Sc;
   constexpr int kThreads = 2 * DP * ROLES, NT = ROLES + 2;
   constexpr int kWaves = kThreads / kWave;
+  constexpr int E = Elems<T>::value;
+  // bf16: three sets of chunks, two of them under way; f32 has room for two
+  constexpr int kSets = Tl::kHalf ? 3 : 2;
+  // V, of which a wavefront reads its own 32 columns alone, has tiles by
+  // wavefront where no role has it for something else; they take its outputs
+  // once V has been read
   constexpr bool kOwn = Tl::kHalf && ROLES == 1;
   constexpr int kShared = kOwn ? 2 : NT;  // tensors with a tile for all
-  constexpr int E = Elems<T>::value;
-  typedef Chunks<T, DP, kShared, kThreads, 2> Ch;
-  typedef OwnChunk<T, kThreads> Own;
-  __shared__ __align__(1024) char tiles[2 * Ch::kSet + (kOwn ? 2 * Own::kSet : 0)];
+  constexpr int kSet =
+      kShared * Tl::kBytes + (kOwn ? kWaves * Sc::kBytes : 0);
+  typedef Loader<Tl, kThreads> Ld;
+  typedef Loader<Sc, kWave> OwnLd;
+  __shared__ __align__(1024) char tiles[kSets * kSet];
   // outputs on their way out (f32: 16 bytes a lane as they stand, for which
   // LDS has no room beside two sets of tiles anyway)
-  __shared__ __align__(16) char outs[Tl::kHalf && !kOwn ? kWaves : 1][kOwn || !Tl::kHalf ? 16 : kChunk * 64];
+  __shared__ __align__(16) char outs[Tl::kHalf && !kOwn ? kWaves : 1]
+                                    [kOwn || !Tl::kHalf ? 16 : kChunk * 64];
   // the scores, decayed, in two parts: rows are the tokens t, 32 scores each
-  typedef Tile<T, 32> Sc;
   constexpr int kScParts = Parts<T, 2>::kParts;
   __shared__ __align__(1024) char scores[ROLES * kScParts * Sc::kBytes];
-  float kept[Tl::kHalf ? 1 : 16];
-  const Ch ch = {(lds_char *)tiles};
-  const Own own = {(lds_char *)tiles + 2 * Ch::kSet +
-                   wave_id() * Own::Tl::kBytes};
+  lds_char *lds = (lds_char *)tiles;
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
-  const int wave = wave_id(), lane = lane_id();
+  const int wave = wave_id(), tid = threadIdx.x;
   const int role = ROLES == 1 ? 0 : wave / (DP / 32);
   const int m0 = ROLES == 1 ? wave : wave % (DP / 32);
   const int c0 = 32 * m0;
-  Part in[NT];
+  const int chunks = (st.n + kChunk - 1) / kChunk;
+  auto from = [&](int i) { return (REV ? chunks - 1 - i : i) * kChunk; };
+  Ld ld[kShared];
+  OwnLd own;
 #pragma unroll
   for (int a = 0; a < NT; ++a) {
-    in[a] = p.in[a];
-    in[a].data += (st.batch * in[a].batch + (int64_t)h * in[a].head) * 16;
+    Part in = p.in[a];
+    in.data += (st.batch * in.batch + (int64_t)h * in.head) * 16;
+    if (a < kShared)
+      ld[a].init(in, st.start + from(0), REV ? -1 : 1, 0, p.nvec, tid);
+    else
+      own.init(in, st.start + from(0), REV ? -1 : 1, c0 / E, p.nvec, lane_id());
   }
+  auto own_at = [&](int i) {
+    return lds + i % kSets * kSet + kShared * Tl::kBytes + wave * Sc::kBytes;
+  };
+  auto load_shared = [&](int i) {
+    const int n = min(kChunk, st.n - from(i));
+#pragma unroll
+    for (int a = 0; a < kShared; ++a)
+      ld[a].load((uint32_t)(uintptr_t)lds + i % kSets * kSet + a * Tl::kBytes,
+                 wave * kWave, n, tid);
+  };
+  auto load_own = [&](int i) {
+    if constexpr (kOwn)
+      own.load((uint32_t)(uintptr_t)own_at(i), 0,
+               min(kChunk, st.n - from(i)), lane_id());
+  };
+  if (p.nvec < Tl::kRowVecs) {
+    clear(lds, 0, kSets * kSet / 16, tid, kThreads);
+    __syncthreads();
+  }
+  for (int i = 0; i < min(chunks, kSets - 1); ++i) {
+    load_shared(i);
+    load_own(i);
+  }
+  // the block of scores that does not count is never written
+  clear((lds_char *)scores, 0, sizeof scores / 16, tid, kThreads);
   const Part out = p.out[role];
   char *dst = const_cast<char *>(out.data) +
               (st.batch * out.batch + (int64_t)h * out.head) * 16;
   const float g = decay_of(p, h);
   const int64_t dd = (int64_t)p.d * p.d;
-  // the one stretch of a sequence also makes the state behind it
-  const int parts = p.states == nullptr ? 3 : 2;
-  const int chunks = (st.n + kChunk - 1) / kChunk;
-  auto from = [&](int i) { return (REV ? chunks - 1 - i : i) * kChunk; };
-  Part both[kShared];
-#pragma unroll
-  for (int a = 0; a < kShared; ++a) both[a] = in[a];
-  // the block of scores that does not count is never written
-  for (int x = threadIdx.x; x < (int)sizeof scores / 16; x += kThreads)
-    store_vec(scores + x * 16, vzero());
-  auto load = [&](int i) {
-    const int n = min(kChunk, st.n - from(i));
-    ch.load(both, st.start + from(i), n, p.nvec, i & 1);
-    if constexpr (kOwn)
-      own.load(in[2], st.start + from(i), n, p.nvec, c0 / E, i & 1);
-  };
-  if (p.nvec < Tl::kRowVecs) {
-    ch.clear_all();
-    if constexpr (kOwn) own.clear_all();
-    __syncthreads();
-  }
-  if (chunks > 0) load(0);
-  State<DP> S;
-  const float *src = p.states != nullptr ? p.states + job * dd
+  State<T, DP> S;
+  const float *src = !ONE ? p.states + job * dd
                      : p.init != nullptr
                          ? p.init + ((int64_t)st.seq * p.H + h) * dd
                          : nullptr;
@@ -763,121 +806,183 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     S.clear();
   // Of the 32 x 32 scores of a chunk only those of t >= s (REV: s >= t) count:
   // of their four blocks of 16 x 16 three, a wavefront of the role each (one
-  // wavefront, or two, take them in turn).
+  // wavefront, or two, take them in turn; a fourth computes one again, which
+  // costs nothing that a branch would not).
   constexpr int kTeam = DP / 32;
   constexpr int kTurns = (2 + kTeam) / kTeam;
   auto block_s = [](int i) { return REV ? (i > 0) : (i == 2); };
   auto block_t = [](int i) { return REV ? (i == 2) : (i > 0); };
   // powers of the lane's scores: s = 4 (lane / 16) + r, t = lane % 16; those
   // of the block off the diagonal are 16 tokens further apart
-  float near[4], far[4];
+  float near[kTurns][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int s = 4 * (lane / 16) + r, t = lane % 16;
-    const int e = REV ? s - t : t - s;
-    near[r] = e >= 0 ? p.scale * exp2f(g * e) : 0.f;
-    far[r] = p.scale * exp2f(g * (e + 16));
+  for (int turn = 0; turn < kTurns; ++turn)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int lane = lane_id();
+      const int s = 4 * (lane / 16) + r, t = lane % 16;
+      const int e = (REV ? s - t : t - s) +
+                    (min(m0 + turn * kTeam, 2) == 1 ? 16 : 0);
+      near[turn][r] = e >= 0 ? p.scale * exp2f(g * e) : 0.f;
+    }
+  // minus one where a row of 32 is summed element 16 x + slot(i)
+  Frag<T> minus[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      y[i] = lane_id() % 32 == 16 * x + slot(i) ? -1.f : 0.f;
+    to_frag(minus[x], y);
   }
   Powers<REV> pw;
-  const int row0 = Tl::row_place();
+  const int row0 = Tl::pair_place(), score_row0 = Sc::row_place();
   int place0[Tl::kCols], place_v0[Tl::kCols];
-  Tl::col_places(place0);
+  Tl::template col_places<true>(place0);
   if constexpr (kOwn) {
-    Own::Tl::col_places(place_v0);
+    Sc::col_places(place_v0);
   } else {
+    Tl::col_places(place_v0);
 #pragma unroll
     for (int x = 0; x < Tl::kCols; ++x)
-      place_v0[x] = place0[x] ^ (m0 * (Tl::kHalf ? 64 : 128));
+      place_v0[x] ^= m0 * (Tl::kHalf ? 64 : 128);
   }
-  // where 4 outputs of a token stand: 8 bytes, turned for the banks' sake
+  // The wavefront's outputs of a chunk are kept (in LDS, or f32 in registers)
+  // until the next one's loads are awaited, so that a store has a chunk's time
+  // to complete.  Where 4 bf16 of a token stand: 8 bytes, turned for the
+  // banks' sake.
   auto out_at = [&](int i, int t, int u) {
-    char *base = kOwn ? tiles + 2 * Ch::kSet + (i & 1) * Own::kSet +
-                            wave * Own::Tl::kBytes
+    char *base = kOwn ? tiles + i % kSets * kSet + kShared * Tl::kBytes +
+                            wave * Sc::kBytes
                       : outs[kOwn ? 0 : wave];
     return reinterpret_cast<uint2 *>(base + t * 64 + (u ^ (t >> 2 & 3)) * 8);
   };
-  // the wavefront's outputs of a chunk, kept in LDS until the next one's loads
-  // are awaited: so a store has a chunk's time to complete
-  auto store = [&](int i) {
-    constexpr int kRow = 32 / E;  // vectors of 32 features
-    const int n = min(kChunk, st.n - from(i));
-    const int lane = fresh(lane_id());
-    if constexpr (!Tl::kHalf) {
-      const int t = lane % 32;
+  constexpr int kRow = 32 / E;                    // vectors of 32 features
+  constexpr int kKept = Tl::kHalf ? kChunk * kRow / kWave : 4;
+  float kept[Tl::kHalf ? 1 : 16];
+  uint32_t out_off[kKept];
+  bool out_ok[kKept];
+  int out_t[kKept];
 #pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const int j = (c0 + 16 * (r / 8) + slot(r % 8)) / 4;
-        const float x[4] = {kept[r], kept[r + 1], kept[r + 2], kept[r + 3]};
-        if (t < n && j < p.nvec)
-          store_vec(dst + ((st.start + from(i) + t) * out.token + j) * 16,
-                    pack<float>(x));
+  for (int x = 0; x < kKept; ++x) {
+    const int lane = lane_id();
+    const int t = Tl::kHalf ? (lane + x * kWave) / kRow : lane % 32;
+    const int j = Tl::kHalf ? (lane + x * kWave) % kRow
+                            : (16 * (x / 2) + slot(x % 2 * 4)) / 4;
+    out_t[x] = t;
+    out_off[x] = ((uint32_t)t * (uint32_t)out.token + c0 / E + j) * 16;
+    out_ok[x] = c0 / E + j < p.nvec;
+  }
+  auto take = [&](int i, Vec (&y)[kKept]) {
+#pragma unroll
+    for (int x = 0; x < kKept; ++x) {
+      if constexpr (Tl::kHalf) {
+        const int lane = fresh(lane_id()) + x * kWave;
+        const int t = lane / kRow, j = lane % kRow;
+        const uint2 lo = *out_at(i, t, 2 * j), hi = *out_at(i, t, 2 * j + 1);
+        y[x].w[0] = lo.x;
+        y[x].w[1] = lo.y;
+        y[x].w[2] = hi.x;
+        y[x].w[3] = hi.y;
+      } else {
+        const float f[4] = {kept[4 * x], kept[4 * x + 1], kept[4 * x + 2],
+                            kept[4 * x + 3]};
+        y[x] = pack<float>(f);
       }
-      return;
-    }
-#pragma unroll
-    for (int x = lane; x < kChunk * kRow; x += kWave) {
-      const int t = x / kRow, j = x % kRow;
-      Vec y;
-      const uint2 lo = *out_at(i, t, 2 * j), hi = *out_at(i, t, 2 * j + 1);
-      y.w[0] = lo.x;
-      y.w[1] = lo.y;
-      y.w[2] = hi.x;
-      y.w[3] = hi.y;
-      if (t < n && c0 / E + j < p.nvec)
-        store_vec(dst + ((st.start + from(i) + t) * out.token + c0 / E + j) * 16,
-                  y);
     }
   };
+  auto store = [&](int i, const Vec (&y)[kKept]) {
+    const int n = min(kChunk, st.n - from(i));
+    char *base = dst + (st.start + from(i)) * out.token * 16;
+#pragma unroll
+    for (int x = 0; x < kKept; ++x)
+      if (out_ok[x] && (n == kChunk || out_t[x] < n))
+        store_stream(base + out_off[x], y[x]);
+  };
   for (int i = 0; i < chunks; ++i) {
-    arrive<0>();
-    if (i > 0) store(i - 1);
-    if (i + 1 < chunks) load(i + 1);
+    // (a chunk that is not whole may have fewer loads)
+    if (kSets > 2 && i + 1 < chunks && from(i + 1) + kChunk <= st.n)
+      arrive<(kSets - 2) * (kShared * Ld::kLoads + (kOwn ? OwnLd::kLoads : 0))>();
+    else
+      arrive<0>();
+    {
+      Vec y[kKept];
+      if (i > 0) take(i - 1, y);
+      if (i + kSets - 1 < chunks) load_shared(i + kSets - 1);
+      if (i > 0) store(i - 1, y);
+      // (into the tile that the outputs have just been taken from)
+      if (i + kSets - 1 < chunks) load_own(i + kSets - 1);
+    }
     pw.set(g, p.scale, min(kChunk, st.n - from(i)));
-    const int row = fresh(row0), lane = fresh(lane_id());
-    const int score_row = Sc::row_place();
+    const int row = fresh(row0), score_row = fresh(score_row0);
     int place[Tl::kCols], place_v[Tl::kCols];
 #pragma unroll
     for (int x = 0; x < Tl::kCols; ++x) {
       place[x] = fresh(place0[x]);
       place_v[x] = fresh(place_v0[x]);
     }
-    const lds_char *tile = ch.lds + (i & 1) * Ch::kSet;
+    const lds_char *tile = lds + i % kSets * kSet;
     const lds_char *Q =
         tile + (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
     const lds_char *K =
         tile + (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
     const lds_char *V =
-        kOwn ? own.lds + (i & 1) * Own::kSet
+        kOwn ? own_at(i)
              : tile + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
     lds_char *P = (lds_char *)scores + role * kScParts * Sc::kBytes;
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
-      const int i3 = m0 + turn * kTeam;
-      if (i3 < 3) {
-        const int s0 = 16 * block_s(i3), t0 = 16 * block_t(i3);
-        f32x4 a = {};
-        score<T, DP>(a, K, Q, s0, t0);
-        // s along the lane's row of the tile: four of them side by side
-        float x[8] = {};
+      const int i3 = min(m0 + turn * kTeam, 2);
+      const int s0 = 16 * block_s(i3), t0 = 16 * block_t(i3);
+      f32x4 a = {};
+      score<T, DP>(a, K, Q, s0, t0);
+      // s along the lane's row of the tile: four of them side by side
+      float x[8] = {};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = a[r] * (i3 == 1 ? far[r] : near[r]);
-        const int t = t0 + lane % 16;
-        put_scores<T>(P, x, t, s0 / 4 + lane / 16);
-      }
+      for (int r = 0; r < 4; ++r) x[r] = a[r] * near[turn][r];
+      const int lane = fresh(lane_id());
+      put_scores<T>(P, x, t0 + lane % 16, s0 / 4 + lane / 16);
     }
-    // the state's part
+    // the state's part; what its rounding to bf16 leaves, the matrix cores
+    // subtract (exactly): S - 1 * hi
     f32x16 o = {};
 #pragma unroll
-    for (int b = 0; b < DP / 16; ++b) {
-      const Frag<T> q = Tl::rows(Q, row, b);
-      float x[8];
+    for (int m = 0; m < DP / 32; ++m) {
+      const Frag<T> q[2] = {Tl::pairs(Q, row, 2 * m),
+                            Tl::pairs(Q, row, 2 * m + 1)};
+      Frag<T> hi[2];
+      f32x16 rest = S.s[m];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = S.s[b / 2][8 * (b % 2) + e];
-      Parts<T, 2> y;
-      y.set(x);
-      mma(o, y, q);
-      if (b % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+      for (int x = 0; x < 2; ++x) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = S.s[m][8 * x + e];
+        to_frag(hi[x], y);
+        mma(o, hi[x], q[x]);
+        if constexpr (Tl::kHalf) mma(rest, minus[x], hi[x]);
+      }
+      if constexpr (Tl::kHalf) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = rest[8 * x + e];
+          Frag<T> lo;
+          to_frag(lo, y);
+          mma(o, lo, q[x]);
+        }
+      }
     }
+    Frag<T> v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (kOwn)
+        v[j] = Sc::cols(V, place_v, j, 0);
+      else
+        v[j] = Tl::cols(V, place_v, j, 0);
+    }
+    Parts<T, 3> vs[2];
+    decayed<T, REV>(vs, v, pw, 1.f);
     if (kTeam > 1) {
       arrive_lds();
     } else {
@@ -885,20 +990,15 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[r] *= pw.own;
-    Frag<T> v[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if constexpr (kOwn)
-        v[j] = Own::Tl::cols(V, place_v, j, 0);
-      else
-        v[j] = Tl::cols(V, place_v, j, 0);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int part = 0; part < kScParts; ++part)
         mma(o, v[j], Sc::rows(P + part * Sc::kBytes, score_row, j));
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    gather<ONE ? 3 : 2, T, DP>(S, K, place, vs, pw.over);
     // o: rows are features, the lane's column its token
     if constexpr (Tl::kHalf) {
+      const int lane = fresh(lane_id());
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const float x[8] = {o[r], o[r + 1], o[r + 2], o[r + 3], 0, 0, 0, 0};
@@ -910,18 +1010,14 @@ __global__ __launch_bounds__(2 * DP * ROLES,
 #pragma unroll
       for (int r = 0; r < 16; ++r) kept[r] = o[r];
     }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int m = 0; m < DP / 32; ++m)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) S.s[m][r] *= pw.over;
-    gather<T, DP, REV>(S, K, place, v, pw, 1.f, parts);
   }
   if (chunks > 0) {
     __builtin_amdgcn_wave_barrier();
-    store(chunks - 1);
+    Vec y[kKept];
+    take(chunks - 1, y);
+    store(chunks - 1, y);
   }
-  if (p.final != nullptr && p.states == nullptr && role == 0)
+  if (ONE && p.final != nullptr && role == 0)
     S.store(p.final + ((int64_t)st.seq * p.H + h) * dd, p.d, c0);
 }
 
@@ -1089,20 +1185,32 @@ hipError_t run_states(const Lin &p, const Stretches &m, hipStream_t s) {
   return launch_jobs(state_kernel<T, 128, REV>, 256, p, s, m);
 }
 
-template <typename T, bool REV, int ROLES>
+template <typename T, bool REV, int ROLES, bool ONE>
 hipError_t run_out(const Lin &p, const Stretches &m, int32_t across,
                    hipStream_t s) {
   if (p.d <= 32)
-    return launch_jobs(out_kernel<T, 32, REV, ROLES>, 64 * ROLES, p, s, m,
+    return launch_jobs(out_kernel<T, 32, REV, ROLES, ONE>, 64 * ROLES, p, s, m,
                        across);
   if (p.d <= 64)
-    return launch_jobs(out_kernel<T, 64, REV, ROLES>, 128 * ROLES, p, s, m,
-                       across);
+    return launch_jobs(out_kernel<T, 64, REV, ROLES, ONE>, 128 * ROLES, p, s,
+                       m, across);
   if (p.d <= 96)
-    return launch_jobs(out_kernel<T, 96, REV, ROLES>, 192 * ROLES, p, s, m,
-                       across);
-  return launch_jobs(out_kernel<T, 128, REV, ROLES>, 256 * ROLES, p, s, m,
+    return launch_jobs(out_kernel<T, 96, REV, ROLES, ONE>, 192 * ROLES, p, s,
+                       m, across);
+  return launch_jobs(out_kernel<T, 128, REV, ROLES, ONE>, 256 * ROLES, p, s, m,
                      across);
+}
+
+template <bool REV, int ROLES>
+hipError_t outputs(const Lin &p, const Stretches &m, int32_t across, int dtype,
+                   hipStream_t s) {
+  if (p.states == nullptr)
+    return dtype == ADALN_BF16
+               ? run_out<bf16, REV, ROLES, true>(p, m, across, s)
+               : run_out<float, REV, ROLES, true>(p, m, across, s);
+  return dtype == ADALN_BF16
+             ? run_out<bf16, REV, ROLES, false>(p, m, across, s)
+             : run_out<float, REV, ROLES, false>(p, m, across, s);
 }
 
 // The states that the stretches start from: p.in are the two parts that make
@@ -1266,8 +1374,7 @@ ADALN_API int adaln_lin_attn_fwd(
   p.in[1] = part_of(k, B, N, H, dtype);
   p.in[2] = part_of(v, B, N, H, dtype);
   p.out[0] = part_of(o, B, N, H, dtype);
-  e = dtype == ADALN_BF16 ? run_out<bf16, false, 1>(p, m, 0, s)
-                          : run_out<float, false, 1>(p, m, 0, s);
+  e = outputs<false, 1>(p, m, 0, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_fwd launch");
   return ok();
 }
@@ -1332,8 +1439,7 @@ ADALN_API int adaln_lin_attn_bwd(
   p.in[1] = pv;
   p.in[2] = pk;
   p.out[0] = part_of(dq, B, N, H, dtype);
-  e = dtype == ADALN_BF16 ? run_out<bf16, false, 1>(p, m, 1, s)
-                          : run_out<float, false, 1>(p, m, 1, s);
+  e = outputs<false, 1>(p, m, 1, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd dq");
   // dk and dv, from the states' gradients
   p.init = dstate_out;
@@ -1351,8 +1457,7 @@ ADALN_API int adaln_lin_attn_bwd(
   p.in[3] = pdo;
   p.out[0] = part_of(dv, B, N, H, dtype);
   p.out[1] = part_of(dk, B, N, H, dtype);
-  e = dtype == ADALN_BF16 ? run_out<bf16, true, 2>(p, m, 2, s)
-                          : run_out<float, true, 2>(p, m, 2, s);
+  e = outputs<true, 2>(p, m, 2, dtype, s);
   if (e != hipSuccess) return hip_fail(e, "adaln_lin_attn_bwd dk, dv");
   return ok();
 }
