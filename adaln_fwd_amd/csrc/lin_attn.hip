@@ -43,6 +43,7 @@ constexpr int kChunk = 32;
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -150,6 +151,19 @@ __device__ __forceinline__ void mma(f32x16 &acc, const Frag<T> &a,
 
 typedef __attribute__((address_space(3))) char lds_char;
 
+// LDS by its 32-bit addresses.
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at) {
+  return *(__attribute__((address_space(3))) const V *)(lds_char *)at;
+}
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t at, const V &v) {
+  *(__attribute__((address_space(3))) V *)(lds_char *)at = v;
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(lds_char *)p;
+}
+
 // 16 bytes per lane from memory to LDS at `lds` + 16 * lane: a wave-uniform
 // base and a 32-bit offset per lane.  The compiler does not see these loads:
 // arrive() waits for them.  (m0 takes the LDS address; the s_nop is the wait
@@ -200,52 +214,47 @@ struct Tile {
     if (kPieces == 8) return ((r >> 1 & 1) << 2) | (r >> 2 & 3);
     return r >> 2 & 3;
   }
-  // The lane's place in rows(); PAIRED: in pairs().
-  static __device__ __forceinline__ int row_place() {
+  // The lane's place in rows(), relative to the tile.
+  static __device__ __forceinline__ uint32_t row_place() {
     const int r = lane_id() % 32, h = half_of();
     return kHalf ? r * kPitch + turn(r) * 16 + h * 8
                  : r * kPitch + (turn(r) ^ h) * 16;
   }
-  // Token lane % 32, features 16 b + slot(i).
-  static __device__ __forceinline__ Frag<T> rows(const lds_char *tile,
-                                                 int place, int b) {
+  // Token lane % 32, features 16 b + slot(i); at: the tile's address in LDS
+  // plus the lane's place.
+  static __device__ __forceinline__ Frag<T> rows(uint32_t at, int b) {
     Frag<T> f;
     if constexpr (kHalf) {
-      typedef __attribute__((address_space(3))) const s16x4 lds_s16x4;
-      const s16x4 x = *(lds_s16x4 *)(tile + (place ^ (32 * b)));
-      const s16x4 y = *(lds_s16x4 *)(tile + (place ^ (32 * b) ^ 16));
+      const s16x4 x = lds_read<s16x4>(at ^ (32 * b));
+      const s16x4 y = lds_read<s16x4>(at ^ (32 * b) ^ 16);
       const s16x8 v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
       f.v = __builtin_bit_cast(bf16x8, v);
     } else {
-      typedef float f32x4 __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) const f32x4 lds_f4;
-      const f32x4 x = *(lds_f4 *)(tile + (place ^ (64 * b)));
-      const f32x4 y = *(lds_f4 *)(tile + (place ^ (64 * b) ^ 32));
+      const f32x4 x = lds_read<f32x4>(at ^ (64 * b));
+      const f32x4 y = lds_read<f32x4>(at ^ (64 * b) ^ 32);
       f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return f;
   }
-  // The same in the order of a state's rows (state_row): bf16, eight features
+  // The same in the order of a state's rows: bf16, eight features
   // side by side, one read.
-  static __device__ __forceinline__ int pair_place() {
+  static __device__ __forceinline__ uint32_t pair_place() {
     const int r = lane_id() % 32, h = half_of();
     return kHalf ? r * kPitch + (turn(r) ^ h) * 16 : row_place();
   }
-  static __device__ __forceinline__ Frag<T> pairs(const lds_char *tile,
-                                                  int place, int b) {
+  static __device__ __forceinline__ Frag<T> pairs(uint32_t at, int b) {
     if constexpr (kHalf) {
-      typedef __attribute__((address_space(3))) const u32x4 lds_u4;
       Frag<T> f;
-      f.v = __builtin_bit_cast(bf16x8, *(lds_u4 *)(tile + (place ^ (32 * b))));
+      f.v = __builtin_bit_cast(bf16x8, lds_read<u32x4>(at ^ (32 * b)));
       return f;
     } else {
-      return rows(tile, place, b);
+      return rows(at, b);
     }
   }
-  // the lane's places in cols()
-  // (STATE: of features in the order of a state's rows)
-  template <bool STATE = false>
-  static __device__ __forceinline__ void col_places(int (&place)[kCols]) {
+  // The lane's places in cols(); STATE: of features in the order of a state's
+  // rows.
+  template <bool STATE>
+  static __device__ __forceinline__ void col_places(uint32_t (&place)[kCols]) {
     const int l = lane_id(), h = half_of();
 #pragma unroll
     for (int x = 0; x < kCols; ++x) {
@@ -264,26 +273,29 @@ struct Tile {
     }
   }
   // Feature 32 m + lane % 32, tokens 16 j + slot(i).
-  static __device__ __forceinline__ Frag<T> cols(const lds_char *tile,
-                                                 const int (&place)[kCols],
+  static __device__ __forceinline__ Frag<T> cols(const uint32_t (&at)[kCols],
                                                  int j, int m) {
     Frag<T> f;
     if constexpr (kHalf) {
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4 *)(tile + (place[0] ^ (64 * m)) + 16 * j * kPitch));
+          (lds_s16x4 *)(lds_char *)((at[0] ^ (64 * m)) + 16 * j * kPitch));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4 *)(tile + (place[1] ^ (64 * m)) + 16 * j * kPitch));
+          (lds_s16x4 *)(lds_char *)((at[1] ^ (64 * m)) + 16 * j * kPitch));
       const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       f.v = __builtin_bit_cast(bf16x8, v);
     } else {
-      typedef __attribute__((address_space(3))) const float lds_float;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        f.v[i] = *(lds_float *)(tile + (place[i % 4] ^ (128 * m)) +
-                                (16 * j + 8 * (i / 4)) * kPitch);
+        f.v[i] = lds_read<float>((at[i % 4] ^ (128 * m)) +
+                                 (16 * j + 8 * (i / 4)) * kPitch);
     }
     return f;
+  }
+  // 16 rows of a score block: lane l has row l % 16, pieces 4 b + l / 16.
+  static __device__ __forceinline__ uint32_t score_place(int r0) {
+    const int r = r0 + lane_id() % 16;
+    return r * kPitch + ((lane_id() / 16) ^ turn(r)) * 16;
   }
 };
 
@@ -369,18 +381,17 @@ __device__ __forceinline__ float decay_of(const Lin &p, int h) {
 // computed where it is used, an instruction or two, and not kept in registers
 // throughout, where it would push others out (its scratch loads would then wait
 // behind the loads in flight).
-__device__ __forceinline__ int fresh(int x) {
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
   asm volatile("" : "+v"(x));
   return x;
 }
 
 // Pieces that no load fills hold zeros: features past the head's, and tokens
 // past the end.
-__device__ __forceinline__ void clear(lds_char *lds, int from, int to, int id,
+__device__ __forceinline__ void clear(uint32_t lds, int from, int to, int id,
                                       int threads) {
   for (int x = from + id; x < to; x += threads)
-    *(__attribute__((address_space(3))) u32x4 *)(lds + x * 16) =
-        u32x4{0, 0, 0, 0};
+    lds_write(lds + x * 16, u32x4{0, 0, 0, 0});
 }
 
 // A tile's chunks on their way to LDS, a set of tiles for each that is there or
@@ -396,7 +407,6 @@ struct Loader {
   int64_t step;      // from chunk to chunk, bytes
   uint32_t off[kPer];
   bool ok[kPer];
-  bool whole;        // every piece has a vector
 
   // j0: the tile's first vector of nvec; tokens from `start`, chunk by chunk,
   // forwards or backwards
@@ -404,7 +414,6 @@ struct Loader {
                                        int j0, int nvec, int id) {
     next = in.data + start * in.token * 16;
     step = dir * in.token * (kChunk * 16);
-    whole = Tl::kPieces == Tl::kRowVecs && j0 + Tl::kRowVecs <= nvec;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int x = id + i * TEAM;
@@ -414,40 +423,31 @@ struct Loader {
       ok[i] = x < kAll && c < Tl::kRowVecs && j0 + c < nvec;
     }
   }
-  // n tokens into the tile at `lds`, which nobody reads any more; wave: the
-  // wavefront's first id.
-  __device__ __forceinline__ void load(uint32_t lds, uint32_t wave, int n,
+  // A chunk into the tile at `lds`, which nobody reads any more; wave: the
+  // wavefront's first id.  all(): every token and every piece.
+  __device__ __forceinline__ void all(uint32_t lds, uint32_t wave) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (kAll % TEAM == 0 || (int)wave + i * TEAM < kAll)
+        dma(lds + (wave + i * TEAM) * 16, next, off[i]);
+    next += step;
+  }
+  __device__ __forceinline__ void some(uint32_t lds, uint32_t wave, int n,
                                        int id) {
-    if (n == kChunk && whole) {
+    if (n < kChunk) clear(lds, n * Tl::kPieces, kAll, id, TEAM);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (kAll % TEAM == 0 || (int)wave + i * TEAM < kAll)
-          dma(lds + (wave + i * TEAM) * 16, next, off[i]);
-    } else if (n == kChunk) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (ok[i]) dma(lds + (wave + i * TEAM) * 16, next, off[i]);
-    } else {
-      clear((lds_char *)(uintptr_t)lds, n * Tl::kPieces, kAll, id, TEAM);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (ok[i] && (id + i * TEAM) / Tl::kPieces < n)
-          dma(lds + (wave + i * TEAM) * 16, next, off[i]);
-    }
+    for (int i = 0; i < kPer; ++i)
+      if (ok[i] && (id + i * TEAM) / Tl::kPieces < n)
+        dma(lds + (wave + i * TEAM) * 16, next, off[i]);
     next += step;
   }
 };
 
-// A state's row in the order in which its rows are summed: of 16 rows, 0 to 3,
-// 8 to 11, 4 to 7 and 12 to 15, which gives a lane's eight summed elements,
-// slot(i), eight features side by side.
-template <typename T>
-__device__ __forceinline__ int state_row(int x) {
-  return sizeof(T) == 2 ? (x & ~12) | (x & 4) << 1 | (x & 8) >> 1 : x;
-}
+// A state's rows stand in the order in which they are summed, in bf16: of 16
+// rows, 0 to 3, 8 to 11, 4 to 7 and 12 to 15, which gives a lane's eight summed
+// elements, slot(i), eight features side by side.
 
-// A wavefront's 32 columns of a state, rows by blocks of 32, in the order of
-// state_row.
+// A wavefront's 32 columns of a state, rows by blocks of 32.
 template <typename T, int DP>
 struct State {
   f32x16 s[DP / 32];
@@ -458,29 +458,49 @@ struct State {
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[m][r] = 0.f;
   }
-  // [d, d] in memory; `across`: its transpose.
+  // [d, d] in memory; `across`: its transpose.  Register 4 y + i of
+  // 8 in the lanes of half h is row kY y + kH h + i of 16.
+  static constexpr int kH = sizeof(T) == 2 ? 8 : 4;
+  static constexpr int kY = 12 - kH;
+
   __device__ __forceinline__ void load(const float *src, int d, int c0,
                                        bool across) {
-    const int c = c0 + lane_id() % 32;
+    const int c = c0 + lane_id() % 32, r0 = kH * half_of();
+    const float *lane = src + (across ? (int64_t)min(c, d - 1) * d + r0
+                                      : (int64_t)r0 * d + min(c, d - 1));
 #pragma unroll
     for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = state_row<T>(32 * m + 16 * (r / 8) + slot(r % 8));
-        const bool in = row < d && c < d;
-        const int at = across ? c * d + row : row * d + c;
-        const float x = src[in ? at : 0];
-        s[m][r] = in ? x : 0.f;
+      for (int r = 0; r < 16; r += 4) {
+        const int row = 32 * m + 16 * (r / 8) + kY * (r / 4 % 2);
+        const bool in = row + r0 < d && c < d;  // d is a multiple of four
+        float x[4];
+        if (across) {
+          const float4 v =
+              *reinterpret_cast<const float4 *>(lane + (in ? row : 0));
+          x[0] = v.x;
+          x[1] = v.y;
+          x[2] = v.z;
+          x[3] = v.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = lane[in ? (row + i) * d : 0];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[m][r + i] = in ? x[i] : 0.f;
       }
   }
   __device__ __forceinline__ void store(float *dst, int d, int c0) const {
-    const int c = c0 + lane_id() % 32;
+    const int c = c0 + lane_id() % 32, r0 = kH * half_of();
+    float *lane = dst + (int64_t)r0 * d + c;
 #pragma unroll
     for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = state_row<T>(32 * m + 16 * (r / 8) + slot(r % 8));
-        if (row < d && c < d) dst[row * d + c] = s[m][r];
+      for (int r = 0; r < 16; r += 4) {
+        const int row = 32 * m + 16 * (r / 8) + kY * (r / 4 % 2);
+        if (row + r0 < d && c < d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lane[(row + i) * d] = s[m][r + i];
       }
   }
 };
@@ -529,7 +549,7 @@ __device__ __forceinline__ void decayed(Parts<T, 3> (&x)[2],
 // S = over S + sum over the chunk's tokens of k x^T.
 template <int PARTS, typename T, int DP>
 __device__ __forceinline__ void gather(
-    State<T, DP> &S, const lds_char *K, const int (&place)[Tile<T, DP>::kCols],
+    State<T, DP> &S, const uint32_t (&k_at)[Tile<T, DP>::kCols],
     const Parts<T, 3> (&x)[2], float over) {
 #pragma unroll
   for (int m = 0; m < DP / 32; ++m) {
@@ -537,7 +557,7 @@ __device__ __forceinline__ void gather(
     for (int r = 0; r < 16; ++r) S.s[m][r] *= over;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      mma(S.s[m], Tile<T, DP>::cols(K, place, j, m), x[j], PARTS);
+      mma(S.s[m], Tile<T, DP>::cols(k_at, j, m), x[j], PARTS);
   }
 }
 
@@ -554,7 +574,7 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
   constexpr int kSet = 2 * Tl::kBytes;
   typedef Loader<Tl, 2 * DP> Ld;
   __shared__ __align__(1024) char tiles[kSets * kSet];
-  lds_char *lds = (lds_char *)tiles;
+  const uint32_t lds = lds_address(tiles);
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
@@ -571,12 +591,17 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
     in.data += (st.batch * in.batch + (int64_t)h * in.head) * 16;
     ld[a].init(in, st.start + from(0), REV ? 1 : -1, 0, p.nvec, tid);
   }
+  const bool whole = Tl::kPieces == Tl::kRowVecs && p.nvec == Tl::kRowVecs;
   auto load = [&](int i) {
     const int n = min(kChunk, st.n - from(i));
+    const uint32_t set = lds + i % kSets * kSet;
+    if (whole && n == kChunk) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
-      ld[a].load((uint32_t)(uintptr_t)lds + i % kSets * kSet + a * Tl::kBytes,
-                 wave0, n, tid);
+      for (int a = 0; a < 2; ++a) ld[a].all(set + a * Tl::kBytes, wave0);
+    } else {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) ld[a].some(set + a * Tl::kBytes, wave0, n, tid);
+    }
   };
   if (p.nvec < Tl::kRowVecs) {
     clear(lds, 0, kSets * kSet / 16, tid, 2 * DP);
@@ -584,12 +609,12 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
   }
   for (int i = 0; i < min(chunks, kSets - 1); ++i) load(i);
   const float g = decay_of(p, h);
-  int place[Tl::kCols], place_v[Tl::kCols];
-  Tl::template col_places<true>(place);
-  Tl::col_places(place_v);
+  uint32_t k_place[Tl::kCols], v_place[Tl::kCols];
+  Tl::template col_places<true>(k_place);
+  Tl::template col_places<false>(v_place);
 #pragma unroll
   for (int x = 0; x < Tl::kCols; ++x)
-    place_v[x] ^= wave_id() * (Tl::kHalf ? 64 : 128);
+    v_place[x] ^= wave_id() * (Tl::kHalf ? 64 : 128);
   State<T, DP> S;
   S.clear();
   Powers<REV> pw;
@@ -603,13 +628,18 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
     if (i + kSets - 1 < chunks) load(i + kSets - 1);
     pw.set(g, p.scale, n);
     const float w = exp2f(g * (REV ? from(i) : st.n - from(i) - n));
-    const lds_char *K = lds + i % kSets * kSet, *V = K + Tl::kBytes;
+    uint32_t k_at[Tl::kCols], v_at[Tl::kCols];
+#pragma unroll
+    for (int x = 0; x < Tl::kCols; ++x) {
+      k_at[x] = fresh(k_place[x] + lds + i % kSets * kSet);
+      v_at[x] = v_place[x] + lds + i % kSets * kSet + Tl::kBytes;
+    }
     Frag<T> v[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) v[j] = Tl::cols(V, place_v, j, 0);
+    for (int j = 0; j < 2; ++j) v[j] = Tl::cols(v_at, j, 0);
     Parts<T, 3> x[2];
     decayed<T, REV>(x, v, pw, w);
-    gather<3, T, DP>(S, K, place, x, 1.f);
+    gather<3, T, DP>(S, k_at, x, 1.f);
   }
   S.store(p.states + job * p.d * p.d, p.d, 32 * wave_id());
 }
@@ -651,24 +681,15 @@ __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
     *reinterpret_cast<float4 *>(p.final + row * dd + at) = run;
 }
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// a[s][t] = k_s . q_t for 16 tokens each: rows s0 + ..., t0 + ... of the tiles.
-// Lane l has row l % 16 of either operand, and as long as both take the
-// features in the same order, any will do: piece 4 b + l / 16 of block b.
+// a[s][t] = k_s . q_t for 16 tokens each.  As long as both take the features
+// in the same order, any will do: piece 4 b + l / 16 of block b.
 template <typename T, int DP>
-__device__ __forceinline__ void score(f32x4 &a, const lds_char *K,
-                                      const lds_char *Q, int s0, int t0) {
-  typedef Tile<T, DP> Tl;
-  typedef __attribute__((address_space(3))) const u32x4 lds_u4;
-  const int l = fresh(lane_id());
-  const int s = s0 + l % 16, t = t0 + l % 16;
+__device__ __forceinline__ void score(f32x4 &a, uint32_t k_at, uint32_t q_at) {
 #pragma unroll
-  for (int b = 0; b < Tl::kRowVecs / 4; ++b) {
-    const int c = 4 * b + l / 16;
-    const u32x4 k = *(lds_u4 *)(K + s * Tl::kPitch + (c ^ Tl::turn(s)) * 16);
-    const u32x4 q = *(lds_u4 *)(Q + t * Tl::kPitch + (c ^ Tl::turn(t)) * 16);
-    if constexpr (Tl::kHalf) {
+  for (int b = 0; b < Tile<T, DP>::kRowVecs / 4; ++b) {
+    const u32x4 k = lds_read<u32x4>(k_at ^ (64 * b));
+    const u32x4 q = lds_read<u32x4>(q_at ^ (64 * b));
+    if constexpr (sizeof(T) == 2) {
       a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
           __builtin_bit_cast(bf16x8, k), __builtin_bit_cast(bf16x8, q), a, 0,
           0, 0);
@@ -684,24 +705,25 @@ __device__ __forceinline__ void score(f32x4 &a, const lds_char *K,
 
 // Four scores of token t, s = 4 u + [0, 4), into the tiles of their parts.
 template <typename T>
-__device__ __forceinline__ void put_scores(lds_char *P, float (&x)[8], int t,
-                                           int u) {
+__device__ __forceinline__ uint32_t put_place(int t, int u) {
   typedef Tile<T, 32> Sc;
-  if constexpr (Sc::kHalf) {
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return Sc::kHalf
+             ? t * Sc::kPitch + ((u / 2) ^ Sc::turn(t)) * 16 + u % 2 * 8
+             : t * Sc::kPitch + (u ^ Sc::turn(t)) * 16;
+}
+template <typename T>
+__device__ __forceinline__ void put_scores(uint32_t at, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
     Parts<T, 2> y;
     y.set(x);
-    const int at = t * Sc::kPitch + ((u / 2) ^ Sc::turn(t)) * 16 + u % 2 * 8;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const s16x8 v = __builtin_bit_cast(s16x8, y.f[part].v);
-      *(lds_s16x4 *)(P + part * Sc::kBytes + at) =
-          __builtin_shufflevector(v, v, 0, 1, 2, 3);
+      const s16x4 four = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+      lds_write(at + part * Tile<T, 32>::kBytes, four);
     }
   } else {
-    typedef __attribute__((address_space(3))) f32x4 lds_f4;
-    const f32x4 v = {x[0], x[1], x[2], x[3]};
-    *(lds_f4 *)(P + t * Sc::kPitch + (u ^ Sc::turn(t)) * 16) = v;
+    lds_write(at, f32x4{x[0], x[1], x[2], x[3]});
   }
 }
 
@@ -739,12 +761,12 @@ __global__ __launch_bounds__(2 * DP * ROLES,
   __shared__ __align__(1024) char tiles[kSets * kSet];
   // outputs on their way out (f32: 16 bytes a lane as they stand, for which
   // LDS has no room beside two sets of tiles anyway)
-  __shared__ __align__(16) char outs[Tl::kHalf && !kOwn ? kWaves : 1]
+  __shared__ __align__(1024) char outs[Tl::kHalf && !kOwn ? kWaves : 1]
                                     [kOwn || !Tl::kHalf ? 16 : kChunk * 64];
   // the scores, decayed, in two parts: rows are the tokens t, 32 scores each
   constexpr int kScParts = Parts<T, 2>::kParts;
   __shared__ __align__(1024) char scores[ROLES * kScParts * Sc::kBytes];
-  lds_char *lds = (lds_char *)tiles;
+  const uint32_t lds = lds_address(tiles), P = lds_address(scores);
   const int64_t job = p.first + blockIdx.x;
   const int id = (int)(job / p.H), h = (int)(job - (int64_t)id * p.H);
   const Stretch st = find_stretch(map, id);
@@ -765,31 +787,30 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     else
       own.init(in, st.start + from(0), REV ? -1 : 1, c0 / E, p.nvec, lane_id());
   }
+  const bool whole = Tl::kPieces == Tl::kRowVecs && p.nvec == Tl::kRowVecs;
+  auto tokens = [&](int i) { return min(kChunk, st.n - from(i)); };
+  auto set_at = [&](int i) { return lds + i % kSets * kSet; };
   auto own_at = [&](int i) {
-    return lds + i % kSets * kSet + kShared * Tl::kBytes + wave * Sc::kBytes;
+    return set_at(i) + kShared * Tl::kBytes + wave * Sc::kBytes;
   };
-  auto load_shared = [&](int i) {
-    const int n = min(kChunk, st.n - from(i));
+  auto load_all = [&](int i) {
 #pragma unroll
     for (int a = 0; a < kShared; ++a)
-      ld[a].load((uint32_t)(uintptr_t)lds + i % kSets * kSet + a * Tl::kBytes,
-                 wave * kWave, n, tid);
+      ld[a].all(set_at(i) + a * Tl::kBytes, wave * kWave);
   };
-  auto load_own = [&](int i) {
-    if constexpr (kOwn)
-      own.load((uint32_t)(uintptr_t)own_at(i), 0,
-               min(kChunk, st.n - from(i)), lane_id());
+  auto load_some = [&](int i) {
+#pragma unroll
+    for (int a = 0; a < kShared; ++a)
+      ld[a].some(set_at(i) + a * Tl::kBytes, wave * kWave, tokens(i), tid);
+    if constexpr (kOwn) own.some(own_at(i), 0, tokens(i), lane_id());
   };
   if (p.nvec < Tl::kRowVecs) {
     clear(lds, 0, kSets * kSet / 16, tid, kThreads);
     __syncthreads();
   }
-  for (int i = 0; i < min(chunks, kSets - 1); ++i) {
-    load_shared(i);
-    load_own(i);
-  }
+  for (int i = 0; i < min(chunks, kSets - 1); ++i) load_some(i);
   // the block of scores that does not count is never written
-  clear((lds_char *)scores, 0, sizeof scores / 16, tid, kThreads);
+  clear(P, 0, sizeof scores / 16, tid, kThreads);
   const Part out = p.out[role];
   char *dst = const_cast<char *>(out.data) +
               (st.batch * out.batch + (int64_t)h * out.head) * 16;
@@ -819,8 +840,7 @@ __global__ __launch_bounds__(2 * DP * ROLES,
   for (int turn = 0; turn < kTurns; ++turn)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int lane = lane_id();
-      const int s = 4 * (lane / 16) + r, t = lane % 16;
+      const int s = 4 * (lane_id() / 16) + r, t = lane_id() % 16;
       const int e = (REV ? s - t : t - s) +
                     (min(m0 + turn * kTeam, 2) == 1 ? 16 : 0);
       near[turn][r] = e >= 0 ? p.scale * exp2f(g * e) : 0.f;
@@ -836,27 +856,50 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     to_frag(minus[x], y);
   }
   Powers<REV> pw;
-  const int row0 = Tl::pair_place(), score_row0 = Sc::row_place();
-  int place0[Tl::kCols], place_v0[Tl::kCols];
-  Tl::template col_places<true>(place0);
+  // the lane's places in the tiles
+  const int lane = lane_id();
+  const uint32_t q_tile = (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
+  const uint32_t k_tile = (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
+  const uint32_t v_tile = kOwn ? kShared * Tl::kBytes + wave * Sc::kBytes
+                          : (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
+  const uint32_t q_place = Tl::pair_place() + q_tile;
+  uint32_t k_place[Tl::kCols], v_place[Tl::kCols];
+  Tl::template col_places<true>(k_place);
   if constexpr (kOwn) {
-    Sc::col_places(place_v0);
+    Sc::template col_places<false>(v_place);
   } else {
-    Tl::col_places(place_v0);
+    Tl::template col_places<false>(v_place);
+  }
 #pragma unroll
-    for (int x = 0; x < Tl::kCols; ++x)
-      place_v0[x] ^= m0 * (Tl::kHalf ? 64 : 128);
+  for (int x = 0; x < Tl::kCols; ++x) {
+    k_place[x] += k_tile;
+    if (!kOwn) v_place[x] ^= m0 * (Tl::kHalf ? 64 : 128);
+    v_place[x] += v_tile;
+  }
+  const uint32_t scores_at = P + role * kScParts * Sc::kBytes;
+  const uint32_t score_row = scores_at + Sc::row_place();
+  uint32_t score_k[kTurns], score_q[kTurns], score_put[kTurns];
+#pragma unroll
+  for (int turn = 0; turn < kTurns; ++turn) {
+    const int i3 = min(m0 + turn * kTeam, 2);
+    const int s0 = 16 * block_s(i3), t0 = 16 * block_t(i3);
+    score_k[turn] = Tl::score_place(s0) + k_tile;
+    score_q[turn] = Tl::score_place(t0) + q_tile;
+    // s along the token's row: four of them side by side
+    score_put[turn] =
+        scores_at + put_place<T>(t0 + lane % 16, s0 / 4 + lane / 16);
   }
   // The wavefront's outputs of a chunk are kept (in LDS, or f32 in registers)
   // until the next one's loads are awaited, so that a store has a chunk's time
-  // to complete.  Where 4 bf16 of a token stand: 8 bytes, turned for the
-  // banks' sake.
-  auto out_at = [&](int i, int t, int u) {
-    char *base = kOwn ? tiles + i % kSets * kSet + kShared * Tl::kBytes +
-                            wave * Sc::kBytes
-                      : outs[kOwn ? 0 : wave];
-    return reinterpret_cast<uint2 *>(base + t * 64 + (u ^ (t >> 2 & 3)) * 8);
+  // to complete.  Unit u, 4 bf16 of token t, stands at u ^ (t / 4) % 4 of the
+  // token's eight, for the banks' sake.
+  auto out_at = [&](int i) {
+    return kOwn ? own_at(i) : lds_address(outs[kOwn ? 0 : wave]);
   };
+  const uint32_t put_out =
+      lane % 32 * 64 + (half_of() ^ (lane % 32 >> 2 & 3)) * 8;
+  const uint32_t take_out =
+      lane / 4 * 64 + ((2 * (lane % 4)) ^ (lane / 4 >> 2 & 3)) * 8;
   constexpr int kRow = 32 / E;                    // vectors of 32 features
   constexpr int kKept = Tl::kHalf ? kChunk * kRow / kWave : 4;
   float kept[Tl::kHalf ? 1 : 16];
@@ -865,7 +908,6 @@ __global__ __launch_bounds__(2 * DP * ROLES,
   int out_t[kKept];
 #pragma unroll
   for (int x = 0; x < kKept; ++x) {
-    const int lane = lane_id();
     const int t = Tl::kHalf ? (lane + x * kWave) / kRow : lane % 32;
     const int j = Tl::kHalf ? (lane + x * kWave) % kRow
                             : (16 * (x / 2) + slot(x % 2 * 4)) / 4;
@@ -877,13 +919,14 @@ __global__ __launch_bounds__(2 * DP * ROLES,
 #pragma unroll
     for (int x = 0; x < kKept; ++x) {
       if constexpr (Tl::kHalf) {
-        const int lane = fresh(lane_id()) + x * kWave;
-        const int t = lane / kRow, j = lane % kRow;
-        const uint2 lo = *out_at(i, t, 2 * j), hi = *out_at(i, t, 2 * j + 1);
-        y[x].w[0] = lo.x;
-        y[x].w[1] = lo.y;
-        y[x].w[2] = hi.x;
-        y[x].w[3] = hi.y;
+        const uint32_t at = out_at(i) + take_out;
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 lo = lds_read<u32x2>(at + x * 1024),
+                    hi = lds_read<u32x2>((at ^ 8) + x * 1024);
+        y[x].w[0] = lo[0];
+        y[x].w[1] = lo[1];
+        y[x].w[2] = hi[0];
+        y[x].w[3] = hi[1];
       } else {
         const float f[4] = {kept[4 * x], kept[4 * x + 1], kept[4 * x + 2],
                             kept[4 * x + 3]};
@@ -891,12 +934,17 @@ __global__ __launch_bounds__(2 * DP * ROLES,
       }
     }
   };
-  auto store = [&](int i, const Vec (&y)[kKept]) {
-    const int n = min(kChunk, st.n - from(i));
+  // every token and feature, or some
+  auto store_all = [&](int i, const Vec (&y)[kKept]) {
+    char *base = dst + (st.start + from(i)) * out.token * 16;
+#pragma unroll
+    for (int x = 0; x < kKept; ++x) store_stream(base + out_off[x], y[x]);
+  };
+  auto store_some = [&](int i, const Vec (&y)[kKept]) {
     char *base = dst + (st.start + from(i)) * out.token * 16;
 #pragma unroll
     for (int x = 0; x < kKept; ++x)
-      if (out_ok[x] && (n == kChunk || out_t[x] < n))
+      if (out_ok[x] && out_t[x] < tokens(i))
         store_stream(base + out_off[x], y[x]);
   };
   for (int i = 0; i < chunks; ++i) {
@@ -906,50 +954,47 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     else
       arrive<0>();
     {
+      const int more = i + kSets - 1;
       Vec y[kKept];
-      if (i > 0) take(i - 1, y);
-      if (i + kSets - 1 < chunks) load_shared(i + kSets - 1);
-      if (i > 0) store(i - 1, y);
-      // (into the tile that the outputs have just been taken from)
-      if (i + kSets - 1 < chunks) load_own(i + kSets - 1);
+      // (V goes into the tile that the outputs have just been taken from)
+      if (whole && i > 0 && more < chunks && tokens(i - 1) == kChunk &&
+          tokens(more) == kChunk) {
+        take(i - 1, y);
+        load_all(more);
+        store_all(i - 1, y);
+        if constexpr (kOwn) own.all(own_at(more), 0);
+      } else {
+        if (i > 0) {
+          take(i - 1, y);
+          store_some(i - 1, y);
+        }
+        if (more < chunks) load_some(more);
+      }
     }
     pw.set(g, p.scale, min(kChunk, st.n - from(i)));
-    const int row = fresh(row0), score_row = fresh(score_row0);
-    int place[Tl::kCols], place_v[Tl::kCols];
-#pragma unroll
-    for (int x = 0; x < Tl::kCols; ++x) {
-      place[x] = fresh(place0[x]);
-      place_v[x] = fresh(place_v0[x]);
-    }
-    const lds_char *tile = lds + i % kSets * kSet;
-    const lds_char *Q =
-        tile + (ROLES == 1 ? 0 : role == 0 ? 1 : 2) * Tl::kBytes;
-    const lds_char *K =
-        tile + (ROLES == 1 ? 1 : role == 0 ? 0 : 3) * Tl::kBytes;
-    const lds_char *V =
-        kOwn ? own_at(i)
-             : tile + (ROLES == 1 ? 2 : role == 0 ? 3 : 0) * Tl::kBytes;
-    lds_char *P = (lds_char *)scores + role * kScParts * Sc::kBytes;
+    const uint32_t set = set_at(i);
 #pragma unroll
     for (int turn = 0; turn < kTurns; ++turn) {
-      const int i3 = min(m0 + turn * kTeam, 2);
-      const int s0 = 16 * block_s(i3), t0 = 16 * block_t(i3);
       f32x4 a = {};
-      score<T, DP>(a, K, Q, s0, t0);
-      // s along the lane's row of the tile: four of them side by side
+      score<T, DP>(a, fresh(score_k[turn] + set), fresh(score_q[turn] + set));
       float x[8] = {};
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] = a[r] * near[turn][r];
-      const int lane = fresh(lane_id());
-      put_scores<T>(P, x, t0 + lane % 16, s0 / 4 + lane / 16);
+      put_scores<T>(score_put[turn], x);
+    }
+    uint32_t q_at = fresh(q_place + set), k_at[Tl::kCols], v_at[Tl::kCols];
+#pragma unroll
+    for (int x = 0; x < Tl::kCols; ++x) {
+      k_at[x] = fresh(k_place[x] + set);
+      v_at[x] = fresh(v_place[x] + set);
     }
     // the state's part; what its rounding to bf16 leaves, the matrix cores
     // subtract (exactly): S - 1 * hi
     f32x16 o = {};
 #pragma unroll
     for (int m = 0; m < DP / 32; ++m) {
-      const Frag<T> q[2] = {Tl::pairs(Q, row, 2 * m),
-                            Tl::pairs(Q, row, 2 * m + 1)};
+      const Frag<T> q[2] = {Tl::pairs(q_at, 2 * m),
+                            Tl::pairs(q_at, 2 * m + 1)};
       Frag<T> hi[2];
       f32x16 rest = S.s[m];
 #pragma unroll
@@ -977,9 +1022,9 @@ __global__ __launch_bounds__(2 * DP * ROLES,
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if constexpr (kOwn)
-        v[j] = Sc::cols(V, place_v, j, 0);
+        v[j] = Sc::cols(v_at, j, 0);
       else
-        v[j] = Tl::cols(V, place_v, j, 0);
+        v[j] = Tl::cols(v_at, j, 0);
     }
     Parts<T, 3> vs[2];
     decayed<T, REV>(vs, v, pw, 1.f);
@@ -994,17 +1039,17 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int part = 0; part < kScParts; ++part)
-        mma(o, v[j], Sc::rows(P + part * Sc::kBytes, score_row, j));
-    gather<ONE ? 3 : 2, T, DP>(S, K, place, vs, pw.over);
+        mma(o, v[j], Sc::rows(score_row + part * Sc::kBytes, j));
+    gather<ONE ? 3 : 2, T, DP>(S, k_at, vs, pw.over);
     // o: rows are features, the lane's column its token
     if constexpr (Tl::kHalf) {
-      const int lane = fresh(lane_id());
+      const uint32_t at = fresh(out_at(i) + put_out);
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const float x[8] = {o[r], o[r + 1], o[r + 2], o[r + 3], 0, 0, 0, 0};
         const Vec y = pack<bf16>(x);
-        *out_at(i, lane % 32, (16 * (r / 8) + slot(r % 8)) / 4) =
-            make_uint2(y.w[0], y.w[1]);
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        lds_write(at ^ (4 * r), u32x2{y.w[0], y.w[1]});
       }
     } else {
 #pragma unroll
@@ -1015,7 +1060,7 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     __builtin_amdgcn_wave_barrier();
     Vec y[kKept];
     take(chunks - 1, y);
-    store(chunks - 1, y);
+    store_some(chunks - 1, y);
   }
   if (ONE && p.final != nullptr && role == 0)
     S.store(p.final + ((int64_t)st.seq * p.H + h) * dd, p.d, c0);
