@@ -546,19 +546,26 @@ __device__ __forceinline__ void decayed(Parts<T, 3> (&x)[2],
   }
 }
 
+// The chunk's k by columns, as both uses of a state's update want it.
+template <typename T, int DP>
+struct KeyCols {
+  Frag<T> f[DP / 32][2];
+  __device__ __forceinline__ void read(
+      const uint32_t (&k_at)[Tile<T, DP>::kCols], int m) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f[m][j] = Tile<T, DP>::cols(k_at, j, m);
+  }
+};
+
 // S = over S + sum over the chunk's tokens of k x^T.
 template <int PARTS, typename T, int DP>
-__device__ __forceinline__ void gather(
-    State<T, DP> &S, const uint32_t (&k_at)[Tile<T, DP>::kCols],
-    const Parts<T, 3> (&x)[2], float over) {
+__device__ __forceinline__ void gather(State<T, DP> &S,
+                                       const KeyCols<T, DP> &k, int m,
+                                       const Parts<T, 3> (&x)[2], float over) {
 #pragma unroll
-  for (int m = 0; m < DP / 32; ++m) {
+  for (int r = 0; r < 16; ++r) S.s[m][r] *= over;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) S.s[m][r] *= over;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      mma(S.s[m], Tile<T, DP>::cols(k_at, j, m), x[j], PARTS);
-  }
+  for (int j = 0; j < 2; ++j) mma(S.s[m], k.f[m][j], x[j], PARTS);
 }
 
 // What each stretch adds to the state (from zero): S of its own tokens, at the
@@ -639,7 +646,12 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
     for (int j = 0; j < 2; ++j) v[j] = Tl::cols(v_at, j, 0);
     Parts<T, 3> x[2];
     decayed<T, REV>(x, v, pw, w);
-    gather<3, T, DP>(S, k_at, x, 1.f);
+    KeyCols<T, DP> keys;
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m) {
+      keys.read(k_at, m);
+      gather<3, T, DP>(S, keys, m, x, 1.f);
+    }
   }
   S.store(p.states + job * p.d * p.d, p.d, 32 * wave_id());
 }
@@ -989,35 +1001,42 @@ __global__ __launch_bounds__(2 * DP * ROLES,
       v_at[x] = fresh(v_place[x] + set);
     }
     // the state's part; what its rounding to bf16 leaves, the matrix cores
-    // subtract (exactly): S - 1 * hi
+    // subtract (exactly): S - 1 * hi.  They take some time for it, so the rest
+    // of one block of rows follows behind the next one's rounding.
     f32x16 o = {};
-#pragma unroll
-    for (int m = 0; m < DP / 32; ++m) {
-      const Frag<T> q[2] = {Tl::pairs(q_at, 2 * m),
-                            Tl::pairs(q_at, 2 * m + 1)};
-      Frag<T> hi[2];
-      f32x16 rest = S.s[m];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = S.s[m][8 * x + e];
-        to_frag(hi[x], y);
-        mma(o, hi[x], q[x]);
-        if constexpr (Tl::kHalf) mma(rest, minus[x], hi[x]);
-      }
+    f32x16 rest[2];
+    Frag<T> q[2][2];
+    auto low = [&](int m) {
       if constexpr (Tl::kHalf) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = rest[8 * x + e];
+          for (int e = 0; e < 8; ++e) y[e] = rest[m & 1][8 * x + e];
           Frag<T> lo;
           to_frag(lo, y);
-          mma(o, lo, q[x]);
+          mma(o, lo, q[m & 1][x]);
         }
       }
+    };
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m) {
+      Frag<T> hi[2];
+      rest[m & 1] = S.s[m];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        q[m & 1][x] = Tl::pairs(q_at, 2 * m + x);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = S.s[m][8 * x + e];
+        to_frag(hi[x], y);
+        if constexpr (Tl::kHalf) mma(rest[m & 1], minus[x], hi[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) mma(o, hi[x], q[m & 1][x]);
+      if (m > 0) low(m - 1);
     }
+    low(DP / 32 - 1);
     Frag<T> v[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -1028,6 +1047,13 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     }
     Parts<T, 3> vs[2];
     decayed<T, REV>(vs, v, pw, 1.f);
+    // (bf16: k is read before the wavefronts wait for each other, f32 has no
+    // registers for that)
+    constexpr bool kEarly = Tl::kHalf;
+    KeyCols<T, DP> keys;
+    if constexpr (kEarly)
+#pragma unroll
+      for (int m = 0; m < DP / 32; ++m) keys.read(k_at, m);
     if (kTeam > 1) {
       arrive_lds();
     } else {
@@ -1040,7 +1066,11 @@ __global__ __launch_bounds__(2 * DP * ROLES,
 #pragma unroll
       for (int part = 0; part < kScParts; ++part)
         mma(o, v[j], Sc::rows(score_row + part * Sc::kBytes, j));
-    gather<ONE ? 3 : 2, T, DP>(S, k_at, vs, pw.over);
+#pragma unroll
+    for (int m = 0; m < DP / 32; ++m) {
+      if (!kEarly) keys.read(k_at, m);
+      gather<ONE ? 3 : 2, T, DP>(S, keys, m, vs, pw.over);
+    }
     // o: rows are features, the lane's column its token
     if constexpr (Tl::kHalf) {
       const uint32_t at = fresh(out_at(i) + put_out);
