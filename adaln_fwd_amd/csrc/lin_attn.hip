@@ -657,7 +657,11 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
 }
 
 // Along each sequence: states[j] = the state before stretch j, and the state
-// behind the last.
+// behind the last.  A thread's next reads are under way together, else each
+// would wait for memory in turn: 504 stretches of 128 x 128 take 15 us (4.5
+// TB/s), one read at a time 20.
+constexpr int kScanAtOnce = 8;
+
 template <bool REV>
 __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
                                                       int32_t blocks) {
@@ -674,20 +678,30 @@ __global__ __launch_bounds__(kBlock) void scan_kernel(Lin p, Stretches map,
     run = *reinterpret_cast<const float4 *>(p.init + row * dd + at);
   const int64_t tokens =
       map.nseg == 0 ? map.N : map.row[seq + 1] - map.row[seq];
-  for (int i = 0; i < count; ++i) {
-    const int j = REV ? count - 1 - i : i;
-    float4 *s = reinterpret_cast<float4 *>(
-        p.states + ((int64_t)(first + j) * p.H + h) * dd + at);
-    const float4 before = run;
-    if (i + 1 < count || p.final != nullptr) {
-      const float4 own = *s;
-      const float over = exp2f(g * (float)min(map.len, tokens - j * map.len));
-      run.x = fmaf(run.x, over, own.x);
-      run.y = fmaf(run.y, over, own.y);
-      run.z = fmaf(run.z, over, own.z);
-      run.w = fmaf(run.w, over, own.w);
+  const auto turn = [&](int i) { return REV ? count - 1 - i : i; };
+  const auto place = [&](int i) {
+    return reinterpret_cast<float4 *>(
+        p.states + ((int64_t)(first + turn(i)) * p.H + h) * dd + at);
+  };
+  const int used = p.final != nullptr ? count : count - 1;
+  for (int i0 = 0; i0 < count; i0 += kScanAtOnce) {
+    float4 own[kScanAtOnce];
+#pragma unroll
+    for (int u = 0; u < kScanAtOnce; ++u)
+      if (i0 + u < used) own[u] = *place(i0 + u);
+#pragma unroll
+    for (int u = 0; u < kScanAtOnce; ++u) {
+      const int i = i0 + u;
+      if (i >= count) break;
+      *place(i) = run;
+      if (i >= used) break;
+      const float over =
+          exp2f(g * (float)min(map.len, tokens - turn(i) * map.len));
+      run.x = fmaf(run.x, over, own[u].x);
+      run.y = fmaf(run.y, over, own[u].y);
+      run.z = fmaf(run.z, over, own[u].z);
+      run.w = fmaf(run.w, over, own[u].w);
     }
-    *s = before;
   }
   if (p.final != nullptr)
     *reinterpret_cast<float4 *>(p.final + row * dd + at) = run;
@@ -1097,7 +1111,13 @@ __global__ __launch_bounds__(2 * DP * ROLES,
 }
 
 // One token of each sample: S' = l S + k v^T, o = c S'^T q.  A thread holds
-// four columns of every R-th row.
+// four columns of every R-th row, the next kStepRows of them under way while
+// it works on these.  Bound by the state, read and written once.  It is not
+// read again before the other layers' states have been, so it goes past the
+// caches: 128 samples of 12 heads of 128 take 38 us (5.3 TB/s), 43 without
+// the streaming hint; 512 of 24 292 and 312.  Eight rows under way at once
+// take 268 us there, but 22 us, not 18, for 200 samples of 10 f32 heads of 72,
+// whose threads have six.
 struct Step {
   Part q, k, v, o;
   const float *log_decay, *state;
@@ -1120,6 +1140,8 @@ __device__ __forceinline__ float scalar(const Part &p, int64_t b, int h,
     return reinterpret_cast<const float *>(at)[i];
 }
 
+constexpr int kStepRows = 4;
+
 template <typename T>
 __global__ __launch_bounds__(kBlock) void step_kernel(Step p) {
   __shared__ float sums[kBlock][4];
@@ -1132,6 +1154,16 @@ __global__ __launch_bounds__(kBlock) void step_kernel(Step p) {
     const int h = (int)(bh - b * p.H);
     const int col = ((int)(job - bh * p.groups) * p.cols + c) * 4;
     const bool active = r0 < R && col < p.d;
+    const float *src = p.state + bh * p.d * p.d + col;
+    float *dst = p.state_out + bh * p.d * p.d + col;
+    f32x4 rows[kStepRows], next[kStepRows];
+    const auto read = [&](f32x4 (&x)[kStepRows], int r) {
+#pragma unroll
+      for (int u = 0; u < kStepRows; ++u)
+        if (active && r + u * R < p.d)
+          x[u] = __builtin_nontemporal_load(
+              reinterpret_cast<const f32x4 *>(src + (r + u * R) * p.d));
+    };
     __syncthreads();
     if (t < p.d) qk[0][t] = scalar<T>(p.q, b, h, t);
     if (t >= kMaxHead && t - kMaxHead < p.d)
@@ -1141,24 +1173,25 @@ __global__ __launch_bounds__(kBlock) void step_kernel(Step p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = scalar<T>(p.v, b, h, col + i);
     const float l = expf(p.log_decay[h]);
+    read(rows, r0);
     __syncthreads();
-    if (active) {
-      const float *src = p.state + bh * p.d * p.d + col;
-      float *dst = p.state_out + bh * p.d * p.d + col;
-#pragma unroll 4
-      for (int r = r0; r < p.d; r += R) {
-        const float4 s = *reinterpret_cast<const float4 *>(src + r * p.d);
-        const float k = qk[1][r], q = qk[0][r];
-        float4 n;
-        n.x = fmaf(l, s.x, k * v[0]);
-        n.y = fmaf(l, s.y, k * v[1]);
-        n.z = fmaf(l, s.z, k * v[2]);
-        n.w = fmaf(l, s.w, k * v[3]);
-        sum[0] = fmaf(q, n.x, sum[0]);
-        sum[1] = fmaf(q, n.y, sum[1]);
-        sum[2] = fmaf(q, n.z, sum[2]);
-        sum[3] = fmaf(q, n.w, sum[3]);
-        *reinterpret_cast<float4 *>(dst + r * p.d) = n;
+    for (int r = r0; r < p.d; r += kStepRows * R) {
+      read(next, r + kStepRows * R);
+#pragma unroll
+      for (int u = 0; u < kStepRows; ++u) {
+        const int row = r + u * R;
+        if (active && row < p.d) {
+          const float k = qk[1][row], q = qk[0][row];
+          f32x4 n;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            n[i] = fmaf(l, rows[u][i], k * v[i]);
+            sum[i] = fmaf(q, n[i], sum[i]);
+          }
+          __builtin_nontemporal_store(
+              n, reinterpret_cast<f32x4 *>(dst + row * p.d));
+        }
+        rows[u] = next[u];
       }
     }
 #pragma unroll
@@ -1189,42 +1222,75 @@ int elems_per_vec(int dtype) { return dtype == ADALN_BF16 ? 8 : 4; }
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 
-// Stretches are long enough that the GPU is filled about twice, and not
-// shorter than 128 tokens: what a stretch adds, its state written and read
-// three times, is the traffic of some 200 tokens.
-constexpr int64_t kFill = 3 * kCUs;
-constexpr int64_t kShort = 128;
+// How long the stretches are.  A stretch more is more work at once, but its
+// state is written, read and written, and read: the traffic of some 200
+// tokens, a fourth of the chunk that it starts with, and a share of the scan.
+// Measured, forward and backward in us:
+// - Sequences that all fit one workgroup per CU as they are, none longer
+//   than 4/3 of a CU's share, stay whole, without states: 16 x 1560 tokens of
+//   12 bf16 heads of 128 take 101 and 259 so, 128 and 290 halved.
+// - Else one workgroup per CU, for less than a whole second one would run
+//   alone: 4096 tokens of 16 such heads take 45 and 75 cut in 16, 51 and 95
+//   in 24.  f32's tiles leave room for one (8190 tokens of 12 heads: 153 and
+//   315 in 21, 170 and 344 in 42).
+// - bf16's leave room for two, which pays if stretches stay long: 32760 tokens
+//   of 24 heads take 285 and 631 in 21, 300 and 650 in 10, and 8 x 1560 of 12
+//   70 and 147 in 5, 80 and 161 in 2, but 4 x 1560 46 and 82 in 5, 50 and 93
+//   in 10.
+// - What is done in four chunks is not worth two more launches.
+constexpr int64_t kLong = 256;
+constexpr int64_t kWhole = 4 * kChunk;
+
+int64_t stretches_of(int64_t tokens, int64_t len) {
+  return std::max<int64_t>(1, (tokens + len - 1) / len);
+}
 
 // false: more stretches than can be numbered.
 bool make_stretches(Stretches &m, const int64_t *off, int64_t nseg, int64_t B,
-                    int64_t N, int64_t H, int64_t *count) {
+                    int64_t N, int64_t H, int dtype, int64_t *count) {
   m = Stretches{};
-  const int64_t tokens = off != nullptr ? (nseg > 0 ? off[nseg] : 0) : B * N;
-  int64_t len = std::max(kShort, tokens * H / kFill);
-  len = (len + kChunk - 1) / kChunk * kChunk;
+  const auto sum = [&](int64_t len) {
+    if (off == nullptr) return B * stretches_of(N, len);
+    int64_t n = 0;
+    for (int64_t s = 0; s < nseg; ++s)
+      n += stretches_of(off[s + 1] - off[s], len);
+    return n;
+  };
+  int64_t longest = off == nullptr ? N : 0;
+  if (off != nullptr)
+    for (int64_t s = 0; s < nseg; ++s)
+      longest = std::max(longest, off[s + 1] - off[s]);
+  const int64_t share = (off == nullptr ? B * N : off[nseg]) * H / kCUs;
+  const auto chunks = [](int64_t n) {
+    return std::max<int64_t>(1, (n + kChunk - 1) / kChunk) * kChunk;
+  };
+  int64_t len = chunks(longest);
+  if (longest > kWhole && longest > share * 4 / 3) {
+    const int64_t each = dtype == ADALN_BF16 && share / 2 >= kLong ? 2 : 1;
+    const int64_t even = chunks(share / each), step = chunks(even / 16);
+    // the ends of sequences are stretches too: up to twice as long, if that
+    // leaves no workgroup over
+    len = even;
+    while (len < 2 * even && sum(len) * H > each * kCUs) len += step;
+    if (sum(len) * H > each * kCUs) len = even;
+  }
   m.N = N;
   m.len = len;
-  if (off == nullptr) {
-    m.splits = (int32_t)std::max<int64_t>(1, (N + len - 1) / len);
-    *count = B * m.splits;
-    return *count * H <= kMaxRows;
+  *count = sum(len);
+  m.splits = (int32_t)(off == nullptr ? stretches_of(N, len)
+                                      : 1 + (longest > len));
+  if (off != nullptr) {
+    m.nseg = (int32_t)nseg;
+    int64_t n = 0;
+    for (int64_t s = 0; s < nseg; ++s) {
+      m.first[s] = (int32_t)n;
+      m.row[s] = off[s];
+      n += stretches_of(off[s + 1] - off[s], len);
+    }
+    m.first[nseg] = (int32_t)n;
+    m.row[nseg] = off[nseg];
   }
-  m.nseg = (int32_t)nseg;
-  int64_t n = 0;
-  bool more = false;
-  for (int64_t s = 0; s < nseg; ++s) {
-    m.first[s] = (int32_t)n;
-    m.row[s] = off[s];
-    const int64_t k =
-        std::max<int64_t>(1, (off[s + 1] - off[s] + len - 1) / len);
-    more |= k > 1;
-    n += k;
-  }
-  m.first[nseg] = (int32_t)n;
-  m.row[nseg] = tokens;
-  m.splits = more ? 2 : 1;
-  *count = n;
-  return n * H <= kMaxRows;
+  return *count * H <= kMaxRows;
 }
 
 size_t states_bytes(const Stretches &m, int64_t count, int64_t H, int64_t d) {
@@ -1408,7 +1474,7 @@ ADALN_API size_t adaln_lin_attn_states_bytes(const int64_t *seg_offsets,
     return 0;
   Stretches m;
   int64_t count;
-  if (!make_stretches(m, seg_offsets, nseg, B, N, H, &count)) return 0;
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, dtype, &count)) return 0;
   return states_bytes(m, count, H, d);
 }
 
@@ -1428,7 +1494,7 @@ ADALN_API int adaln_lin_attn_fwd(
   if (B == 0 || H == 0) return ok();
   Stretches m;
   int64_t count;
-  if (!make_stretches(m, seg_offsets, nseg, B, N, H, &count))
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, dtype, &count))
     return fail(kTooMany, "too many sequences and heads");
   const size_t need = states_bytes(m, count, H, d);
   ADALN_TRY(check_workspace(states, states_size, need, "states"));
@@ -1484,7 +1550,7 @@ ADALN_API int adaln_lin_attn_bwd(
   if (B == 0 || H == 0) return ok();
   Stretches m;
   int64_t count;
-  if (!make_stretches(m, seg_offsets, nseg, B, N, H, &count))
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, dtype, &count))
     return fail(kTooMany, "too many sequences and heads");
   const size_t one = states_bytes(m, count, H, d);
   ADALN_TRY(check_workspace(workspace, workspace_bytes,
