@@ -659,7 +659,7 @@ __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) 
 // Along each sequence: states[j] = the state before stretch j, and the state
 // behind the last.  A thread's next reads are under way together, else each
 // would wait for memory in turn: 504 stretches of 128 x 128 take 15 us (4.5
-// TB/s), one read at a time 20.
+// TB/s), with one read at a time 18.
 constexpr int kScanAtOnce = 8;
 
 template <bool REV>
