@@ -1115,8 +1115,8 @@ __global__ __launch_bounds__(2 * DP * ROLES,
 // it works on these.  Bound by the state, read and written once.  It is not
 // read again before the other layers' states have been, so it goes past the
 // caches: 128 samples of 12 heads of 128 take 38 us (5.3 TB/s), 43 without
-// the streaming hint; 512 of 24 292 and 312.  Eight rows under way at once
-// take 268 us there, but 22 us, not 18, for 200 samples of 10 f32 heads of 72,
+// the streaming hint; 512 of 24 296 and 312.  Eight rows under way at once
+// take 268 us there, but 22 us, not 17, for 200 samples of 10 f32 heads of 72,
 // whose threads have six.
 struct Step {
   Part q, k, v, o;
@@ -1164,16 +1164,17 @@ __global__ __launch_bounds__(kBlock) void step_kernel(Step p) {
           x[u] = __builtin_nontemporal_load(
               reinterpret_cast<const f32x4 *>(src + (r + u * R) * p.d));
     };
-    __syncthreads();
-    if (t < p.d) qk[0][t] = scalar<T>(p.q, b, h, t);
-    if (t >= kMaxHead && t - kMaxHead < p.d)
-      qk[1][t - kMaxHead] = scalar<T>(p.k, b, h, t - kMaxHead);
-    float v[4] = {}, sum[4] = {};
+    // (every load is under way before the first is awaited)
+    float mine = 0.f, v[4] = {}, sum[4] = {};
+    const int own = t % kMaxHead;
+    if (own < p.d) mine = scalar<T>(t < kMaxHead ? p.q : p.k, b, h, own);
     if (active)
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = scalar<T>(p.v, b, h, col + i);
-    const float l = expf(p.log_decay[h]);
     read(rows, r0);
+    const float l = expf(p.log_decay[h]);
+    __syncthreads();
+    if (own < p.d) qk[t / kMaxHead][own] = mine;
     __syncthreads();
     for (int r = r0; r < p.d; r += kStepRows * R) {
       read(next, r + kStepRows * R);
