@@ -30,7 +30,8 @@ def _choices(T, k, E, lost=0.0, seed=0):
 
 PLANS = [(1, 1, 1), (1, 2, 16), (5, 3, 7), (64, 1, 2), (1000, 8, 60),
          (4096, 2, 512), (8191, 1, 3), (8193, 1, 3), (5000, 4, 64),
-         (70001, 3, 37), (33, 64, 512), (300000, 4, 129)]
+         (70001, 3, 37), (33, 64, 512), (300000, 4, 129), (6144, 1, 3),
+         (6145, 1, 3)]
 
 
 @pytest.mark.parametrize("size", PLANS, ids=str)
