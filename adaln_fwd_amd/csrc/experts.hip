@@ -402,7 +402,8 @@ hipError_t launch_waves(K k, int64_t waves, hipStream_t s, const Move &p) {
 // Infinity Cache, and the next one finds them there: up to kCachedBytes read
 // and written a call takes plain accesses, past it the streaming hint (those
 // 32760 tokens: gathered 281 us, plainly 319, the join's backward 589 and 614,
-// scattered 326 and 313; 100000 of 1024 features, one choice: 66 and 73 each
+// scattered 326 and 313, but the kernels behind it then take longer, all four
+// together 1472 and 1496; 100000 of 1024 features, one choice: 66 and 73 each
 // way; 777 of 1000 f32 features: within 0.3 us).
 constexpr int64_t kCachedBytes = int64_t(192) << 20;
 
