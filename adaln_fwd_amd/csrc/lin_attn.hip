@@ -463,17 +463,31 @@ struct State {
   static constexpr int kH = sizeof(T) == 2 ? 8 : 4;
   static constexpr int kY = 12 - kH;
 
+  // The lane's first element, column c's in the half's first row.  It stands in
+  // for what is outside the state, so it is inside also where that row is not
+  // (d = kH).
+  static __host__ __device__ __forceinline__ int first_at(int d, int c,
+                                                          int half,
+                                                          bool across) {
+    const int col = c < d ? c : d - 1;
+    const int row = kH * half < d ? kH * half : 0;
+    return across ? col * d + row : row * d + col;
+  }
+  static __host__ __device__ __forceinline__ bool inside(int d, int c,
+                                                         int half, int row) {
+    return row + kH * half < d && c < d;  // d is a multiple of four
+  }
+
   __device__ __forceinline__ void load(const float *src, int d, int c0,
                                        bool across) {
-    const int c = c0 + lane_id() % 32, r0 = kH * half_of();
-    const float *lane = src + (across ? (int64_t)min(c, d - 1) * d + r0
-                                      : (int64_t)r0 * d + min(c, d - 1));
+    const int c = c0 + lane_id() % 32, h = half_of();
+    const float *lane = src + first_at(d, c, h, across);
 #pragma unroll
     for (int m = 0; m < DP / 32; ++m)
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const int row = 32 * m + 16 * (r / 8) + kY * (r / 4 % 2);
-        const bool in = row + r0 < d && c < d;  // d is a multiple of four
+        const bool in = inside(d, c, h, row);
         float x[4];
         if (across) {
           const float4 v =
