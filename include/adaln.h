@@ -495,7 +495,9 @@ int adaln_lin_attn_bwd(const adaln_heads_t *d_o, const adaln_heads_t *q,
 
 /*
  * One token of each of B samples (token strides are not read): state_out = l
- * state + k v^T, o = scale * state_out^T q.  state_out may be state.
+ * state + k v^T, o = scale * state_out^T q.  state_out may be state.  Every
+ * step rounds the state to float32, so of a decay within 2^-24 of 1 a step
+ * takes more or less, or nothing.
  */
 int adaln_lin_attn_step(const adaln_heads_t *q, const adaln_heads_t *k,
                         const adaln_heads_t *v, const float *log_decay,
