@@ -1253,9 +1253,19 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 // state is written, read and written, and read: the traffic of some 200
 // tokens, a fourth of the chunk that it starts with, and a share of the scan.
 // Measured, forward and backward in us:
-// - Sequences that all fit one workgroup per CU as they are, none longer
-//   than 4/3 of a CU's share, stay whole, without states: 16 x 1560 tokens of
-//   12 bf16 heads of 128 take 101 and 259 so, 128 and 290 halved.
+// - Sequences none of which is longer than 3/2 of a CU's share stay whole,
+//   without states, a workgroup each: equal ones from 171 of them (times heads)
+//   on.  Fewer, two workgroups to a CU have room for three stretches of each,
+//   more only for two.  Tokens 1560, bf16, whole and cut (stretches):
+//     168 (504) heads of 128 90 and 241, 108 and 247; of 96 80 and 204, 82 and
+//               188; of 64 69 and 159, 62 and 118
+//     176 (352) heads of 128 87 and 239, 122 and 285; of 96 81 and 204, 100 and
+//               226; of 64 69 and 160, 81 and 151
+//     192 (384) heads of 128 92 and 253, 130 and 312; of 64 69 and 160, 82 and
+//               155
+//   A workgroup of heads of up to 32 is one wavefront, so that whole sequences
+//   leave most of a CU idle.  Theirs are cut up to 4/3 of the share: 176 (352)
+//   take 53 and 102, whole 57 and 125.
 // - Else one workgroup per CU, for less than a whole second one would run
 //   alone: 4096 tokens of 16 such heads take 45 and 75 cut in 16, 51 and 95
 //   in 24.  f32's tiles leave room for one (8190 tokens of 12 heads: 153 and
@@ -1268,13 +1278,22 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kLong = 256;
 constexpr int64_t kWhole = 4 * kChunk;
 
+// Whether sequences stay whole: in exact arithmetic, so that of equal ones
+// their number alone decides, not their length too.
+bool stay_whole(int64_t longest, int64_t tokens, int64_t H, int64_t d) {
+  if (longest <= kWhole) return true;
+  return d <= 32 ? longest * kCUs * 3 <= tokens * H * 4
+                 : longest * kCUs * 2 <= tokens * H * 3;
+}
+
 int64_t stretches_of(int64_t tokens, int64_t len) {
   return std::max<int64_t>(1, (tokens + len - 1) / len);
 }
 
 // false: more stretches than can be numbered.
 bool make_stretches(Stretches &m, const int64_t *off, int64_t nseg, int64_t B,
-                    int64_t N, int64_t H, int dtype, int64_t *count) {
+                    int64_t N, int64_t H, int64_t d, int dtype,
+                    int64_t *count) {
   m = Stretches{};
   const auto sum = [&](int64_t len) {
     if (off == nullptr) return B * stretches_of(N, len);
@@ -1287,12 +1306,13 @@ bool make_stretches(Stretches &m, const int64_t *off, int64_t nseg, int64_t B,
   if (off != nullptr)
     for (int64_t s = 0; s < nseg; ++s)
       longest = std::max(longest, off[s + 1] - off[s]);
-  const int64_t share = (off == nullptr ? B * N : off[nseg]) * H / kCUs;
+  const int64_t tokens = off == nullptr ? B * N : off[nseg];
+  const int64_t share = tokens * H / kCUs;
   const auto chunks = [](int64_t n) {
     return std::max<int64_t>(1, (n + kChunk - 1) / kChunk) * kChunk;
   };
   int64_t len = chunks(longest);
-  if (longest > kWhole && longest > share * 4 / 3) {
+  if (!stay_whole(longest, tokens, H, d)) {
     const int64_t each = dtype == ADALN_BF16 && share / 2 >= kLong ? 2 : 1;
     const int64_t even = chunks(share / each), step = chunks(even / 16);
     // the ends of sequences are stretches too: up to twice as long, if that
@@ -1501,7 +1521,7 @@ ADALN_API size_t adaln_lin_attn_states_bytes(const int64_t *seg_offsets,
     return 0;
   Stretches m;
   int64_t count;
-  if (!make_stretches(m, seg_offsets, nseg, B, N, H, dtype, &count)) return 0;
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, d, dtype, &count)) return 0;
   return states_bytes(m, count, H, d);
 }
 
@@ -1521,7 +1541,7 @@ ADALN_API int adaln_lin_attn_fwd(
   if (B == 0 || H == 0) return ok();
   Stretches m;
   int64_t count;
-  if (!make_stretches(m, seg_offsets, nseg, B, N, H, dtype, &count))
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, d, dtype, &count))
     return fail(kTooMany, "too many sequences and heads");
   const size_t need = states_bytes(m, count, H, d);
   ADALN_TRY(check_workspace(states, states_size, need, "states"));
@@ -1577,7 +1597,7 @@ ADALN_API int adaln_lin_attn_bwd(
   if (B == 0 || H == 0) return ok();
   Stretches m;
   int64_t count;
-  if (!make_stretches(m, seg_offsets, nseg, B, N, H, dtype, &count))
+  if (!make_stretches(m, seg_offsets, nseg, B, N, H, d, dtype, &count))
     return fail(kTooMany, "too many sequences and heads");
   const size_t one = states_bytes(m, count, H, d);
   ADALN_TRY(check_workspace(workspace, workspace_bytes,
