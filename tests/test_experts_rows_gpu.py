@@ -1,5 +1,6 @@
 """The rows to the experts and back, every one compared so that no missing number
-passes, also in place; rows that no choice has hold NaN.
+passes: small calls, whose unowned rows hold NaN, and calls past the caches'
+size, whose kernels access memory with the streaming hint, also in place.
 
 Tolerances: those of test_experts_gpu.py.  Copies are exact.  Sums of k terms:
 (k + 1) * 2^-24 of the terms' absolute values (and one for the weight), then half
@@ -78,3 +79,12 @@ def test_small_calls(size, dt, lost):
     if lost and ((e >= 0) & (e < E)).all():
         lost = 0.0                   # (so few choices that none was dropped)
     _check(T, k, E, D, dt, lost)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,k,row", [(24000, 3, 4112), (60000, 1, 1808)])
+def test_past_the_caches(T, k, row, dt):
+    """Every call moves more than 192 MiB, by rows that end inside a tile."""
+    assert T * (1 + k) * row > 192 << 20
+    print(f"[experts] {T} x {k}, {row} bytes a row", flush=True)
+    _check(T, k, 9, row // (2 if dt == BF16 else 4), dt, 0.2)
