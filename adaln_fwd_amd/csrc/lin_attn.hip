@@ -768,6 +768,40 @@ __device__ __forceinline__ void put_scores(uint32_t at, float (&x)[8]) {
   }
 }
 
+// In the product with the scores every token meets every v, with zeros where it
+// does not count; one that is not finite spoils them all.  clean() puts zeros in
+// the place of such, and gives the chunk's first token (REV: the last) that has
+// one.  v: feature lane % 32 of 32, tokens 16 j + slot(i).
+template <bool REV, typename T>
+__device__ __forceinline__ int clean(Frag<T> (&v)[2]) {
+  int at = REV ? -1 : kChunk;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float y[8];
+    from_frag(y, v[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!isfinite(y[i])) {
+        y[i] = 0.f;
+        const int token = 16 * j + slot(i);
+        at = REV ? max(at, token) : min(at, token);
+      }
+    to_frag(v[j], y);
+  }
+  const int other = __shfl_xor(at, 32);
+  return REV ? max(at, other) : min(at, other);
+}
+// That token's output, and those of tokens that it counts for, become NaN.
+template <bool REV>
+__device__ __forceinline__ void spoil(f32x16 &o, int at) {
+  const int t = lane_id() % 32;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int from = __shfl(at, r / 4 * 8 + 4 * half_of() + r % 4);
+    if (REV ? t <= from : t >= from) o[r] = __builtin_nanf("");
+  }
+}
+
 // What this wavefront has written to LDS is there, then that of every one.
 __device__ __forceinline__ void arrive_lds() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -1025,7 +1059,10 @@ __global__ __launch_bounds__(2 * DP * ROLES,
       score<T, DP>(a, fresh(score_k[turn] + set), fresh(score_q[turn] + set));
       float x[8] = {};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = a[r] * near[turn][r];
+      for (int r = 0; r < 4; ++r)
+        // (selected: a k or q that is not finite does not reach the tokens
+        // that it does not count for)
+        x[r] = near[turn][r] != 0.f ? a[r] * near[turn][r] : 0.f;
       put_scores<T>(score_put[turn], x);
     }
     uint32_t q_at = fresh(q_place + set), k_at[Tl::kCols], v_at[Tl::kCols];
@@ -1093,18 +1130,37 @@ __global__ __launch_bounds__(2 * DP * ROLES,
     } else {
       __builtin_amdgcn_wave_barrier();
     }
+    f32x16 near_o = {};
+    auto scored = [&] {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[r] *= pw.own;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int part = 0; part < kScParts; ++part)
-        mma(o, v[j], Sc::rows(score_row + part * Sc::kBytes, j));
+        for (int part = 0; part < kScParts; ++part)
+          mma(near_o, v[j], Sc::rows(score_row + part * Sc::kBytes, j));
+    };
+    scored();
 #pragma unroll
     for (int m = 0; m < DP / 32; ++m) {
       if (!kEarly) keys.read(k_at, m);
       gather(S, keys, m, vs, pw.over);
     }
+    // (a v that is not finite has left its column of the state so, each row: one
+    // of them tells, and stays so, which costs these sequences some time)
+    if (__builtin_expect(__any(!isfinite(S.s[0][0])), 0)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (kOwn)
+          v[j] = Sc::cols(v_at, j, 0);
+        else
+          v[j] = Tl::cols(v_at, j, 0);
+      }
+      const int at = clean<REV>(v);
+      near_o = f32x16{};
+      scored();
+      spoil<REV>(near_o, at);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[r] = fmaf(o[r], pw.own, near_o[r]);
     // o: rows are features, the lane's column its token
     if constexpr (Tl::kHalf) {
       const uint32_t at = fresh(out_at(i) + put_out);

@@ -4,11 +4,7 @@ for torch tensors.
 q, k and v are [B, N, H, d], or [T, H, d] for packed tokens, in any memory order
 that keeps a head's features contiguous, as the rotations leave them: views of
 one projection's output, or transposed [B, H, N, d].  Checks, streams and
-allocation are those of :mod:`adaln_fwd_amd.ops`.
-
-Inputs are finite, padding behind a sample's last token too: a token that is not
-may spoil the outputs of up to 31 tokens before it (sequences of different
-lengths go packed)."""
+allocation are those of :mod:`adaln_fwd_amd.ops`."""
 
 from __future__ import annotations
 

@@ -448,9 +448,9 @@ int adaln_glu_bwd(const void *dh, const void *x, const void *wg,
  * most 2^20; tokens at most 64 MiB apart.  States and sums are float32; of bf16
  * inputs, what enters a product besides them does so as the sum of two bf16
  * (scores, states) or three (decayed values on their way into a state).
- * A sequence without tokens hands its state on.  Inputs are finite: one that is
- * not spoils its own and all later tokens' outputs, as the formula has it, and
- * may spoil those of up to 31 tokens before it; no other sequence's or head's.
+ * A sequence without tokens hands its state on.  A number that is not finite
+ * spoils its own token's and later tokens' outputs, as the formula has it (q its
+ * own token's alone, v its own feature alone), and nothing else.
  */
 size_t adaln_lin_attn_states_bytes(const int64_t *seg_offsets, int64_t nseg,
                                    int64_t B, int64_t N, int64_t H, int64_t d,
@@ -476,9 +476,8 @@ int adaln_lin_attn_fwd(const adaln_heads_t *q, const adaln_heads_t *k,
  *   dstate      [B,H,d,d] f32 out, or NULL: gradient of state
  *   workspace   adaln_lin_attn_bwd_workspace_bytes bytes; `saved`: whether
  *               `states` is given
- * Results are bitwise reproducible.  An input that is not finite spoils dq as it
- * does o, and dk and dv the other way round: of its own and all earlier tokens,
- * and of up to 31 after it.
+ * Results are bitwise reproducible.  A number that is not finite spoils dq as it
+ * does o, and dk and dv of its own and earlier tokens.
  */
 size_t adaln_lin_attn_bwd_workspace_bytes(int saved,
                                           const int64_t *seg_offsets,

@@ -1,8 +1,7 @@
-"""Linear attention, one token of which is infinite or no number: which outputs
-and gradients that may spoil, and that all the others stay as they are, bit by
-bit.  An output goes by its own and earlier tokens, and so does dq; dk and dv by
-their own and later ones.  Up to 31 tokens on the other side may be spoilt too;
-other samples, heads and packed sequences never are."""
+"""Linear attention, one token of which is infinite or no number: that it spoils
+what the formulas let it reach, and nothing else.  An output goes by its own and
+earlier tokens, and so does dq; dk and dv by their own and later ones.  All others
+stay as they are, bit by bit: tokens, features, heads, samples and sequences."""
 
 import pytest
 import torch
@@ -14,6 +13,10 @@ pytestmark = pytest.mark.gpu
 
 BF16, F32 = torch.bfloat16, torch.float32
 NAMES = ("q", "k", "v", "do")
+# what each result is made of, x_t . sum of y_s z_s^T: x spoils its own token, y
+# every feature from its token on, z its own feature from its token on
+MADE = {"o": ("q", "k", "v"), "dq": ("do", "v", "k"), "dk": ("v", "do", "q"),
+        "dv": ("k", "q", "do")}
 
 
 def _run(ins, decay, tab=None):
@@ -24,32 +27,30 @@ def _run(ins, decay, tab=None):
     return {"o": o, "dq": dq, "dk": dk, "dv": dv}
 
 
-def _same(got, want, keep):
-    for n in want:
-        a, b = got[n][keep[n]], want[n][keep[n]]
-        assert torch.equal(a, b), n
-
-
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("N", [120, 700])   # whole, and cut in stretches
-@pytest.mark.parametrize("d", [64, 72])
+@pytest.mark.parametrize("d", [24, 64, 72, 128])
 @pytest.mark.parametrize("value", [float("nan"), float("-inf")], ids=str)
 def test_samples(dt, N, d, value):
     ins = [t.cuda() for t in _make(2, N, 3, d, dt)[:4]]
     decay = torch.tensor([-0.5, -0.01, 0.0], device="cuda")
     want = _run(ins, decay)
-    for at in (0, 37, N // 2, N - 1):
-        keep = {n: torch.ones(2, N, 3, dtype=torch.bool, device="cuda")
-                for n in want}
-        for n in want:
-            gone = slice(max(0, at - 31), N) if n in ("o", "dq") else \
-                slice(0, at + 32)
-            keep[n][1, gone, 1] = False
+    for at in (0, 37, 63, 64, N // 2, N - 1):
         for i, name in enumerate(NAMES):
-            bad = [t.clone() for t in ins]
-            bad[i][1, at, 1, 5] = value
-            print(f"[nonfinite] {name} of token {at}", flush=True)
-            _same(_run(bad, decay), want, keep)
+            for f in (5, d - 2):
+                bad = [t.clone() for t in ins]
+                bad[i][1, at, 1, f] = value
+                print(f"[nonfinite] {name} of token {at}, {f}", flush=True)
+                for n, got in _run(bad, decay).items():
+                    hit = torch.zeros_like(got, dtype=torch.bool)
+                    reach = slice(at, N) if n in ("o", "dq") else \
+                        slice(0, at + 1)
+                    if name in MADE[n]:
+                        role = MADE[n].index(name)
+                        hit[1, at if role == 0 else reach, 1,
+                            f if role == 2 else slice(None)] = True
+                    assert not got[hit].isfinite().any(), n
+                    assert torch.equal(got[~hit], want[n][~hit]), n
 
 
 @pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
@@ -64,4 +65,22 @@ def test_packed_sequences(dt):
         for i in range(4):
             bad = [t.clone() for t in ins]
             bad[i][a:b] = float("nan")
-            _same(_run(bad, decay, off), want, {n: keep for n in want})
+            for n, got in _run(bad, decay, off).items():
+                assert torch.equal(got[keep], want[n][keep]), n
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_padding_behind_a_sample(dt):
+    """Samples of different lengths in one tensor, NaN behind their ends."""
+    B, N, d = 3, 100, 64
+    ins = [t.cuda() for t in _make(B, N, 2, d, dt)[:4]]
+    decay = torch.tensor([-0.2, -0.01], device="cuda")
+    want = _run(ins, decay)
+    for b, n in enumerate((1, 45, 97)):
+        for t in ins[:3]:
+            t[b, n:] = float("nan")
+    got = _run(ins, decay)
+    for b, n in enumerate((1, 45, 97)):
+        for name in ("o", "dq"):
+            assert torch.equal(got[name][b, :n], want[name][b, :n])
+            assert not got[name][b, n:].isfinite().any()
