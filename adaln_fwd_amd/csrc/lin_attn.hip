@@ -176,9 +176,11 @@ __device__ __forceinline__ void dma(uint32_t lds, const void *base,
       : "memory", "m0");
 }
 
-// Everything that this wavefront has under way but its last LATER loads (loads
-// return in order; with stores among them LATER has to be 0) has landed, then
-// that of every wavefront.
+// All of this wavefront's accesses to memory but the last LATER have landed, then
+// those of every wavefront.  LATER is the least number of loads that any wavefront
+// has begun behind those awaited, and counts no stores: loads return in order, so
+// with at most LATER accesses of any kind left, none of the awaited ones is among
+// them.  (Stores begun meanwhile only make it wait for more.)
 template <int LATER>
 __device__ __forceinline__ void arrive() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER)
@@ -186,12 +188,15 @@ __device__ __forceinline__ void arrive() {
 }
 
 // The 32 tokens of a chunk of one tensor, a row of kPieces pieces of 16 bytes
-// each.  Piece c of token r stands at c ^ turn(r), so that the rows which a
-// read takes together lie in distinct banks: 16 rows of 8 bytes, four rows of
-// 32 (a transposing read), or of f32 8 rows of 16 bytes, two of 128.  The loads
-// apply the turn to the addresses that they read from.  A turn's bits are the
-// pieces' own, so a lane's place for block b or columns 32 m is that for the
-// first by an exclusive or.
+// each.  Piece c of token r stands at c ^ turn(r), which spreads the rows that a
+// read takes together over the banks: 16 rows of 8 bytes, four rows of 32 (a
+// transposing read), or of f32 8 rows of 16 bytes, two of 128.  (Not all the way:
+// 8-byte accesses take 32 rows, and in tiles of four pieces, those of scores, of
+// a wavefront's own columns and of outputs, rows 16 apart share their banks.  36%
+// of the LDS's active cycles are conflicts in out_kernel, none in state_kernel,
+// which has no such tile.)  The loads apply the turn to the addresses that they
+// read from.  A turn's bits are the pieces' own, so a lane's place for block b or
+// columns 32 m is that for the first by an exclusive or.
 template <typename T, int DP>
 struct Tile {
   static constexpr bool kHalf = sizeof(T) == 2;
@@ -586,7 +591,7 @@ __device__ __forceinline__ void gather(State<T, DP> &S,
 // place of the state that the next one starts from.  It walks the stretch the
 // other way round than the pass behind it does, so that this one finds what
 // was read last in the caches.  Bound by HBM: 32760 tokens of 24 bf16 heads of
-// 128 take 82-98 us (4.4-5.3 TB/s), the matrix cores busy for 44% of it.
+// 128 take 81-98 us (4.4-5.4 TB/s), the matrix cores busy for half of it.
 template <typename T, int DP, bool REV>
 __global__ __launch_bounds__(2 * DP, 2) void state_kernel(Lin p, Stretches map) {
   typedef Tile<T, DP> Tl;
@@ -814,10 +819,13 @@ __device__ __forceinline__ void arrive_lds() {
 // the state behind it.  `across` (bit by role): the states in memory are the
 // transpose of this role's.
 // Bound by HBM and the matrix cores together, on a card at its power limit:
-// 32760 tokens of 24 bf16 heads of 128 take 181-207 us (4.2-4.8 TB/s, matrix
-// cores 47%); 16 x 1560 of 12, a sequence to a workgroup, 101-115 us, their dv
-// and dk 169-192 (matrix cores 51%, on three of four CUs).  f32, 2 x 1777 of
-// 10 heads of 72: 36 and 55 us, five chunks in a row on each CU.
+// 32760 tokens of 24 bf16 heads of 128 take 193-225 us (3.9-4.5 TB/s, matrix
+// cores 49%); 16 x 1560 of 12, a sequence to a workgroup, 106-124 us, their dv
+// and dk 171-199 (matrix cores 50%, on three of four CUs).  f32, 2 x 1777 of
+// 10 heads of 72: 36 and 56 us, five chunks in a row on each CU.  (A wavefront
+// stores 64 bytes of a token, half a line, with the streaming hint: up to a fifth
+// more than the outputs' bytes is written, 240 MB for 201 in the first case.
+// Plain stores write 201, but take 3% longer.)
 template <typename T, int DP, bool REV, int ROLES, bool ONE>
 __global__ __launch_bounds__(2 * DP * ROLES,
                              ROLES == 1 ? 2 : 1) void out_kernel(
@@ -1323,13 +1331,17 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 //   leave most of a CU idle.  Theirs are cut up to 4/3 of the share: 176 (352)
 //   take 53 and 102, whole 57 and 125.
 // - Else one workgroup per CU, for less than a whole second one would run
-//   alone: 4096 tokens of 16 such heads take 45 and 75 cut in 16, 51 and 95
-//   in 24.  f32's tiles leave room for one (8190 tokens of 12 heads: 153 and
-//   315 in 21, 170 and 344 in 42).
+//   alone: 4096 tokens of 16 such heads take 45 and 79 cut in 16, 51 and 102
+//   in 22.  f32's tiles leave room for one (8190 tokens of 12 heads: 147 and
+//   316 in 20, 169 and 346 in 37).
 // - bf16's leave room for two, which pays if stretches stay long: 32760 tokens
-//   of 24 heads take 285 and 631 in 21, 300 and 650 in 10, and 8 x 1560 of 12
-//   70 and 147 in 5, 80 and 161 in 2, but 4 x 1560 46 and 82 in 5, 50 and 93
+//   of 24 heads take 295 and 684 in 21, 327 and 718 in 10, and 8 x 1560 of 12
+//   74 and 158 in 5, 85 and 171 in 2, but 4 x 1560 47 and 85 in 5, 52 and 98
 //   in 10.
+//   (Those are heads of 128.  Narrower ones leave room for more, f32's of up to 64
+//   for two, which these rules do not use: 8190 f32 tokens of 12 heads of 64 take
+//   84 and 150 in 20, 68 and 144 in 37; 4 x 1560 bf16 of 12 of 64 35 and 58 in 5,
+//   33 and 53 in 10; 32760 of 24 of 64 161 and 315 in 21, 157 and 316 in 41.)
 // - What is done in four chunks is not worth two more launches.
 constexpr int64_t kLong = 256;
 constexpr int64_t kWhole = 4 * kChunk;

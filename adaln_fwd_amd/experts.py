@@ -6,7 +6,10 @@ of :mod:`adaln_fwd_amd.ops`.
     xs = experts_sort_fwd(x, slot)                 # rows by expert
     ...                                            # ys: each expert's rows
     y = experts_join_fwd(ys, slot, w)              # weighted, back at the tokens
-"""
+
+Plan, sort and join go by what stands on the GPU, and a captured graph of them by
+each replay's choices.  The experts' own products need their rows' limits on the
+host (``offsets.tolist()``, which waits for the GPU); captured, they keep those."""
 
 from __future__ import annotations
 
