@@ -1321,15 +1321,15 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 //   without states, a workgroup each: equal ones from 171 of them (times heads)
 //   on.  Fewer, two workgroups to a CU have room for three stretches of each,
 //   more only for two.  Tokens 1560, bf16, whole and cut (stretches):
-//     168 (504) heads of 128 90 and 241, 108 and 247; of 96 80 and 204, 82 and
-//               188; of 64 69 and 159, 62 and 118
-//     176 (352) heads of 128 87 and 239, 122 and 285; of 96 81 and 204, 100 and
-//               226; of 64 69 and 160, 81 and 151
-//     192 (384) heads of 128 92 and 253, 130 and 312; of 64 69 and 160, 82 and
-//               155
+//     160 (480) heads of 128 94 and 244, 104 and 240; of 96 86 and 215, 82 and
+//               182; of 64 74 and 168, 64 and 118
+//     176 (352) heads of 128 95 and 246, 123 and 290; of 96 87 and 216, 102 and
+//               236; of 64 74 and 169, 84 and 154
+//     192 (384) heads of 128 98 and 263, 132 and 311; of 96 87 and 215, 104 and
+//               239; of 64 74 and 167, 85 and 158
 //   A workgroup of heads of up to 32 is one wavefront, so that whole sequences
 //   leave most of a CU idle.  Theirs are cut up to 4/3 of the share: 176 (352)
-//   take 53 and 102, whole 57 and 125.
+//   take 55 and 105, whole 58 and 132.  (So would 256 gain, 55 and 107.)
 // - Else one workgroup per CU, for less than a whole second one would run
 //   alone: 4096 tokens of 16 such heads take 45 and 79 cut in 16, 51 and 102
 //   in 22.  f32's tiles leave room for one (8190 tokens of 12 heads: 147 and
